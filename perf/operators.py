@@ -368,7 +368,7 @@ def _own(st):
     if op == "conv_bwd":
         g = ssm.causal_conv1d_bwd(st["x"], st["w"], st["dout"], bias=st["bias"], silu=True)
         return [g["dx"], g["dw"], g["dbias"]]
-    return [ssm.state_slots_copy(st["pool"], st["src"], st["dst"])]
+    return [ssm.state_slots_copy(st["pool"], st["src"], st["dst"], slot_dim=1)]
 
 
 def run(state):
