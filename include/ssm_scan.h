@@ -403,6 +403,142 @@ int ssm_selective_scan_bwd_device_status(void* workspace, ssm_stream_t stream);
  * SSM_ERR_INVALID_ARG for a budget outside [0, 10 s]. */
 int ssm_selective_scan_bwd_test_hooks(int stall, int64_t wait_budget_us);
 
+/* ------------------------------------------------------- packed prompts and state slots
+ *
+ * Serving keeps every sequence's recurrent state in a slot of a pool: the last width - 1 inputs
+ * of the causal convolution and the fp32 state of the scan ("architecture-details" page,
+ * "Memory Efficiency": a constant-size state, no cache of past inputs).  Prompts run packed end
+ * to end and leave their states in slots, single tokens step the slots, and
+ * ssm_state_slots_copy forks, moves and clears them.  Shared arguments:
+ *
+ *   cu_seqlens  (n_seq + 1) int32, device: sequence i is the tokens [cu_seqlens[i],
+ *               cu_seqlens[i+1]) of the packed buffer.  A length may be zero.  Tokens ahead of
+ *               the first and behind the last sequence are neither read nor written.  Bounds
+ *               that lie outside the buffer or run backwards are clamped to it.
+ *   slots       (n_seq or batch) int32, device, nullable: the slot of each sequence or row;
+ *               NULL means slot i for i.  A negative slot marks padding: nothing is written for
+ *               it, its outputs stay as they were.  A slot >= n_slots touches no state and its
+ *               outputs are NaN.  The slots >= 0 of a call must be distinct: with one named
+ *               twice, which of its rows' states stays is unspecified.
+ *   has_state   (n_seq) uint8, device, nullable: nonzero starts the sequence from its slot's
+ *               state, zero (or NULL) from zeros.
+ *   n_slots, slot_stride
+ *               the pool's slots and the elements from one slot to the next (at least a slot's
+ *               own), so a pool may hold several layers' states side by side.
+ *
+ * All four calls launch on `stream` without a plan, allocate nothing, and may be captured into
+ * a graph; their slots, lengths and flags are read when the kernels run.
+ */
+
+/*
+ * ssm_causal_conv1d_fwd over packed prompts: x and out are (dim, total), w (dim, width) fp32,
+ * bias (dim) fp32 or NULL.  The taps before a sequence's first token come from its slot's
+ * history, and the sequence's last width - 1 inputs replace that history (inputs of a sequence
+ * shorter than that join what the slot held).  states: the pool, slot s at s * slot_stride, a
+ * slot being (dim, width - 1) in io_dtype, the oldest input first; not used for width 1.
+ * width is 1 to 4, else SSM_ERR_UNSUPPORTED.  out must not alias x.  One kernel.
+ * SSM_ERR_INVALID_ARG for a bad size, stride or dtype, a pointer off its element's alignment,
+ * or a NULL w, cu_seqlens, states (width > 1), x or out (total > 0).
+ */
+int ssm_causal_conv1d_packed_fwd(int64_t dim, int64_t total, int64_t n_seq, int32_t width, int32_t io_dtype,
+                                 const void* x, const float* w, const float* bias, int silu,
+                                 const int32_t* cu_seqlens, const int32_t* slots, const uint8_t* has_state,
+                                 void* states, int64_t n_slots, int64_t slot_stride, void* out,
+                                 ssm_stream_t stream);
+
+/*
+ * The same convolution for one new token of each row: x and out are (batch, dim); each row's
+ * history is read from its slot and moved on by the token.  One kernel.  Errors as above.
+ */
+int ssm_causal_conv1d_update(int64_t batch, int64_t dim, int32_t width, int32_t io_dtype, const void* x,
+                             const float* w, const float* bias, int silu, const int32_t* slots, void* states,
+                             int64_t n_slots, int64_t slot_stride, void* out, ssm_stream_t stream);
+
+/*
+ * The forward scan over packed prompts: dims->batch is the number of sequences and dims->seqlen
+ * the tokens of the packed buffer, so u, z, out are (dim, seqlen), delta is (nheads, seqlen), B
+ * and C are (ngroups, dstate, seqlen) in the io dtype; A, D, delta_bias and softplus as for
+ * ssm_selective_scan_fwd.  states: the pool, slot s at s * slot_stride, a slot being
+ * (dim, dstate) fp32; each sequence starts from its slot's state or zero, and its final state
+ * goes to its slot.  dstate is 8, 16, 32, 64 or 128, else SSM_ERR_UNSUPPORTED.
+ *
+ * max_seqlen: the longest sequence if the caller knows it, else 0.  It is a hint: with few long
+ * sequences the call cuts them into chunks that run at the same time and join their states
+ * (two kernels instead of one), and the hint saves that where every sequence is short.  The
+ * result is right for any value; the same arguments give the same bits.  `workspace` (device,
+ * 16-byte aligned, caller-owned) has at least ssm_selective_scan_packed_workspace_size bytes
+ * for the same dims and max_seqlen (0 bytes: it may be NULL); it is scratch after the call, and
+ * one workspace must not serve two calls at once, nor two graphs that may run at once.
+ *
+ * out must not alias an input.  SSM_ERR_INVALID_ARG for a bad shape or stride, a pointer off its
+ * element's alignment, a workspace that is too small, or a NULL A, cu_seqlens, states, or u,
+ * delta, B, C, out (seqlen > 0).
+ */
+int ssm_selective_scan_packed_workspace_size(const ssm_dims_t* dims, int64_t max_seqlen, size_t* bytes);
+
+int ssm_selective_scan_packed_fwd(const ssm_dims_t* dims, const void* u, const void* delta, const float* A,
+                                  const void* B, const void* C, const float* D, const void* z,
+                                  const float* delta_bias, int softplus, const int32_t* cu_seqlens,
+                                  const int32_t* slots, const uint8_t* has_state, float* states,
+                                  int64_t n_slots, int64_t slot_stride, int64_t max_seqlen, void* out,
+                                  void* workspace, size_t workspace_bytes, ssm_stream_t stream);
+
+/*
+ * ssm_selective_state_update with the states in slots of a pool: row b's state is slot slots[b],
+ * updated in place.  dims->seqlen must be 1; the inputs' layouts are
+ * ssm_selective_state_update's.  states must be 16-byte aligned and slot_stride a multiple of 4,
+ * B and C 8-byte (bf16) or 16-byte (fp32) aligned, and A 16-byte aligned in the per-channel
+ * layout; otherwise SSM_ERR_UNSUPPORTED.  One kernel.  SSM_ERR_INVALID_ARG for a NULL required
+ * pointer (states, u, delta, A, B, C, out), seqlen != 1, or a bad shape or stride.
+ */
+int ssm_selective_state_update_slots(const ssm_dims_t* dims, float* states, const int32_t* slots,
+                                     int64_t n_slots, int64_t slot_stride, const void* u, const void* delta,
+                                     const float* A, const void* B, const void* C, const float* D,
+                                     const void* z, const float* delta_bias, int softplus, void* out,
+                                     ssm_stream_t stream);
+
+/*
+ * Copies, moves and clears slots, of any element type, in every layer of a pool: layer l's slot s
+ * is the slot_bytes bytes at pool + l * layer_stride + s * slot_stride (strides in bytes; the
+ * slots of one layer behind the other's, or the layers of one slot side by side).  For all pairs
+ * i < n_pairs at once,
+ *
+ *     slot dst[i] = src[i] >= 0 ? what slot src[i] held before the call : zeros
+ *
+ * so a fork names one source with several destinations, a compaction names any moves (chains and
+ * swaps included), and freeing a slot names source -1.  src and dst are (n_pairs) int32 on the
+ * device.  A pair with src >= n_slots, dst < 0 or dst >= n_slots is skipped.  Destinations must
+ * be distinct: with one named twice, which pair's bytes stay is unspecified, byte by byte.
+ * One kernel, which allocates nothing.  SSM_ERR_UNSUPPORTED for n_pairs > 4096;
+ * SSM_ERR_INVALID_ARG for a NULL pool, src or dst, a negative size or overlapping slots.
+ */
+int ssm_state_slots_copy(void* pool, int64_t n_layers, int64_t n_slots, int64_t slot_bytes, int64_t slot_stride,
+                         int64_t layer_stride, const int32_t* src, const int32_t* dst, int64_t n_pairs,
+                         ssm_stream_t stream);
+
+/*
+ * Gradients of ssm_causal_conv1d_fwd, for training: given dout = dLoss/dout, with v the sum that
+ * the forward takes silu of (recomputed from x) and dv = dout * silu'(v) (dout without silu),
+ *
+ *     dx[b,d,t] = sum_{k < width} w[d,k] * dv[b,d,t + width - 1 - k]     (dv = 0 past the end)
+ *     dw[d,k]   = sum_{b,t} dv[b,d,t] * x[b,d,t - width + 1 + k],   dbias[d] = sum_{b,t} dv[b,d,t]
+ *
+ * dx is (batch, dim, seqlen) in io_dtype; dw (dim, width) and dbias (dim, nullable: not computed)
+ * are fp32, summed in a fixed order.  bias is the forward's (NULL: zero).  `workspace` (device,
+ * 4-byte aligned, caller-owned) has at least ssm_causal_conv1d_bwd_workspace_size bytes; one
+ * workspace must not serve two calls at once.  Two kernels on `stream`; the call allocates
+ * nothing.  dx must not alias x or dout.  width is 1 to 4, else SSM_ERR_UNSUPPORTED;
+ * SSM_ERR_INVALID_ARG for a bad shape or dtype, a pointer off its element's alignment, a
+ * workspace that is too small, or a NULL w, dw, x, dout or dx.
+ */
+int ssm_causal_conv1d_bwd_workspace_size(int64_t batch, int64_t dim, int64_t seqlen, int32_t width,
+                                         int32_t io_dtype, size_t* bytes);
+
+int ssm_causal_conv1d_bwd(int64_t batch, int64_t dim, int64_t seqlen, int32_t width, int32_t io_dtype,
+                          const void* x, const float* w, const float* bias, int silu, const void* dout,
+                          void* dx, float* dw, float* dbias, void* workspace, size_t workspace_bytes,
+                          ssm_stream_t stream);
+
 /* Release the plan and its workspace.  NULL is accepted.  Synchronises the device. */
 int ssm_scan_destroy(ssm_plan_t plan);
 

@@ -6,6 +6,15 @@ and adds a small torch-tensor front end:
 
     out, last_state = selective_scan_fwd(u, delta, A, B, C, D, z, delta_bias, softplus=True)
     out, last_state = selective_scan_fn(...)   # the same, differentiable (torch autograd)
+    out = causal_conv1d_fn(x, w, bias)         # the convolution in front of it, differentiable
+
+and, for serving, the forms that keep each sequence's state in a slot of a pool:
+
+    u = causal_conv1d_packed(x, w, cu_seqlens, conv_states, slots)            # prompts, packed end to end
+    out = selective_scan_packed(u, delta, A, B, C, cu_seqlens, states, slots)
+    u = causal_conv1d_update(x, w, conv_states, slots)                        # one token per row
+    out = selective_state_update_slots(states, u, delta, A, B, C, slots)
+    state_slots_copy(states, src, dst)                                        # fork, move, free
 
 PyTorch is only used for device memory and streams; the scan runs in the
 library's kernels.  There is no CPU or PyTorch fallback.
@@ -31,7 +40,13 @@ from ._abi import (SSM_BF16, SSM_ERR_BOUNDS, SSM_ERR_CUDA, SSM_ERR_INVALID_ARG, 
                    ssm_selective_scan_bwd_workspace_size, ssm_selective_scan_bwd_device_status,
                    ssm_selective_scan_bwd_test_hooks, ssm_grads_t,
                    GRAD_NAMES,
-                   ssm_status_string)
+                   ssm_status_string,
+                   ssm_causal_conv1d_packed_fwd, ssm_causal_conv1d_update, ssm_selective_scan_packed_workspace_size,
+                   ssm_selective_scan_packed_fwd, ssm_selective_state_update_slots, ssm_state_slots_copy,
+                   ssm_causal_conv1d_bwd_workspace_size, ssm_causal_conv1d_bwd)
+from .slots import (causal_conv1d_packed, causal_conv1d_update, selective_scan_packed,  # noqa: F401
+                    selective_state_update_slots, state_slots_copy)
+from .conv1d import causal_conv1d_bwd, causal_conv1d_fn, causal_conv1d_fwd  # noqa: F401
 
 __all__ = ["selective_scan_fwd", "selective_scan_fwd_host", "selective_scan_fn", "Plan", "get_plan", "ssm_scan_plan",
            "ssm_selective_scan_fwd", "ssm_selective_scan_fwd_h0", "ssm_selective_scan_fwd_ckpt",
@@ -43,7 +58,13 @@ __all__ = ["selective_scan_fwd", "selective_scan_fwd_host", "selective_scan_fn",
            "ssm_selective_scan_bwd_device_status", "ssm_selective_scan_bwd_test_hooks",
            "ssm_scan_destroy", "ssm_scan_device_status", "ssm_status_string", "ssm_scan_plan_info",
            "ssm_scan_set_option", "ssm_scan_plan_schedule",
-           "ssm_probe_ex2", "make_dims", "SsmError", "load_library"]
+           "ssm_probe_ex2", "make_dims", "SsmError", "load_library",
+           "causal_conv1d_fwd", "causal_conv1d_bwd", "causal_conv1d_fn", "ssm_causal_conv1d_bwd",
+           "ssm_causal_conv1d_bwd_workspace_size",
+           "causal_conv1d_packed", "causal_conv1d_update", "selective_scan_packed", "selective_state_update_slots",
+           "state_slots_copy", "ssm_causal_conv1d_packed_fwd", "ssm_causal_conv1d_update",
+           "ssm_selective_scan_packed_workspace_size", "ssm_selective_scan_packed_fwd",
+           "ssm_selective_state_update_slots", "ssm_state_slots_copy"]
 
 
 class Plan:

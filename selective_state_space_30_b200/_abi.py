@@ -33,7 +33,10 @@ EXPORTS = ("ssm_scan_plan", "ssm_selective_scan_fwd", "ssm_selective_scan_fwd_h0
            "ssm_selective_scan_bwd_ckpt", "ssm_selective_scan_bwd_device_status", "ssm_selective_scan_bwd_test_hooks",
            "ssm_scan_set_option",
            "ssm_scan_plan_schedule", "ssm_scan_destroy",
-           "ssm_scan_device_status", "ssm_status_string", "ssm_scan_plan_info", "ssm_probe_ex2")
+           "ssm_scan_device_status", "ssm_status_string", "ssm_scan_plan_info", "ssm_probe_ex2",
+           "ssm_causal_conv1d_packed_fwd", "ssm_causal_conv1d_update", "ssm_selective_scan_packed_workspace_size",
+           "ssm_selective_scan_packed_fwd", "ssm_selective_state_update_slots", "ssm_state_slots_copy",
+           "ssm_causal_conv1d_bwd_workspace_size", "ssm_causal_conv1d_bwd")
 
 SSM_OPT_SPIN_LIMIT = 1
 SSM_OPT_INJECT_STALL = 2
@@ -92,6 +95,15 @@ def load_library(path: Optional[str] = None):
     lib.ssm_selective_scan_noalloc_test_hooks.argtypes = [i32, i64]
     lib.ssm_selective_state_update.argtypes = [dims_p, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp]
     lib.ssm_causal_conv1d_fwd.argtypes = [i64, i64, i64, i32, i32, vp, vp, vp, i32, vp, vp]
+    sz = ctypes.c_size_t
+    lib.ssm_causal_conv1d_packed_fwd.argtypes = [i64, i64, i64, i32, i32, vp, vp, vp, i32, vp, vp, vp, vp, i64, i64, vp, vp]
+    lib.ssm_causal_conv1d_update.argtypes = [i64, i64, i32, i32, vp, vp, vp, i32, vp, vp, i64, i64, vp, vp]
+    lib.ssm_selective_scan_packed_workspace_size.argtypes = [dims_p, i64, ctypes.POINTER(sz)]
+    lib.ssm_selective_scan_packed_fwd.argtypes = [dims_p] + [vp] * 8 + [i32, vp, vp, vp, vp, i64, i64, i64, vp, vp, sz, vp]
+    lib.ssm_selective_state_update_slots.argtypes = [dims_p, vp, vp, i64, i64] + [vp] * 8 + [i32, vp, vp]
+    lib.ssm_state_slots_copy.argtypes = [vp, i64, i64, i64, i64, i64, vp, vp, i64, vp]
+    lib.ssm_causal_conv1d_bwd_workspace_size.argtypes = [i64, i64, i64, i32, i32, ctypes.POINTER(sz)]
+    lib.ssm_causal_conv1d_bwd.argtypes = [i64, i64, i64, i32, i32, vp, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp]
     lib.ssm_selective_scan_bwd_workspace_size.argtypes = [dims_p, ctypes.POINTER(ctypes.c_size_t)]
     lib.ssm_selective_scan_bwd.argtypes = [dims_p, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp,
                                            ctypes.POINTER(ssm_grads_t), vp, ctypes.c_size_t, vp]
@@ -227,6 +239,82 @@ def ssm_causal_conv1d_fwd(batch: int, dim: int, seqlen: int, width: int, io_dtyp
     rc = load_library().ssm_causal_conv1d_fwd(int(batch), int(dim), int(seqlen), int(width), int(io_dtype), _ptr(x),
                                               _ptr(w), _ptr(bias), 1 if silu else 0, _ptr(out), _stream(stream))
     return _check(rc, "ssm_causal_conv1d_fwd") if check else rc
+
+
+def ssm_causal_conv1d_packed_fwd(dim: int, total: int, n_seq: int, width: int, io_dtype: int, x, w, bias, silu: bool,
+                                 cu_seqlens, slots, has_state, states, n_slots: int, slot_stride: int, out,
+                                 stream=None, check: bool = True) -> int:
+    """The causal convolution over packed prompts with its history in slots (see include/ssm_scan.h)."""
+    rc = load_library().ssm_causal_conv1d_packed_fwd(
+        dim, total, n_seq, width, io_dtype, _ptr(x), _ptr(w), _ptr(bias), 1 if silu else 0, _ptr(cu_seqlens), _ptr(slots),
+        _ptr(has_state), _ptr(states), n_slots, slot_stride, _ptr(out), _stream(stream))
+    return _check(rc, "ssm_causal_conv1d_packed_fwd") if check else rc
+
+
+def ssm_causal_conv1d_update(batch: int, dim: int, width: int, io_dtype: int, x, w, bias, silu: bool, slots, states,
+                             n_slots: int, slot_stride: int, out, stream=None, check: bool = True) -> int:
+    """The causal convolution of one token per row with its history in slots (see include/ssm_scan.h)."""
+    rc = load_library().ssm_causal_conv1d_update(
+        batch, dim, width, io_dtype, _ptr(x), _ptr(w), _ptr(bias), 1 if silu else 0, _ptr(slots), _ptr(states), n_slots,
+        slot_stride, _ptr(out), _stream(stream))
+    return _check(rc, "ssm_causal_conv1d_update") if check else rc
+
+
+def ssm_selective_scan_packed_workspace_size(dims: ssm_dims_t, max_seqlen: int = 0, check: bool = True) -> int:
+    """Bytes of device scratch ssm_selective_scan_packed_fwd needs (see include/ssm_scan.h)."""
+    n = ctypes.c_size_t()
+    rc = load_library().ssm_selective_scan_packed_workspace_size(ctypes.byref(dims), int(max_seqlen), ctypes.byref(n))
+    if check:
+        _check(rc, "ssm_selective_scan_packed_workspace_size")
+    return int(n.value) if rc == SSM_OK else -rc
+
+
+def ssm_selective_scan_packed_fwd(dims: ssm_dims_t, u, delta, A, B, C, D, z, delta_bias, softplus: bool, cu_seqlens,
+                                  slots, has_state, states, n_slots: int, slot_stride: int, max_seqlen: int, out,
+                                  workspace, workspace_bytes: int, stream=None, check: bool = True) -> int:
+    """The forward scan over packed prompts with states in slots (see include/ssm_scan.h)."""
+    rc = load_library().ssm_selective_scan_packed_fwd(
+        ctypes.byref(dims), _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(delta_bias),
+        1 if softplus else 0, _ptr(cu_seqlens), _ptr(slots), _ptr(has_state), _ptr(states), n_slots, slot_stride,
+        max_seqlen, _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream))
+    return _check(rc, "ssm_selective_scan_packed_fwd") if check else rc
+
+
+def ssm_selective_state_update_slots(dims: ssm_dims_t, states, slots, n_slots: int, slot_stride: int, u, delta, A, B, C,
+                                     D, z, delta_bias, softplus: bool, out, stream=None, check: bool = True) -> int:
+    """One recurrence step of rows whose states sit in slots (see include/ssm_scan.h)."""
+    rc = load_library().ssm_selective_state_update_slots(
+        ctypes.byref(dims), _ptr(states), _ptr(slots), n_slots, slot_stride, _ptr(u), _ptr(delta), _ptr(A), _ptr(B),
+        _ptr(C), _ptr(D), _ptr(z), _ptr(delta_bias), 1 if softplus else 0, _ptr(out), _stream(stream))
+    return _check(rc, "ssm_selective_state_update_slots") if check else rc
+
+
+def ssm_state_slots_copy(pool, n_layers: int, n_slots: int, slot_bytes: int, slot_stride: int, layer_stride: int, src,
+                         dst, n_pairs: int, stream=None, check: bool = True) -> int:
+    """Copies, moves and clears state slots (see include/ssm_scan.h); strides in bytes."""
+    rc = load_library().ssm_state_slots_copy(_ptr(pool), n_layers, n_slots, slot_bytes, slot_stride, layer_stride,
+                                             _ptr(src), _ptr(dst), n_pairs, _stream(stream))
+    return _check(rc, "ssm_state_slots_copy") if check else rc
+
+
+def ssm_causal_conv1d_bwd_workspace_size(batch: int, dim: int, seqlen: int, width: int, io_dtype: int,
+                                         check: bool = True) -> int:
+    """Bytes of device scratch ssm_causal_conv1d_bwd needs (see include/ssm_scan.h)."""
+    n = ctypes.c_size_t()
+    rc = load_library().ssm_causal_conv1d_bwd_workspace_size(int(batch), int(dim), int(seqlen), int(width),
+                                                             int(io_dtype), ctypes.byref(n))
+    if check:
+        _check(rc, "ssm_causal_conv1d_bwd_workspace_size")
+    return int(n.value) if rc == SSM_OK else -rc
+
+
+def ssm_causal_conv1d_bwd(batch: int, dim: int, seqlen: int, width: int, io_dtype: int, x, w, bias, silu: bool, dout, dx,
+                          dw, dbias, workspace, workspace_bytes: int, stream=None, check: bool = True) -> int:
+    """Gradients of the causal convolution (see include/ssm_scan.h)."""
+    rc = load_library().ssm_causal_conv1d_bwd(
+        batch, dim, seqlen, width, io_dtype, _ptr(x), _ptr(w), _ptr(bias), 1 if silu else 0, _ptr(dout), _ptr(dx),
+        _ptr(dw), _ptr(dbias), _ptr(workspace), workspace_bytes, _stream(stream))
+    return _check(rc, "ssm_causal_conv1d_bwd") if check else rc
 
 
 def ssm_selective_scan_bwd_workspace_size(dims: ssm_dims_t, check: bool = True) -> int:

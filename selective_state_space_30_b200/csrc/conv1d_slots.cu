@@ -1,0 +1,436 @@
+// The causal depthwise convolution with its history in a pool of slots: over prompts packed end
+// to end, and for one new token of each row.  Declared in include/ssm_scan.h as
+// ssm_causal_conv1d_packed_fwd and ssm_causal_conv1d_update; the convolution is
+// ssm_causal_conv1d_fwd's (Mamba "architecture-details" page, "Model Configuration": d_conv).
+//
+//   v = bias[d] + sum_{k<W} w[d,k] x[d, t-W+1+k],   out = silu ? v / (1 + exp(-v)) : v
+//
+// A sequence's first W-1 tokens take their earlier inputs from its slot (or zero), and its last
+// W-1 inputs replace the slot's.  HBM-bound: every input is read and every output written once.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "scan_kernel.cuh"   // silu1
+#include "slots.h"
+#include "ssm_scan.h"
+
+namespace {
+
+constexpr int kMaxWidth = 4;
+constexpr int kThreads = 256;
+constexpr int kMaxGridY = 65535;
+
+template <typename T> __device__ __forceinline__ float to_f(T v);
+template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// V = 16 / sizeof(T) elements of a 16-byte piece
+template <typename T> __device__ __forceinline__ void unpack(const uint4& q, float* v);
+template <> __device__ __forceinline__ void unpack<float>(const uint4& q, float* v) {
+    v[0] = __uint_as_float(q.x); v[1] = __uint_as_float(q.y); v[2] = __uint_as_float(q.z); v[3] = __uint_as_float(q.w);
+}
+template <> __device__ __forceinline__ void unpack<__nv_bfloat16>(const uint4& q, float* v) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+template <typename T> __device__ __forceinline__ uint4 pack(const float* v);
+template <> __device__ __forceinline__ uint4 pack<float>(const float* v) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+template <> __device__ __forceinline__ uint4 pack<__nv_bfloat16>(const float* v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ------------------------------------------------------------- packed prompts
+
+struct PackedConv {
+    const void* x;
+    const float *w, *bias;
+    void* out;
+    void* states;
+    const int *cu, *slots;
+    const unsigned char* has_state;
+    int64_t dim, total, n_seq, n_slots, slot_stride;
+    int64_t head_ctas;       // CTAs of the sequences' first tokens, ahead of the others
+    unsigned head_tiles;     // channel tiles of those
+    unsigned time_tiles;     // time tiles of the others
+    int tx;                  // 16-byte pieces of a row that a CTA covers (a power of two)
+    int rows_per_thread;
+    int silu;
+};
+
+// The 16 bytes at p, where they lie inside [lo, hi); elements outside read as zero.
+template <typename T>
+__device__ __forceinline__ uint4 load_piece(const unsigned char* p, const unsigned char* lo, const unsigned char* hi) {
+    if (p >= lo && p + 16 <= hi) return __ldg(reinterpret_cast<const uint4*>(p));
+    constexpr int V = 16 / sizeof(T);
+    float v[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const unsigned char* q = p + e * (int)sizeof(T);
+        v[e] = q >= lo && q < hi ? to_f<T>(*reinterpret_cast<const T*>(q)) : 0.f;
+    }
+    return pack<T>(v);
+}
+
+// Role 1, one thread per (sequence, channel): the outputs of the sequence's first W-1 tokens,
+// which need the slot's history, and the slot's new history.  One thread reads the old history
+// and writes the new one, so no other CTA's read can meet the write.
+template <typename T, int W>
+__device__ __forceinline__ void sequence_heads(const PackedConv& p, int64_t bid) {
+    const int64_t seq = bid / p.head_tiles;
+    const int64_t d = (int64_t)(bid % p.head_tiles) * kThreads + threadIdx.x;
+    if (d >= p.dim) return;
+    const ssm::TokenRange r = ssm::token_range(p.cu, seq, p.total);
+    const int slot = p.slots ? __ldg(p.slots + seq) : (int)seq;
+    const ssm::SlotKind kind = ssm::slot_kind(slot, p.n_slots);
+    if (kind == ssm::kSlotPad) return;
+    const int64_t len = r.hi - r.lo;
+    T* orow = static_cast<T*>(p.out) + d * p.total + r.lo;
+    if (kind == ssm::kSlotBad) {
+        for (int64_t t = 0; t < len && t < W - 1; ++t) orow[t] = from_f<T>(__int_as_float(0x7FC00000));
+        return;
+    }
+    const T* xrow = static_cast<const T*>(p.x) + d * p.total + r.lo;
+    T* st = static_cast<T*>(p.states) + slot * p.slot_stride + d * (W - 1);
+    const bool has = p.has_state && __ldg(p.has_state + seq) != 0;
+    // the history, then the first tokens
+    T v[2 * (W - 1)];
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+        v[k] = has ? st[k] : from_f<T>(0.f);
+        v[W - 1 + k] = k < len ? xrow[k] : from_f<T>(0.f);
+    }
+    float w[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k] = __ldg(p.w + d * W + k);
+    const float b = p.bias ? __ldg(p.bias + d) : 0.f;
+#pragma unroll
+    for (int t = 0; t < W - 1; ++t) {
+        float o = b;
+#pragma unroll
+        for (int k = 0; k < W; ++k) o = fmaf(w[k], to_f<T>(v[t + k]), o);
+        if (t < len) orow[t] = from_f<T>(p.silu ? ssm::silu1(o) : o);
+    }
+    // element k of the new history is input len - (W-1) + k, or an older one of the slot's
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+        T keep;
+        if (len >= W - 1) {
+            keep = xrow[len - (W - 1) + k];
+        } else {
+            keep = v[k];
+#pragma unroll
+            for (int s = 1; s < W - 1; ++s)
+                if (len == s) keep = v[s + k];
+        }
+        st[k] = keep;
+    }
+}
+
+// Role 2: every other token.  A CTA covers tx pieces of a row and walks rows; the 16-byte pieces
+// follow each row's own alignment, so odd row lengths move whole pieces too.  Bit t of `live`
+// says that token t0 + t has its W-1 earlier inputs in its own sequence; it is made once per CTA
+// and serves every row.
+template <typename T, int W>
+__device__ __forceinline__ void sequence_bodies(const PackedConv& p, int64_t bid) {
+    constexpr int V = 16 / sizeof(T), ES = (int)sizeof(T);
+    constexpr int kWords = (kThreads * V + 2 * V + 31) / 32 + 1;
+    __shared__ unsigned live[kWords], bad[kWords];
+    const int64_t tile = bid % p.time_tiles, rt = bid / p.time_tiles;
+    const int tx = p.tx, ty = kThreads / tx;
+    const int64_t span = (int64_t)tx * V;
+    const int64_t t0 = tile * span - V;                 // token of bit 0: a piece may start up to V-1 tokens early
+    const int bits = (int)span + V;
+    for (int i = threadIdx.x; i < kWords; i += kThreads) live[i] = bad[i] = 0u;
+    __syncthreads();
+    // sequences that meet [t0, t0 + bits): the bounds rise, so a binary search finds the first.
+    // Bounds out of order mark the wrong tokens at most, each inside the buffer.
+    int64_t a = 0, b = p.n_seq;
+    while (a < b) {
+        const int64_t m = (a + b) / 2;
+        if (__ldg(p.cu + m + 1) <= t0) a = m + 1;
+        else b = m;
+    }
+    for (int64_t s = a + threadIdx.x; s < p.n_seq; s += kThreads) {
+        const ssm::TokenRange r = ssm::token_range(p.cu, s, p.total);
+        if (r.lo >= t0 + bits) break;
+        const ssm::SlotKind kind = ssm::slot_kind(p.slots ? __ldg(p.slots + s) : (int)s, p.n_slots);
+        if (kind == ssm::kSlotPad) continue;
+        int64_t lo = r.lo + (W - 1) - t0, hi = r.hi - t0;
+        lo = lo < 0 ? 0 : lo;
+        hi = hi > bits ? bits : hi;
+        for (int64_t w = lo >> 5; w * 32 < hi; ++w) {
+            const int f = lo > w * 32 ? (int)(lo - w * 32) : 0;
+            const int e = hi < w * 32 + 32 ? (int)(hi - w * 32) : 32;
+            if (f < e) {
+                const unsigned m = (e == 32 ? 0xffffffffu : (1u << e) - 1u) & ~((1u << f) - 1u);
+                atomicOr(live + w, m);
+                if (kind == ssm::kSlotBad) atomicOr(bad + w, m);
+            }
+        }
+    }
+    __syncthreads();
+    const int px = threadIdx.x % tx, py = threadIdx.x / tx;
+    const unsigned char* lo = static_cast<const unsigned char*>(p.x);
+    const unsigned char* hi = lo + p.dim * p.total * ES;
+    // out pieces follow out's alignment; where x's differs the inputs are read by elements
+    for (int i = 0; i < p.rows_per_thread; ++i) {
+        const int64_t d = (rt * p.rows_per_thread + i) * ty + py;
+        if (d >= p.dim) break;
+        unsigned char* orow = static_cast<unsigned char*>(p.out) + d * p.total * ES;
+        const unsigned char* xrow = lo + d * p.total * ES;
+        const int m = (int)((reinterpret_cast<uintptr_t>(orow) & 15u) / ES);
+        const int64_t t = tile * span + (int64_t)px * V - m;     // first token of the piece
+        const int bit = (int)(t - t0);
+        const unsigned sel = (1u << V) - 1u;
+        const unsigned mask = __funnelshift_r(live[bit >> 5], live[(bit >> 5) + 1], bit & 31) & sel;
+        if (mask == 0u) continue;
+        const unsigned nan = __funnelshift_r(bad[bit >> 5], bad[(bit >> 5) + 1], bit & 31) & mask;
+        float xv[2 * V];                                          // tokens t - V .. t + V - 1
+        const unsigned char* xp = xrow + t * ES;
+        if ((reinterpret_cast<uintptr_t>(xp) & 15u) == 0) {
+            unpack<T>(load_piece<T>(xp - 16, lo, hi), xv);
+            unpack<T>(load_piece<T>(xp, lo, hi), xv + V);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V + W - 1; ++e) {
+                const unsigned char* q = xp + (e - (W - 1)) * ES;
+                xv[V - (W - 1) + e] = q >= lo && q < hi ? to_f<T>(*reinterpret_cast<const T*>(q)) : 0.f;
+            }
+        }
+        float w[W];
+#pragma unroll
+        for (int k = 0; k < W; ++k) w[k] = __ldg(p.w + d * W + k);
+        const float bs = p.bias ? __ldg(p.bias + d) : 0.f;
+        float o[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            float v = bs;
+#pragma unroll
+            for (int k = 0; k < W; ++k) v = fmaf(w[k], xv[V + e - (W - 1) + k], v);
+            o[e] = p.silu ? ssm::silu1(v) : v;
+            if ((nan >> e) & 1u) o[e] = __int_as_float(0x7FC00000);
+        }
+        if (mask == sel) {
+            *reinterpret_cast<uint4*>(orow + t * ES) = pack<T>(o);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if ((mask >> e) & 1u) reinterpret_cast<T*>(orow)[t + e] = from_f<T>(o[e]);
+        }
+    }
+}
+
+template <typename T, int W>
+__global__ void __launch_bounds__(kThreads) conv1d_packed_kernel(const PackedConv p) {
+    if (blockIdx.x < p.head_ctas) sequence_heads<T, W>(p, blockIdx.x);
+    else sequence_bodies<T, W>(p, blockIdx.x - p.head_ctas);
+}
+
+// width 1: no history, so role 1 has nothing to do
+template <typename T>
+__global__ void __launch_bounds__(kThreads) conv1d_packed_kernel_w1(const PackedConv p) {
+    sequence_bodies<T, 1>(p, blockIdx.x);
+}
+
+template <typename T, int W>
+int launch_packed(PackedConv p, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    const int64_t pieces = (p.total + V - 1 + V - 1) / V;   // of a row, its first one up to V-1 tokens early
+    p.tx = 16;
+    while (p.tx < 128 && p.tx < pieces) p.tx *= 2;
+    const int ty = kThreads / p.tx;
+    const int64_t tt = p.total > 0 ? (pieces + p.tx - 1) / p.tx : 0;
+    // enough rows per CTA to carry the making of the mask, as long as 8 CTAs per SM remain
+    int rows = 1;
+    while (rows < 16 && tt * ((p.dim + ty - 1) / ty) / (2 * rows) >= 148 * 8) rows *= 2;
+    p.rows_per_thread = rows;
+    const int64_t rtiles = (p.dim + (int64_t)ty * rows - 1) / ((int64_t)ty * rows);
+    const int64_t head_tiles = (p.dim + kThreads - 1) / kThreads;
+    p.head_ctas = W > 1 ? p.n_seq * head_tiles : 0;
+    const int64_t ctas = p.head_ctas + tt * rtiles;
+    if (ctas > 0x7FFFFFFF) return SSM_ERR_UNSUPPORTED;
+    if (ctas == 0) return SSM_OK;
+    p.head_tiles = (unsigned)head_tiles;
+    p.time_tiles = (unsigned)(tt > 0 ? tt : 1);
+    if constexpr (W > 1) conv1d_packed_kernel<T, W><<<(unsigned)ctas, kThreads, 0, s>>>(p);
+    else conv1d_packed_kernel_w1<T><<<(unsigned)ctas, kThreads, 0, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
+}
+
+template <typename T>
+int launch_packed_t(const PackedConv& p, int width, cudaStream_t s) {
+    switch (width) {
+        case 1: return launch_packed<T, 1>(p, s);
+        case 2: return launch_packed<T, 2>(p, s);
+        case 3: return launch_packed<T, 3>(p, s);
+        case 4: return launch_packed<T, 4>(p, s);
+        default: return SSM_ERR_UNSUPPORTED;
+    }
+}
+
+// -------------------------------------------------------------- single tokens
+
+struct TokenConv {
+    const void* x;
+    const float *w, *bias;
+    void* out;
+    void* states;
+    const int* slots;
+    int64_t batch, dim, n_slots, slot_stride;
+    int silu;
+};
+
+// C channels per thread, of one row: 16 bytes of x and out and W-1 times 16 bytes of the slot
+// (C = V), or one channel (C = 1) where those are not 16-byte aligned.
+template <typename T, int W, int C>
+__global__ void __launch_bounds__(128) conv1d_update_kernel(const TokenConv p) {
+    const int64_t d = ((int64_t)blockIdx.x * 128 + threadIdx.x) * C;
+    if (d >= p.dim) return;
+    for (int64_t b = blockIdx.y; b < p.batch; b += gridDim.y) {
+        const int slot = p.slots ? __ldg(p.slots + b) : (int)b;
+        const ssm::SlotKind kind = ssm::slot_kind(slot, p.n_slots);
+        if (kind == ssm::kSlotPad) continue;
+        float x[C], o[C], h[C * (W > 1 ? W - 1 : 1)];
+        T* st = static_cast<T*>(p.states) + (kind == ssm::kSlotLive ? slot : 0) * p.slot_stride + d * (W - 1);
+        const T* xr = static_cast<const T*>(p.x) + b * p.dim + d;
+        T* orow = static_cast<T*>(p.out) + b * p.dim + d;
+        if constexpr (C > 1) {
+            const uint4 q = __ldg(reinterpret_cast<const uint4*>(xr));
+            unpack<T>(q, x);
+        } else {
+            x[0] = to_f<T>(*xr);
+        }
+        if (W > 1 && kind == ssm::kSlotLive) {
+            if constexpr (C > 1) {
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) unpack<T>(reinterpret_cast<const uint4*>(st)[k], h + k * C);
+            } else {
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) h[k] = to_f<T>(st[k]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < C * (W - 1); ++k) h[k] = 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const float* wr = p.w + (d + c) * W;
+            float v = p.bias ? __ldg(p.bias + d + c) : 0.f;
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) v = fmaf(__ldg(wr + k), h[c * (W - 1) + k], v);
+            v = fmaf(__ldg(wr + W - 1), x[c], v);
+            o[c] = p.silu ? ssm::silu1(v) : v;
+            if (kind == ssm::kSlotBad) o[c] = __int_as_float(0x7FC00000);
+        }
+        // the oldest input leaves, this one enters
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+#pragma unroll
+            for (int k = 0; k + 1 < W - 1; ++k) h[c * (W - 1) + k] = h[c * (W - 1) + k + 1];
+            if (W > 1) h[c * (W - 1) + W - 2] = x[c];
+        }
+        if constexpr (C > 1) {
+            *reinterpret_cast<uint4*>(orow) = pack<T>(o);
+            if (kind == ssm::kSlotLive) {
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) reinterpret_cast<uint4*>(st)[k] = pack<T>(h + k * C);
+            }
+        } else {
+            *orow = from_f<T>(o[0]);
+            if (kind == ssm::kSlotLive) {
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) st[k] = from_f<T>(h[k]);
+            }
+        }
+    }
+}
+
+template <typename T, int W>
+int launch_update(const TokenConv& p, bool vec, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    const int64_t per = vec ? V : 1;
+    const int64_t bx = (p.dim / per + (p.dim % per ? 1 : 0) + 127) / 128;
+    const int64_t by = p.batch < kMaxGridY ? p.batch : kMaxGridY;
+    const dim3 g((unsigned)bx, (unsigned)by);
+    if (vec) conv1d_update_kernel<T, W, V><<<g, 128, 0, s>>>(p);
+    else conv1d_update_kernel<T, W, 1><<<g, 128, 0, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
+}
+
+template <typename T>
+int launch_update_t(const TokenConv& p, int width, bool vec, cudaStream_t s) {
+    switch (width) {
+        case 1: return launch_update<T, 1>(p, vec, s);
+        case 2: return launch_update<T, 2>(p, vec, s);
+        case 3: return launch_update<T, 3>(p, vec, s);
+        case 4: return launch_update<T, 4>(p, vec, s);
+        default: return SSM_ERR_UNSUPPORTED;
+    }
+}
+
+bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+}  // namespace
+
+extern "C" int ssm_causal_conv1d_packed_fwd(int64_t dim, int64_t total, int64_t n_seq, int32_t width, int32_t io_dtype,
+                                            const void* x, const float* w, const float* bias, int silu,
+                                            const int32_t* cu_seqlens, const int32_t* slots, const uint8_t* has_state,
+                                            void* states, int64_t n_slots, int64_t slot_stride, void* out,
+                                            ssm_stream_t stream) {
+    if (dim <= 0 || total < 0 || n_seq < 0 || n_slots < 0) return SSM_ERR_INVALID_ARG;
+    if (dim > (1 << 24) || total > 0x7FFFFFFF || n_seq > 0x7FFFFFFF || n_slots > 0x7FFFFFFF) return SSM_ERR_INVALID_ARG;
+    if (io_dtype != SSM_F32 && io_dtype != SSM_BF16) return SSM_ERR_INVALID_ARG;
+    if (width < 1 || width > kMaxWidth) return SSM_ERR_UNSUPPORTED;
+    if (n_seq == 0) return SSM_OK;
+    if (!w || !cu_seqlens || (width > 1 && !states)) return SSM_ERR_INVALID_ARG;
+    if (total > 0 && (!x || !out)) return SSM_ERR_INVALID_ARG;
+    if (width > 1 && slot_stride < dim * (width - 1)) return SSM_ERR_INVALID_ARG;
+    const uintptr_t esz = io_dtype == SSM_BF16 ? 2 : 4;
+    if (!aligned_to(x, esz) || !aligned_to(out, esz) || !aligned_to(states, esz)) return SSM_ERR_INVALID_ARG;
+    PackedConv p{};
+    p.x = x; p.w = w; p.bias = bias; p.out = out; p.states = states;
+    p.cu = cu_seqlens; p.slots = slots; p.has_state = has_state;
+    p.dim = dim; p.total = total; p.n_seq = n_seq; p.n_slots = n_slots; p.slot_stride = slot_stride;
+    p.silu = silu ? 1 : 0;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return io_dtype == SSM_BF16 ? launch_packed_t<__nv_bfloat16>(p, width, s) : launch_packed_t<float>(p, width, s);
+}
+
+extern "C" int ssm_causal_conv1d_update(int64_t batch, int64_t dim, int32_t width, int32_t io_dtype, const void* x,
+                                        const float* w, const float* bias, int silu, const int32_t* slots, void* states,
+                                        int64_t n_slots, int64_t slot_stride, void* out, ssm_stream_t stream) {
+    if (batch < 0 || dim <= 0 || n_slots < 0) return SSM_ERR_INVALID_ARG;
+    if (dim > (1 << 24) || batch > 0x7FFFFFFF || n_slots > 0x7FFFFFFF) return SSM_ERR_INVALID_ARG;
+    if (io_dtype != SSM_F32 && io_dtype != SSM_BF16) return SSM_ERR_INVALID_ARG;
+    if (width < 1 || width > kMaxWidth) return SSM_ERR_UNSUPPORTED;
+    if (batch == 0) return SSM_OK;
+    if (!x || !w || !out || (width > 1 && !states)) return SSM_ERR_INVALID_ARG;
+    if (width > 1 && slot_stride < dim * (width - 1)) return SSM_ERR_INVALID_ARG;
+    const int64_t esz = io_dtype == SSM_BF16 ? 2 : 4, V = 16 / esz;
+    if (!aligned_to(x, esz) || !aligned_to(out, esz) || !aligned_to(states, esz)) return SSM_ERR_INVALID_ARG;
+    const bool vec = dim % V == 0 && aligned_to(x, 16) && aligned_to(out, 16) && aligned_to(states, 16) &&
+                     slot_stride % V == 0;
+    TokenConv p{};
+    p.x = x; p.w = w; p.bias = bias; p.out = out; p.states = states; p.slots = slots;
+    p.batch = batch; p.dim = dim; p.n_slots = n_slots; p.slot_stride = slot_stride; p.silu = silu ? 1 : 0;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return io_dtype == SSM_BF16 ? launch_update_t<__nv_bfloat16>(p, width, vec, s)
+                                : launch_update_t<float>(p, width, vec, s);
+}

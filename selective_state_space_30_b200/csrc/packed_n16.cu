@@ -1,0 +1,5 @@
+// The scan over packed prompts with dstate 16.
+#include "scan_packed.cuh"
+
+template int ssm::packed::launch_n<__nv_bfloat16, 16>(PackedParams&, bool, cudaStream_t);
+template int ssm::packed::launch_n<float, 16>(PackedParams&, bool, cudaStream_t);

@@ -1,0 +1,624 @@
+#pragma once
+// The selective scan over prompts packed end to end, each continuing from its slot of a state
+// pool (declared in include/ssm_scan.h as ssm_selective_scan_packed_fwd): the recurrence of the
+// Mamba "architecture-details" page, section "How S6 Works", per sequence.
+//
+// Mathematics.  Per sequence, channel d and state n, over the sequence's own tokens t:
+//   dt = softplus(delta + bias), h = exp(dt A) h + dt u B, y = sum_n C h + D u, out = y silu(z).
+// A stretch of tokens maps the state by h -> P h + h_loc, with P = exp(A sum dt) and h_loc the
+// end state from zero, so a sequence can be cut into chunks that run at the same time:
+//   launch 1: the first chunk of each sequence in full; every middle chunk for (sum dt, h_loc) only
+//   launch 2: every later chunk joins its predecessors' pairs and runs in full.
+// Uncut sequences need launch 1 alone.  A middle chunk's exps are paid twice, so sequences are
+// cut only where their count leaves SMs without work (choose_chunk).
+//
+// Bound: one ex2 per (t, channel, state), 16 per clock and SM, in the per-channel layout; the
+// fp32 pipe (three operations per (t, channel, state)) in the per-head layout, whose decay is
+// one ex2 per (t, channel).
+//
+// Layout.  A lane holds 8 states of CPL channels, N/8 lanes a channel group: the B and C of a
+// step, fp32 in shared memory, then serve CPL channels per load, and the sum over states
+// crosses lanes only log2(N/8) times.  The tokens of a block (64 bytes of a row) are staged by
+// 16-byte asynchronous copies one block ahead; rows whose starts are not 16-byte aligned are
+// copied as the aligned pieces that hold them and read at their offset.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "scan_kernel.cuh"   // ex2_approx, f32x2 operations, softplus, silu, window_reduce
+#include "slots.h"
+#include "ssm_scan.h"
+
+namespace ssm {
+namespace packed {
+
+using ssm::add2;
+using ssm::dup2;
+using ssm::ex2_approx;
+using ssm::fma2;
+using ssm::kLog2e;
+using ssm::mul2;
+
+struct PackedParams {
+    const void *u, *delta, *B, *C, *z;
+    const float *A, *D, *bias;
+    void* out;
+    float* states;
+    const int *cu, *slots;
+    const unsigned char* has_state;
+    float *ws_h, *ws_p;      // per chunk: (dim, dstate) states and, per channel, sum dt (or the product of decays)
+    int64_t n_seq, total, n_slots, slot_stride;
+    int64_t dim, nheads, ngroups, group_dim, head_dim;
+    int64_t chunk;           // tokens of a chunk; 0: sequences are not cut
+    int64_t n_chunks;        // chunks the workspace has room for
+    unsigned tiles_per_group, n_tiles;
+    int softplus, phase, state_vec;
+};
+
+template <typename T, int N, bool HEAD, bool ALIGNED>
+struct PackedCfg {
+    static constexpr int ESZ = sizeof(T);
+    static constexpr int V = 16 / ESZ;                  // elements per 16-byte piece
+    static constexpr int TB = 64 / ESZ;                 // steps per block
+    static constexpr int S = 8;                         // states per lane
+    static constexpr int TPC = N / S;                   // lanes per channel
+    static constexpr int CPL = N == 128 ? 4 : 2;        // channels per lane
+    static constexpr int LG = 32 / TPC;                 // lane groups of a warp
+    static constexpr int CW = LG * CPL;                 // channels per warp
+    static constexpr int W = N == 8 ? 2 : 4;            // warps
+    static constexpr int CT = W * CW;                   // channels per tile
+    static constexpr int NT = 32 * W;
+    static constexpr int WT = CPL * 4 >= TPC ? 4 : 8;   // steps per window
+    static constexpr int PIECES = ALIGNED ? 4 : 5;      // 16-byte pieces that hold a row's block
+    static constexpr int PITCH = 80;                    // bytes of a staged row: five pieces, so rows start in different banks
+    static constexpr int R_U = 0, R_Z = CT, R_DT = 2 * CT, R_B = 3 * CT, R_C = 3 * CT + N, ROWS = 3 * CT + 2 * N;
+    static constexpr int STAGE = ROWS * PITCH;
+    // steps of a prologue or epilogue item (one channel's)
+    static constexpr int PS = CW * TB / 8 >= 32 ? 8 : 4;
+    static constexpr int ITEMS = CW * TB / PS / 32;     // per lane
+    static constexpr int OFF_BC = 2 * STAGE;            // fp32 [step][B of all states | C of all states]
+    static constexpr int OFF_Q = OFF_BC + TB * 2 * N * 4;   // per warp: [step][channel] (dt or decay, dt u), then y
+    static constexpr int Q_WARP = TB * CW * 8;
+    static constexpr int OFF_PAR = OFF_Q + W * Q_WARP;  // bias, D, and the head's A (log2 e folded in), per channel
+    static constexpr int OFF_MISC = OFF_PAR + 3 * CT * 4;
+    static constexpr int SMEM = OFF_MISC + 64;
+    static_assert(CW * TB / PS % 32 == 0, "whole items per lane");
+    static_assert(TB % WT == 0 && (CPL * WT) % 2 == 0, "whole windows");
+};
+
+__device__ __forceinline__ void cp16(unsigned dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// Elements off the 16-byte grid of the first of a row, for a row that starts at `p`.
+template <typename T> __device__ __forceinline__ int skew(const void* p) {
+    return (int)((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
+}
+
+// CNT elements of a staged row, from element e on.
+template <typename T, bool ALIGNED, int CNT>
+__device__ __forceinline__ void read_row(const unsigned char* row, int e, float (&v)[CNT]) {
+    if constexpr (sizeof(T) == 4) {
+        if constexpr (ALIGNED) {
+#pragma unroll
+            for (int i = 0; i < CNT; i += 4) {
+                const float4 q = *reinterpret_cast<const float4*>(row + (e + i) * 4);
+                v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < CNT; ++i) v[i] = *reinterpret_cast<const float*>(row + (e + i) * 4);
+        }
+    } else {
+        uint32_t w[CNT / 2];
+        if constexpr (ALIGNED) {
+            if constexpr (CNT == 8) {
+                const uint4 q = *reinterpret_cast<const uint4*>(row + e * 2);
+                w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+            } else {
+                const uint2 q = *reinterpret_cast<const uint2*>(row + e * 2);
+                w[0] = q.x; w[1] = q.y;
+            }
+        } else {
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(row + ((e * 2) & ~3));
+            const int sh = (e & 1) * 16;
+            uint32_t lo = p[0];
+#pragma unroll
+            for (int i = 0; i < CNT / 2; ++i) {
+                const uint32_t hi = p[i + 1];
+                w[i] = __funnelshift_r(lo, hi, sh);
+                lo = hi;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < CNT / 2; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+}
+
+template <typename T, bool ALIGNED, int CNT>
+__device__ __forceinline__ void write_row(unsigned char* row, int e, const float (&v)[CNT]) {
+    if constexpr (sizeof(T) == 4) {
+        if constexpr (ALIGNED) {
+#pragma unroll
+            for (int i = 0; i < CNT; i += 4)
+                *reinterpret_cast<float4*>(row + (e + i) * 4) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < CNT; ++i) *reinterpret_cast<float*>(row + (e + i) * 4) = v[i];
+        }
+    } else {
+        uint32_t w[CNT / 2];
+#pragma unroll
+        for (int i = 0; i < CNT / 2; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        if constexpr (ALIGNED) {
+            if constexpr (CNT == 8) *reinterpret_cast<uint4*>(row + e * 2) = make_uint4(w[0], w[1], w[2], w[3]);
+            else *reinterpret_cast<uint2*>(row + e * 2) = make_uint2(w[0], w[1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < CNT; ++i)
+                *reinterpret_cast<unsigned short*>(row + (e + i) * 2) = (unsigned short)(w[i / 2] >> (16 * (i & 1)));
+        }
+    }
+}
+
+// What a CTA works on: one channel tile of one chunk of one sequence.
+struct Task {
+    int64_t g, ci0, d0;      // group, first channel within it, first channel
+    int nch;                 // channels of the tile
+    int64_t t0, t1;          // tokens
+    int64_t chunk_id;        // of the workspace
+    int64_t k;               // chunk of its sequence
+    bool last;
+    int64_t slot;
+    bool has;                // starts from the slot's state
+};
+
+// One chunk.  LOCAL: only its decay and its end state from zero.
+template <typename T, int N, bool HEAD, bool ALIGNED, bool LOCAL>
+__device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk, unsigned char* smem) {
+    using Cf = PackedCfg<T, N, HEAD, ALIGNED>;
+    constexpr int S = Cf::S, TPC = Cf::TPC, CPL = Cf::CPL, CW = Cf::CW, CT = Cf::CT, TB = Cf::TB, V = Cf::V;
+    constexpr int ESZ = Cf::ESZ, NT = Cf::NT, PITCH = Cf::PITCH, WT = Cf::WT, PS = Cf::PS;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int lg = lane / TPC, j = lane % TPC;
+    const int64_t L = p.total;
+    const int64_t h_lo = HEAD ? tk.d0 / p.head_dim : tk.d0;           // first delta row of the tile
+    const int n_dt = HEAD ? (int)((tk.d0 + tk.nch - 1) / p.head_dim - h_lo + 1) : tk.nch;
+    float* bc = reinterpret_cast<float*>(smem + Cf::OFF_BC);
+    float2* q = reinterpret_cast<float2*>(smem + Cf::OFF_Q + warp * Cf::Q_WARP);
+    float* s_bias = reinterpret_cast<float*>(smem + Cf::OFF_PAR);
+    float* s_D = s_bias + CT;
+    float* s_a = s_D + CT;
+
+    // the first step of block 0 sits on the 16-byte grid of an aligned row
+    const int64_t tb0 = tk.t0 & ~(int64_t)(V - 1);
+    const int nblk = (int)((tk.t1 - tb0 + TB - 1) / TB);
+
+    const unsigned char* ub = static_cast<const unsigned char*>(p.u) + tk.d0 * L * ESZ;
+    const unsigned char* zb = p.z ? static_cast<const unsigned char*>(p.z) + tk.d0 * L * ESZ : nullptr;
+    const unsigned char* db = static_cast<const unsigned char*>(p.delta) + h_lo * L * ESZ;
+    const unsigned char* Bb = static_cast<const unsigned char*>(p.B) + tk.g * N * L * ESZ;
+    const unsigned char* Cb = static_cast<const unsigned char*>(p.C) + tk.g * N * L * ESZ;
+    unsigned char* ob = static_cast<unsigned char*>(p.out) + tk.d0 * L * ESZ;
+
+    // Copies of `rows` rows of a tensor (first row at `base`) into staged rows r0 .. of a stage.
+    // A piece is copied if it holds a token of the chunk; others keep what the stage held, and
+    // nothing computed from them is used.  `lo`, `hi`: the tensor's bytes; a piece that starts
+    // before them (a base off the 16-byte grid) is copied by elements, one that ends behind them
+    // is cut.
+    auto stage_rows = [&](int stage, int r0, const unsigned char* base, int rows, int64_t tb, const unsigned char* lo,
+                          const unsigned char* hi) {
+        unsigned char* sb = smem + stage * Cf::STAGE + r0 * PITCH;
+        if constexpr (ALIGNED) {
+            const int g = tid & 3;
+            const int64_t ts = tb + g * V;
+            if (ts < tk.t1 && ts + V > tk.t0) {
+                const unsigned dst = ssm::smem_u32(sb + g * 16);
+                const unsigned char* src = base + ts * ESZ;
+                for (int r = tid >> 2; r < rows; r += NT / 4) cp16(dst + r * PITCH, src + (int64_t)r * L * ESZ, 16);
+            }
+        } else {
+            for (int i = tid; i < rows * Cf::PIECES; i += NT) {
+                const int r = i / Cf::PIECES, g = i % Cf::PIECES;
+                const unsigned char* row = base + (int64_t)r * L * ESZ;
+                const int m = skew<T>(row);
+                const int64_t ts = tb + g * V - m;
+                if (ts < tk.t1 && ts + V > tk.t0) {
+                    const unsigned char* src = row + ts * ESZ;
+                    unsigned char* dst = sb + r * PITCH + g * 16;
+                    if (src >= lo) {
+                        const int64_t left = hi - src;
+                        cp16(ssm::smem_u32(dst), src, left < 16 ? (int)left : 16);
+                    } else {
+                        for (int e = 0; e < V; ++e)
+                            if (src + e * ESZ >= lo && src + e * ESZ < hi)
+                                *reinterpret_cast<T*>(dst + e * ESZ) = *reinterpret_cast<const T*>(src + e * ESZ);
+                    }
+                }
+            }
+        }
+    };
+    auto bytes_of = [&](int64_t rows) { return rows * L * ESZ; };
+    auto issue = [&](int kb) {
+        const int64_t tb = tb0 + (int64_t)kb * TB;
+        const int st = kb & 1;
+        auto put = [&](int r0, const unsigned char* base, int rows, const void* t, int64_t t_rows) {
+            const unsigned char* lo = static_cast<const unsigned char*>(t);
+            stage_rows(st, r0, base, rows, tb, lo, lo + bytes_of(t_rows));
+        };
+        put(Cf::R_U, ub, tk.nch, p.u, p.dim);
+        if (!LOCAL && zb) put(Cf::R_Z, zb, tk.nch, p.z, p.dim);
+        put(Cf::R_DT, db, n_dt, p.delta, p.nheads);
+        put(Cf::R_B, Bb, N, p.B, p.ngroups * N);
+        if (!LOCAL) put(Cf::R_C, Cb, N, p.C, p.ngroups * N);
+        cp_commit();
+    };
+
+    __syncthreads();
+    if (nblk > 0) issue(0);
+    for (int c = tid; c < CT; c += NT) {
+        const int64_t d = tk.d0 + (c < tk.nch ? c : 0);
+        const int64_t hd = HEAD ? d / p.head_dim : d;
+        s_bias[c] = p.bias ? __ldg(p.bias + hd) : 0.f;
+        s_D[c] = p.D ? __ldg(p.D + d) : 0.f;
+        if constexpr (HEAD) s_a[c] = __ldg(p.A + hd) * kLog2e;
+    }
+
+    // this lane's channels and states
+    float2 h[CPL][S / 2], a2[HEAD ? 1 : CPL][S / 2];
+    float acc[CPL];
+    bool ok[CPL];
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+        const int lc = warp * CW + lg * CPL + c;
+        ok[c] = lc < tk.nch;
+        const int64_t d = tk.d0 + (ok[c] ? lc : 0);
+        acc[c] = HEAD ? 1.f : 0.f;
+        if constexpr (!HEAD) {
+            const float* ar = p.A + d * N + j * S;
+#pragma unroll
+            for (int s = 0; s < S / 2; ++s) a2[c][s] = make_float2(__ldg(ar + 2 * s) * kLog2e, __ldg(ar + 2 * s + 1) * kLog2e);
+        }
+        // the state that enters the chunk
+        if (!LOCAL && tk.k > 0) {
+            // join the chunks before: the first holds a state, the later ones (decay, state from zero)
+            const int64_t c0 = tk.chunk_id - tk.k;
+            const float* hr = p.ws_h + (c0 * p.dim + d) * N + j * S;
+#pragma unroll
+            for (int s = 0; s < S / 2; ++s) h[c][s] = __ldcg(reinterpret_cast<const float2*>(hr) + s);
+            for (int64_t i = 1; i < tk.k; ++i) {
+                const float pr = __ldcg(p.ws_p + (c0 + i) * p.dim + d);
+                const float* hi = p.ws_h + ((c0 + i) * p.dim + d) * N + j * S;
+#pragma unroll
+                for (int s = 0; s < S / 2; ++s) {
+                    const float2 loc = __ldcg(reinterpret_cast<const float2*>(hi) + s);
+                    float2 dec;
+                    if constexpr (HEAD) {
+                        dec = dup2(pr);
+                    } else {
+                        const float2 arg = mul2(dup2(pr), a2[c][s]);
+                        dec = make_float2(ex2_approx(arg.x), ex2_approx(arg.y));
+                    }
+                    h[c][s] = fma2(dec, h[c][s], loc);
+                }
+            }
+        } else if (!LOCAL && tk.has) {
+            const float* hr = p.states + tk.slot * p.slot_stride + d * N + j * S;
+            if (p.state_vec) {
+#pragma unroll
+                for (int s = 0; s < S / 2; s += 2) {
+                    const float4 v = *reinterpret_cast<const float4*>(hr + 2 * s);
+                    h[c][s] = make_float2(v.x, v.y);
+                    h[c][s + 1] = make_float2(v.z, v.w);
+                }
+            } else {
+#pragma unroll
+                for (int s = 0; s < S / 2; ++s) h[c][s] = make_float2(hr[2 * s], hr[2 * s + 1]);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < S / 2; ++s) h[c][s] = make_float2(0.f, 0.f);
+        }
+    }
+
+    for (int kb = 0; kb < nblk; ++kb) {
+        const int64_t tb = tb0 + (int64_t)kb * TB;
+        // the chunk's steps of the block: [lo, hi)
+        const int lo = tk.t0 > tb ? (int)(tk.t0 - tb) : 0;
+        const int hi = tk.t1 - tb < TB ? (int)(tk.t1 - tb) : TB;
+        unsigned char* sb = smem + (kb & 1) * Cf::STAGE;
+        cp_wait_all();
+        __syncthreads();   // the block is staged, and every warp is done with the block before
+        if (kb + 1 < nblk) issue(kb + 1);
+
+        // B and C to fp32, [step][state]; steps outside the chunk become zero
+        constexpr int CV = ESZ == 2 ? 8 : 4;
+        constexpr int BCR = LOCAL ? N : 2 * N;
+        for (int i = tid; i < BCR * (TB / CV); i += NT) {
+            const int r = i % BCR, e0 = i / BCR * CV;
+            const unsigned char* src = r < N ? Bb : Cb;
+            const int m = ALIGNED ? 0 : skew<T>(src + (int64_t)(r < N ? r : r - N) * L * ESZ);
+            float v[CV];
+            read_row<T, ALIGNED, CV>(sb + (Cf::R_B + r) * PITCH, m + e0, v);
+#pragma unroll
+            for (int e = 0; e < CV; ++e) bc[(e0 + e) * 2 * N + r] = e0 + e >= lo && e0 + e < hi ? v[e] : 0.f;
+        }
+        // prologue: dt (or the decay) and dt u of the warp's channels
+#pragma unroll
+        for (int it = 0; it < Cf::ITEMS; ++it) {
+            const int idx = lane + 32 * it, c = idx % CW, e0 = idx / CW * PS;
+            const int lc = warp * CW + c;
+            const int cl = lc < tk.nch ? lc : 0;
+            const int dr = HEAD ? (int)((tk.d0 + cl) / p.head_dim - h_lo) : lc;
+            float x[PS], uv[PS];
+            const int mu = ALIGNED ? 0 : skew<T>(ub + (int64_t)lc * L * ESZ);
+            const int md = ALIGNED ? 0 : skew<T>(db + (int64_t)dr * L * ESZ);
+            read_row<T, ALIGNED, PS>(sb + (Cf::R_U + lc) * PITCH, mu + e0, uv);
+            read_row<T, ALIGNED, PS>(sb + (Cf::R_DT + dr) * PITCH, md + e0, x);
+            const float bias = s_bias[lc];
+            const float ah = HEAD ? s_a[lc] : 0.f;
+#pragma unroll
+            for (int e = 0; e < PS; e += 2) {
+                const float2 xb = add2(make_float2(x[e], x[e + 1]), dup2(bias));
+                float2 dt = p.softplus ? ssm::softplus2(xb) : xb;
+                float2 du = mul2(dt, make_float2(uv[e], uv[e + 1]));
+                // steps outside the chunk: no decay, no input
+                if (!(e0 + e >= lo && e0 + e < hi)) { dt.x = 0.f; du.x = 0.f; }
+                if (!(e0 + e + 1 >= lo && e0 + e + 1 < hi)) { dt.y = 0.f; du.y = 0.f; }
+                if constexpr (HEAD) dt = make_float2(ex2_approx(dt.x * ah), ex2_approx(dt.y * ah));
+                q[(e0 + e) * CW + c] = make_float2(dt.x, du.x);
+                q[(e0 + e + 1) * CW + c] = make_float2(dt.y, du.y);
+            }
+        }
+        __syncthreads();   // bc is complete; the warp's own q rows too
+
+        // the recurrence
+        for (int w = lo / WT; w * WT < hi; ++w) {
+            float yw[CPL * WT];
+#pragma unroll
+            for (int tt = 0; tt < WT; ++tt) {
+                const int t = w * WT + tt;
+                float2 bb[S / 2], cc[S / 2];
+                const float* br = bc + t * 2 * N + j * S;
+#pragma unroll
+                for (int s = 0; s < S / 2; s += 2) {
+                    const float4 v = *reinterpret_cast<const float4*>(br + 2 * s);
+                    bb[s] = make_float2(v.x, v.y);
+                    bb[s + 1] = make_float2(v.z, v.w);
+                    if constexpr (!LOCAL) {
+                        const float4 x = *reinterpret_cast<const float4*>(br + N + 2 * s);
+                        cc[s] = make_float2(x.x, x.y);
+                        cc[s + 1] = make_float2(x.z, x.w);
+                    }
+                }
+                const float4* qr = reinterpret_cast<const float4*>(q + t * CW + lg * CPL);
+#pragma unroll
+                for (int c2 = 0; c2 < CPL; c2 += 2) {
+                    const float4 qq = qr[c2 / 2];
+#pragma unroll
+                    for (int ch = 0; ch < 2; ++ch) {
+                        const int c = c2 + ch;
+                        const float dv = ch ? qq.z : qq.x;
+                        const float2 d2 = dup2(dv), du2 = dup2(ch ? qq.w : qq.y);
+                        float2 y2 = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int s = 0; s < S / 2; ++s) {
+                            float2 dA;
+                            if constexpr (HEAD) {
+                                dA = d2;
+                            } else {
+                                const float2 arg = mul2(d2, a2[c][s]);
+                                dA = make_float2(ex2_approx(arg.x), ex2_approx(arg.y));
+                            }
+                            h[c][s] = fma2(dA, h[c][s], mul2(du2, bb[s]));
+                            if constexpr (!LOCAL) y2 = fma2(cc[s], h[c][s], y2);
+                        }
+                        if constexpr (LOCAL) {
+                            if constexpr (HEAD) acc[c] *= dv;
+                            else acc[c] += dv;
+                        } else {
+                            yw[c * WT + tt] = y2.x + y2.y;
+                        }
+                    }
+                }
+            }
+            if constexpr (!LOCAL) {
+                // sum over the lanes of a channel; y takes the place of dt in q, which every lane
+                // of the channel has read before the shuffles
+                int off = 0;
+                constexpr int NV = CPL * WT;
+                if constexpr (TPC > 1) ssm::window_reduce<NV, TPC>(yw, j, off);
+                constexpr int KEPT = NV >= TPC ? NV / TPC : 1;
+                if (TPC <= NV || j % (TPC > NV ? TPC / NV : 1) == 0) {
+#pragma unroll
+                    for (int i = 0; i < KEPT; ++i) {
+                        const int c = (off + i) / WT, tt = (off + i) % WT;
+                        q[(w * WT + tt) * CW + lg * CPL + c].x = yw[i];
+                    }
+                }
+            }
+        }
+        if constexpr (!LOCAL) {
+            __syncwarp();
+            // epilogue: (y + D u) silu(z), staged in the delta rows (every warp is past reading them)
+#pragma unroll
+            for (int it = 0; it < Cf::ITEMS; ++it) {
+                const int idx = lane + 32 * it, c = idx % CW, e0 = idx / CW * PS;
+                const int lc = warp * CW + c;
+                const int64_t ro = (int64_t)lc * L * ESZ;
+                float uv[PS], zv[PS], o[PS];
+                read_row<T, ALIGNED, PS>(sb + (Cf::R_U + lc) * PITCH, (ALIGNED ? 0 : skew<T>(ub + ro)) + e0, uv);
+                if (zb) read_row<T, ALIGNED, PS>(sb + (Cf::R_Z + lc) * PITCH, (ALIGNED ? 0 : skew<T>(zb + ro)) + e0, zv);
+                const float2 D2 = dup2(s_D[lc]);
+#pragma unroll
+                for (int e = 0; e < PS; e += 2) {
+                    float2 y = fma2(D2, make_float2(uv[e], uv[e + 1]),
+                                    make_float2(q[(e0 + e) * CW + c].x, q[(e0 + e + 1) * CW + c].x));
+                    if (zb) y = mul2(y, ssm::silu2(make_float2(zv[e], zv[e + 1])));
+                    o[e] = y.x;
+                    o[e + 1] = y.y;
+                }
+                write_row<T, ALIGNED, PS>(sb + (Cf::R_DT + lc) * PITCH, (ALIGNED ? 0 : skew<T>(ob + ro)) + e0, o);
+            }
+            __syncwarp();
+            // to global memory, a row's pieces on neighbouring lanes
+            for (int i = lane; i < CW * Cf::PIECES; i += 32) {
+                const int r = i / Cf::PIECES, g = i % Cf::PIECES, lc = warp * CW + r;
+                if (lc >= tk.nch) continue;
+                unsigned char* row = ob + (int64_t)lc * L * ESZ;
+                const int e0 = g * V - (ALIGNED ? 0 : skew<T>(row));     // first step of the piece
+                const unsigned char* src = sb + (Cf::R_DT + lc) * PITCH + g * 16;
+                unsigned char* dst = row + (tb + e0) * ESZ;
+                if (e0 >= lo && e0 + V <= hi) {
+                    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+                } else {
+                    for (int e = 0; e < V; ++e)
+                        if (e0 + e >= lo && e0 + e < hi)
+                            *reinterpret_cast<T*>(dst + e * ESZ) = *reinterpret_cast<const T*>(src + e * ESZ);
+                }
+            }
+        }
+    }
+
+    // the state that leaves the chunk
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+        if (!ok[c]) continue;
+        const int64_t d = tk.d0 + warp * CW + lg * CPL + c;
+        if (!LOCAL && tk.last) {
+            float* hr = p.states + tk.slot * p.slot_stride + d * N + j * S;
+            if (p.state_vec) {
+#pragma unroll
+                for (int s = 0; s < S / 2; s += 2)
+                    *reinterpret_cast<float4*>(hr + 2 * s) = make_float4(h[c][s].x, h[c][s].y, h[c][s + 1].x, h[c][s + 1].y);
+            } else {
+#pragma unroll
+                for (int s = 0; s < S / 2; ++s) { hr[2 * s] = h[c][s].x; hr[2 * s + 1] = h[c][s].y; }
+            }
+        } else if (LOCAL || tk.k == 0) {
+            float* hr = p.ws_h + (tk.chunk_id * p.dim + d) * N + j * S;
+#pragma unroll
+            for (int s = 0; s < S / 2; ++s) __stcg(reinterpret_cast<float2*>(hr) + s, h[c][s]);
+            if (LOCAL && j == 0) __stcg(p.ws_p + tk.chunk_id * p.dim + d, acc[c]);
+        }
+    }
+}
+
+// Finds the sequence that holds chunk x (each sequence has ceil(length / chunk) chunks, at least
+// one).  Returns false behind the last chunk.  All threads of the CTA call it.
+__device__ __forceinline__ bool find_chunk(const PackedParams& p, int64_t x, int64_t* sh, int nt, int64_t& seq, int64_t& k) {
+    // sh: [0] sequence, [1] chunk, [2] chunks before, [4 ..] warp sums
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt / 32;
+    int64_t before = 0;
+    if (tid == 0) sh[0] = -1;
+    for (int64_t i0 = 0; i0 < p.n_seq; i0 += nt) {
+        const int64_t i = i0 + tid;
+        int64_t n = 0;
+        if (i < p.n_seq) {
+            const ssm::TokenRange r = ssm::token_range(p.cu, i, p.total);
+            n = r.hi > r.lo ? (r.hi - r.lo + p.chunk - 1) / p.chunk : 1;
+        }
+        int64_t inc = n;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, inc, m);
+            if (lane >= m) inc += v;
+        }
+        __syncthreads();
+        if (lane == 31) sh[4 + warp] = inc;
+        __syncthreads();
+        int64_t base = before, all = before;
+        for (int w = 0; w < nw; ++w) {
+            if (w < warp) base += sh[4 + w];
+            all += sh[4 + w];
+        }
+        if (n > 0 && x >= base + inc - n && x < base + inc) {
+            sh[0] = i;
+            sh[1] = x - (base + inc - n);
+        }
+        before = all;
+        if (x < all) break;
+    }
+    __syncthreads();
+    seq = sh[0];
+    k = sh[1];
+    return seq >= 0;
+}
+
+template <typename T, int N, bool HEAD, bool ALIGNED>
+__global__ void __launch_bounds__(PackedCfg<T, N, HEAD, ALIGNED>::NT)
+scan_packed_kernel(const PackedParams p) {
+    using Cf = PackedCfg<T, N, HEAD, ALIGNED>;
+    extern __shared__ __align__(16) unsigned char packed_smem[];
+    unsigned char* smem = packed_smem;
+    Task tk;
+    const int64_t x = blockIdx.x / p.n_tiles;
+    const unsigned tile = blockIdx.x % p.n_tiles;
+    tk.g = tile / p.tiles_per_group;
+    tk.ci0 = (int64_t)(tile % p.tiles_per_group) * Cf::CT;
+    tk.d0 = tk.g * p.group_dim + tk.ci0;
+    tk.nch = (int)(p.group_dim - tk.ci0 < Cf::CT ? p.group_dim - tk.ci0 : Cf::CT);
+    int64_t seq = x;
+    tk.k = 0;
+    tk.chunk_id = x;
+    if (p.chunk > 0 && !find_chunk(p, x, reinterpret_cast<int64_t*>(smem), Cf::NT, seq, tk.k)) return;
+    const ssm::TokenRange r = ssm::token_range(p.cu, seq, p.total);
+    tk.t0 = r.lo + tk.k * p.chunk;
+    tk.t1 = p.chunk > 0 && r.hi - tk.t0 > p.chunk ? tk.t0 + p.chunk : r.hi;
+    tk.last = tk.t1 == r.hi;
+    tk.slot = p.slots ? __ldg(p.slots + seq) : (int)seq;
+    tk.has = p.has_state && __ldg(p.has_state + seq) != 0;
+    const ssm::SlotKind kind = ssm::slot_kind((int)tk.slot, p.n_slots);
+    if (kind == ssm::kSlotPad) return;
+    if (kind == ssm::kSlotBad) {
+        if (p.phase == (tk.k > 0 ? 2 : 1)) {
+            const int64_t n = tk.t1 - tk.t0;
+            for (int64_t i = threadIdx.x; i < n * tk.nch; i += Cf::NT)
+                static_cast<T*>(p.out)[(tk.d0 + i / n) * p.total + tk.t0 + i % n] = T(__int_as_float(0x7FC00000));
+        }
+        return;
+    }
+    if (p.phase == 1) {
+        if (tk.k == 0) run_chunk<T, N, HEAD, ALIGNED, false>(p, tk, smem);
+        else if (!tk.last) run_chunk<T, N, HEAD, ALIGNED, true>(p, tk, smem);
+    } else if (tk.k > 0) {
+        run_chunk<T, N, HEAD, ALIGNED, false>(p, tk, smem);
+    }
+}
+
+template <typename T, int N, bool HEAD, bool ALIGNED>
+int launch(PackedParams& p, cudaStream_t s) {
+    using Cf = PackedCfg<T, N, HEAD, ALIGNED>;
+    p.tiles_per_group = (unsigned)((p.group_dim + Cf::CT - 1) / Cf::CT);
+    const int64_t tiles = p.ngroups * p.tiles_per_group;
+    const int64_t ctas = tiles * (p.chunk > 0 ? p.n_chunks : p.n_seq);
+    if (tiles > 0x7FFFFFFF || ctas > 0x7FFFFFFF) return SSM_ERR_UNSUPPORTED;
+    p.n_tiles = (unsigned)tiles;
+    auto* k = scan_packed_kernel<T, N, HEAD, ALIGNED>;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM) != cudaSuccess) return SSM_ERR_CUDA;
+    for (p.phase = 1; p.phase <= (p.chunk > 0 ? 2 : 1); ++p.phase) {
+        k<<<(unsigned)ctas, Cf::NT, Cf::SMEM, s>>>(p);
+        if (cudaGetLastError() != cudaSuccess) return SSM_ERR_CUDA;
+    }
+    return SSM_OK;
+}
+
+// One (dtype, dstate), in a translation unit of its own.
+template <typename T, int N>
+int launch_n(PackedParams& p, bool aligned, cudaStream_t s) {
+    const bool head = p.nheads != p.dim;
+    if (head) return aligned ? launch<T, N, true, true>(p, s) : launch<T, N, true, false>(p, s);
+    return aligned ? launch<T, N, false, true>(p, s) : launch<T, N, false, false>(p, s);
+}
+
+}  // namespace packed
+}  // namespace ssm

@@ -1,0 +1,229 @@
+"""Refusals of the slot and convolution-gradient operators, on the host before anything is launched, and the
+fp64 forms that the GPU tests compare with."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import oracle
+import slots_plain as sp
+
+A16 = 0x10000          # stand-in device addresses: 16-byte aligned,
+OFF1 = 0x10001         # and off every element's alignment
+
+
+@pytest.fixture(scope="module")
+def ssm():
+    import selective_state_space_30_b200 as m
+    from selective_state_space_30_b200 import build
+    build.build()
+    m.load_library()
+    return m
+
+
+def _raises(ssm, status, fn, *args):
+    assert fn(*args, check=False) == status, args
+
+
+def test_conv_packed_refusals(ssm):
+    ok = dict(dim=8, total=20, n_seq=2, width=4, io=ssm.SSM_BF16, x=A16, w=A16, bias=None, silu=True, cu=A16, slots=None,
+              has=None, states=A16, n_slots=3, stride=24, out=A16)
+
+    def rc(**kw):
+        a = dict(ok, **kw)
+        return ssm.ssm_causal_conv1d_packed_fwd(*a.values(), check=False)
+
+    inv, uns = ssm.SSM_ERR_INVALID_ARG, ssm.SSM_ERR_UNSUPPORTED
+    for bad in (dict(dim=0), dict(total=-1), dict(n_seq=-1), dict(io=7), dict(x=None), dict(w=None), dict(cu=None),
+                dict(states=None), dict(out=None), dict(n_slots=-1), dict(stride=23), dict(x=OFF1), dict(out=OFF1),
+                dict(states=OFF1), dict(total=2 ** 31), dict(n_seq=2 ** 31), dict(n_slots=2 ** 31)):
+        assert rc(**bad) == inv, bad
+    assert rc(width=0) == uns and rc(width=5) == uns
+    assert rc(n_seq=0, x=None, w=None, cu=None, states=None, out=None) == ssm.SSM_OK
+
+
+def test_conv_update_refusals(ssm):
+    ok = dict(batch=2, dim=8, width=4, io=ssm.SSM_F32, x=A16, w=A16, bias=None, silu=True, slots=None, states=A16, n_slots=3,
+              stride=24, out=A16)
+
+    def rc(**kw):
+        return ssm.ssm_causal_conv1d_update(*dict(ok, **kw).values(), check=False)
+
+    for bad in (dict(batch=-1), dict(dim=0), dict(io=2), dict(x=None), dict(w=None), dict(out=None), dict(states=None),
+                dict(n_slots=-1), dict(stride=0), dict(x=0x10002), dict(states=0x10002)):
+        assert rc(**bad) == ssm.SSM_ERR_INVALID_ARG, bad
+    assert rc(width=5) == ssm.SSM_ERR_UNSUPPORTED
+    assert rc(batch=0, x=None) == ssm.SSM_OK
+
+
+def test_scan_packed_refusals(ssm):
+    def dims(batch=2, dim=32, total=64, N=16, heads=0, groups=1, io=ssm.SSM_BF16):
+        return ssm.make_dims(batch, dim, total, N, heads, groups, io)
+
+    ok = dict(dims=dims(), u=A16, delta=A16, A=A16, B=A16, C=A16, D=None, z=None, bias=None, softplus=True, cu=A16, slots=None,
+              has=None, states=A16, n_slots=4, stride=512, longest=0, out=A16, ws=None, nws=0)
+
+    def rc(**kw):
+        return ssm.ssm_selective_scan_packed_fwd(*dict(ok, **kw).values(), check=False)
+
+    for bad in (dict(u=None), dict(delta=None), dict(A=None), dict(B=None), dict(C=None), dict(cu=None), dict(states=None),
+                dict(out=None), dict(stride=511), dict(n_slots=-1), dict(u=OFF1), dict(z=OFF1), dict(out=OFF1),
+                dict(dims=dims(heads=5)), dict(dims=dims(groups=3)), dict(dims=dims(batch=-1)), dict(dims=dims(io=4)),
+                dict(dims=dims(total=2 ** 31))):
+        assert rc(**bad) == ssm.SSM_ERR_INVALID_ARG, bad
+    assert rc(dims=dims(N=24)) == ssm.SSM_ERR_UNSUPPORTED
+    assert rc(dims=dims(batch=0), u=None, A=None, cu=None) == ssm.SSM_OK
+    # a workspace where sequences are cut, and only there
+    size = ssm.ssm_selective_scan_packed_workspace_size
+    long = dims(batch=1, total=4096)
+    need = size(long)
+    assert need >= 4096 // 512 * 32 * 17 * 4
+    assert size(long, 200) == 0 and size(dims()) == 0 and size(long, 4096) == need
+    assert rc(dims=long) == ssm.SSM_ERR_INVALID_ARG
+    assert rc(dims=long, ws=A16, nws=need - 1) == ssm.SSM_ERR_INVALID_ARG
+    assert rc(dims=long, ws=A16 + 4, nws=need) == ssm.SSM_ERR_INVALID_ARG
+    assert size(dims(N=24), check=False) == -ssm.SSM_ERR_UNSUPPORTED
+    assert ssm.load_library().ssm_selective_scan_packed_workspace_size(ctypes.byref(long), 0, None) == ssm.SSM_ERR_INVALID_ARG
+
+
+def test_state_update_slots_refusals(ssm):
+    def dims(batch=2, dim=32, L=1, N=16, heads=0, groups=1, io=ssm.SSM_BF16):
+        return ssm.make_dims(batch, dim, L, N, heads, groups, io)
+
+    ok = dict(dims=dims(), states=A16, slots=None, n_slots=4, stride=512, u=A16, delta=A16, A=A16, B=A16, C=A16, D=None, z=None,
+              bias=None, softplus=True, out=A16)
+
+    def rc(**kw):
+        return ssm.ssm_selective_state_update_slots(*dict(ok, **kw).values(), check=False)
+
+    for bad in (dict(states=None), dict(u=None), dict(delta=None), dict(A=None), dict(B=None), dict(C=None), dict(out=None),
+                dict(stride=508), dict(dims=dims(L=2)), dict(dims=dims(heads=5)), dict(n_slots=-1), dict(u=OFF1)):
+        assert rc(**bad) == ssm.SSM_ERR_INVALID_ARG, bad
+    for bad in (dict(dims=dims(N=24)), dict(states=A16 + 4), dict(stride=514), dict(B=A16 + 4), dict(C=A16 + 2),
+                dict(A=A16 + 4)):
+        assert rc(**bad) == ssm.SSM_ERR_UNSUPPORTED, bad
+    assert rc(dims=dims(batch=0), u=None) == ssm.SSM_OK
+
+
+def test_slots_copy_refusals(ssm):
+    ok = dict(pool=A16, layers=2, n_slots=4, slot_bytes=64, slot_stride=64, layer_stride=256, src=A16, dst=A16, n=3)
+
+    def rc(**kw):
+        return ssm.ssm_state_slots_copy(*dict(ok, **kw).values(), check=False)
+
+    for bad in (dict(pool=None), dict(src=None), dict(dst=None), dict(layers=-1), dict(n_slots=-1), dict(slot_bytes=-1),
+                dict(n=-1), dict(slot_stride=63), dict(layer_stride=255), dict(layer_stride=-256),
+                dict(layer_stride=64), dict(slot_stride=2 ** 45), dict(n_slots=2 ** 31)):
+        assert rc(**bad) == ssm.SSM_ERR_INVALID_ARG, bad
+    assert rc(n=4097) == ssm.SSM_ERR_UNSUPPORTED
+    for empty in (dict(n=0), dict(layers=0), dict(slot_bytes=0), dict(n_slots=0)):
+        assert rc(pool=None, **empty) == ssm.SSM_OK
+
+
+def test_conv_bwd_refusals(ssm):
+    size = ssm.ssm_causal_conv1d_bwd_workspace_size
+    need = size(2, 8, 30, 4, ssm.SSM_BF16)
+    assert need >= 2 * 8 * 5 * 4 and size(2, 8, 0, 4, ssm.SSM_BF16) == 0
+    ok = dict(batch=2, dim=8, L=30, width=4, io=ssm.SSM_BF16, x=A16, w=A16, bias=None, silu=True, dout=A16, dx=A16, dw=A16,
+              db=None, ws=A16, nws=need)
+
+    def rc(**kw):
+        return ssm.ssm_causal_conv1d_bwd(*dict(ok, **kw).values(), check=False)
+
+    for bad in (dict(x=None), dict(w=None), dict(dout=None), dict(dx=None), dict(dw=None), dict(ws=None), dict(nws=need - 1),
+                dict(batch=-1), dict(dim=0), dict(L=-1), dict(io=3), dict(x=OFF1), dict(dout=OFF1), dict(dx=OFF1)):
+        assert rc(**bad) == ssm.SSM_ERR_INVALID_ARG, bad
+    assert rc(width=5) == ssm.SSM_ERR_UNSUPPORTED and rc(width=0) == ssm.SSM_ERR_UNSUPPORTED
+    lib = ssm.load_library()
+    assert lib.ssm_causal_conv1d_bwd_workspace_size(1, 1, 1, 4, 0, None) == ssm.SSM_ERR_INVALID_ARG
+
+
+def test_front_end_refusals(ssm):
+    """Tensors that are no CUDA tensors, of other shapes or types: refused before the library is called."""
+    import torch
+    z = torch.zeros
+    with pytest.raises(ValueError, match="CUDA"):
+        ssm.causal_conv1d_packed(z(4, 8), z(4, 4), z(2, dtype=torch.int32), z(1, 4, 3))
+    with pytest.raises(ValueError, match="CUDA"):
+        ssm.causal_conv1d_update(z(2, 4), z(4, 4), z(2, 4, 3))
+    with pytest.raises(ValueError, match="dimensions"):
+        ssm.causal_conv1d_update(z(2, 4, 1), z(4, 4), z(2, 4, 3))
+    with pytest.raises(ValueError, match="CUDA"):
+        ssm.selective_scan_packed(z(4, 8), z(4, 8), z(4, 16), z(1, 16, 8), z(1, 16, 8), z(2, dtype=torch.int32), z(1, 4, 16))
+    with pytest.raises(ValueError, match="CUDA"):
+        ssm.selective_state_update_slots(z(1, 4, 16), z(1, 4), z(1, 4), z(4, 16), z(1, 1, 16), z(1, 1, 16))
+    with pytest.raises(ValueError, match="CUDA"):
+        ssm.state_slots_copy(z(2, 4), z(1, dtype=torch.int32), z(1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="CUDA"):
+        ssm.causal_conv1d_bwd(z(1, 4, 8), z(4, 4), z(1, 4, 8))
+    with pytest.raises(ValueError, match="CUDA"):
+        ssm.causal_conv1d_fn(z(1, 4, 8), z(4, 4))
+
+
+def test_tensor_checks():
+    import torch
+    from selective_state_space_30_b200._tensors import inner_contiguous, io_code, need, need_pool
+    t = torch.zeros(4, 6)
+    need("t", None, torch.float32, (1,), t.device)
+    need("t", t, torch.float32, (4, 6), t.device)
+    for args, word in (((torch.float64, (4, 6)), "float64"), ((torch.float32, (6, 4)), "shape")):
+        with pytest.raises(ValueError, match=word):
+            need("t", t, *args, t.device)
+    with pytest.raises(ValueError, match="contiguous"):
+        need("t", t.t(), torch.float32, (6, 4), t.device)
+    with pytest.raises(ValueError, match="on meta"):
+        need("t", t, torch.float32, (4, 6), torch.device("meta"))
+    with pytest.raises(ValueError):
+        io_code(t.double())
+    pool = torch.zeros(5, 4, 10)[:, :, :6]
+    with pytest.raises(ValueError, match="slot of p"):
+        need_pool("p", pool, torch.float32, (4, 6), t.device)
+    apart = torch.zeros(5, 40)[:, :24].view(5, 4, 6)
+    need_pool("p", apart, torch.float32, (4, 6), t.device)
+    assert inner_contiguous(torch.zeros(3, 5, 4).transpose(0, 1), 2) and not inner_contiguous(pool, 1)
+
+
+# ------------------------------------------------- the fp64 forms against the oracle
+
+def test_plain_scan_is_the_oracles():
+    """A packed scan is the batch oracle run per sequence, from the slot's state."""
+    rng = np.random.default_rng(4)
+    dim, N, G = 6, 8, 2
+    lens = [5, 0, 9]
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    T = int(cu[-1])
+    n = lambda *s: rng.standard_normal(s).astype(np.float32)  # noqa: E731
+    p = dict(u=n(dim, T), delta=n(dim, T), A=-np.abs(n(dim, N)), B=n(G, N, T), C=n(G, N, T), D=n(dim), z=n(dim, T),
+             delta_bias=n(dim), softplus=True)
+    pool = n(3, dim, N)
+    slots, has = [2, 0, 1], [1, 1, 0]
+    bounds = list(zip(cu[:-1].tolist(), cu[1:].tolist()))
+    f = {k: v.astype(np.float64) if isinstance(v, np.ndarray) else v for k, v in p.items()}
+    out, err, got_pool, _ = sp.scan_packed(f, bounds, slots, has, pool.astype(np.float64), np.zeros((dim, T)))
+    import ssm_inputs as si
+    for (lo, hi), s, h in zip(bounds, slots, has):
+        if hi == lo:
+            assert np.array_equal(got_pool[s], pool[s])
+            continue
+        d = si.Dims(1, dim, hi - lo, N, ngroups=G, dtype="f32")
+        cut = {k: np.ascontiguousarray(p[k][..., lo:hi])[None] for k in ("u", "delta", "B", "C", "z")}
+        o, last, _ = oracle.run_inputs(d, dict(p, **cut), h0=pool[s][None] if h else None)
+        assert np.allclose(out[:, lo:hi], o[0], rtol=1e-12, atol=1e-13)
+        assert np.allclose(got_pool[s], last[0], rtol=1e-12, atol=1e-13)
+    assert np.all(err > 0) and err.max() < 1e-4
+
+
+def test_plain_conv_is_the_oracles():
+    rng = np.random.default_rng(5)
+    x, w, b = rng.standard_normal((3, 20)), rng.standard_normal((3, 4)), rng.standard_normal(3)
+    x, w, b = (t.astype(np.float32) for t in (x, w, b))
+    out, err, pool = sp.conv_packed(x.astype(np.float64), w.astype(np.float64), b.astype(np.float64), True, [(0, 20)], [0], [0],
+                                    np.zeros((1, 3, 3)), np.zeros((3, 20)))
+    assert np.allclose(out, oracle.causal_conv1d(x[None], w, b, silu=True)[0], rtol=1e-12, atol=1e-14)
+    assert np.array_equal(pool[0], x[:, -3:])
+    # two halves from the kept inputs
+    o2, _, p2 = sp.conv_packed(x.astype(np.float64), w.astype(np.float64), b.astype(np.float64), True, [(0, 2)], [0], [0],
+                               np.zeros((1, 3, 3)), np.zeros((3, 20)))
+    o3, _, p3 = sp.conv_packed(x[:, 2:].astype(np.float64), w.astype(np.float64), b.astype(np.float64), True, [(0, 18)], [0], [1],
+                               p2, np.zeros((3, 18)))
+    assert np.allclose(np.concatenate([o2[:, :2], o3], 1), out, rtol=1e-13, atol=1e-15) and np.array_equal(p3, pool)

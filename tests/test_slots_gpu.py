@@ -1,0 +1,648 @@
+"""The operators on packed prompts and state slots against their fp64 forms (needs a B200).
+
+Tolerances are the running error bounds of tests/slots_plain.py.  Inputs are normals in the I/O type;
+untouched places of outputs and pools hold a pattern that has to survive.
+"""
+import numpy as np
+import pytest
+import torch
+
+import slots_plain as sp
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ssm():
+    import selective_state_space_30_b200 as m
+    return m
+
+
+IO = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def rnd(gen, *shape, dtype="f32", scale=1.0):
+    return (scale * torch.randn(*shape, generator=gen)).to(IO[dtype]).cuda()
+
+
+def unaligned(t):
+    """The same values one element off the allocation's alignment."""
+    buf = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    v = buf[1:].view(t.shape)
+    v.copy_(t)
+    return v
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def packing(lens, head=0, tail=0):
+    cu = np.concatenate([[0], np.cumsum(lens)]) + head
+    return cu.astype(np.int64), int(cu[-1] + tail), list(zip(cu[:-1].tolist(), cu[1:].tolist()))
+
+
+def gapped_pool(gen, n_slots, dim, last, dtype, gap):
+    """A pool (n_slots, dim, last) whose slots lie `gap` elements apart, and the whole buffer."""
+    buf = rnd(gen, n_slots, dim * last + gap, dtype=dtype)
+    return buf[:, :dim * last].view(n_slots, dim, last) if gap == 0 else \
+        torch.as_strided(buf, (n_slots, dim, last), (dim * last + gap, last, 1)), buf
+
+
+# ------------------------------------------------------------------ the convolution
+
+CONV = [
+    # lens, dim, width, dtype, silu, bias, head, tail, gap, shift bases
+    ([5, 1, 17, 0, 64, 3], 40, 4, "bf16", True, True, 0, 0, 0, False),     # 90 tokens: rows off the 16-byte grid
+    ([8, 8, 16, 32], 16, 4, "bf16", True, True, 0, 0, 0, False),           # aligned rows
+    ([1], 24, 4, "bf16", True, True, 0, 0, 0, False),
+    ([1, 1, 1, 1, 2, 2, 3], 33, 4, "f32", True, False, 0, 5, 3, False),
+    ([0, 0, 7, 0], 8, 3, "f32", False, True, 3, 6, 0, False),
+    ([700, 3, 1300, 21], 70, 4, "bf16", True, True, 2, 7, 8, False),       # several time tiles
+    ([2100], 9, 2, "f32", True, True, 0, 0, 0, True),
+    ([40, 55], 12, 4, "bf16", True, True, 1, 0, 0, True),
+    ([40, 56], 12, 1, "bf16", True, True, 0, 0, 0, False),                 # no history at all
+    ([3, 4, 5] * 40, 300, 4, "bf16", True, True, 0, 0, 0, False),          # many short prompts
+]
+
+
+def _conv_case(case, seed=7):
+    lens, dim, width, dtype, silu, bias, head, tail, gap, shift = case
+    gen = torch.Generator().manual_seed(seed)
+    cu, total, bounds = packing(lens, head, tail)
+    n = len(lens)
+    x = rnd(gen, dim, total, dtype=dtype)
+    w = rnd(gen, dim, width, scale=0.5)
+    b = rnd(gen, dim, scale=0.3) if bias else None
+    pool, buf = gapped_pool(gen, n + 3, dim, width - 1, dtype, gap)
+    out = rnd(gen, dim, total, dtype=dtype)
+    if shift:
+        x, out = unaligned(x), unaligned(out)
+    rng = np.random.default_rng(seed)
+    slots = rng.permutation(n + 3)[:n].tolist()
+    has = rng.integers(0, 2, n).tolist()
+    return x, w, b, pool, buf, out, cu, bounds, slots, has, silu, dtype
+
+
+@pytest.mark.parametrize("case", CONV, ids=range(len(CONV)))
+def test_conv_packed(ssm, case):
+    x, w, b, pool, buf, out, cu, bounds, slots, has, silu, dtype = _conv_case(case)
+    before = f64(buf)
+    ref, err, ref_pool = sp.conv_packed(f64(x), f64(w), f64(b) if b is not None else np.zeros(w.shape[0]), silu, bounds,
+                                        slots, has, f64(pool), f64(out))
+    # tokens of no sequence are not read: NaN there changes nothing
+    x[:, :bounds[0][0]] = float("nan")
+    x[:, bounds[-1][1]:] = float("nan")
+    got = ssm.causal_conv1d_packed(x, w, i32(cu), pool, slots=i32(slots), has_state=torch.tensor(has, dtype=torch.uint8).cuda(),
+                                   bias=b, silu=silu, out=out)
+    assert got is out
+    sp.check(f64(got), ref, err, dtype, "out")
+    assert np.array_equal(f64(pool), ref_pool), "the kept inputs are copies"
+    after = f64(buf)
+    gap = buf.shape[1] - pool.shape[1] * pool.shape[2]
+    if gap:
+        assert np.array_equal(after[:, -gap:], before[:, -gap:])
+
+
+def test_conv_packed_padding_and_bad_slots(ssm):
+    case = ([6, 9, 2, 30, 4], 20, 4, "bf16", True, True, 0, 3, 0, False)
+    x, w, b, pool, buf, out, cu, bounds, slots, has, silu, dtype = _conv_case(case)
+    has = [1] * 5
+    slots[1], slots[3], slots[4] = -1, len(pool), 2 ** 31 - 1
+    ref, err, ref_pool = sp.conv_packed(f64(x), f64(w), f64(b), silu, bounds, slots, has, f64(pool), f64(out))
+    got = ssm.causal_conv1d_packed(x, w, i32(cu), pool, slots=i32(slots), has_state=torch.ones(5, dtype=torch.bool).cuda(),
+                                   bias=b, silu=silu, out=out)
+    sp.check(f64(got), ref, err, dtype, "out")
+    assert np.array_equal(f64(pool), ref_pool)
+
+
+def test_conv_packed_defaults(ssm):
+    """No slots (slot i for i), no flags (from zero), an output of the call's own (zeros where no token is)."""
+    gen = torch.Generator().manual_seed(3)
+    x, w, pool = rnd(gen, 16, 40, dtype="bf16"), rnd(gen, 16, 4), rnd(gen, 2, 16, 3, dtype="bf16")
+    bounds = [(0, 11), (11, 32)]
+    ref, err, ref_pool = sp.conv_packed(f64(x), f64(w), np.zeros(16), True, bounds, [0, 1], [0, 0], f64(pool), np.zeros((16, 40)))
+    got = ssm.causal_conv1d_packed(x, w, i32([0, 11, 32]), pool)
+    sp.check(f64(got), ref, err, "bf16", "out")
+    assert np.array_equal(f64(pool), ref_pool)
+
+
+@pytest.mark.parametrize("dim,batch,width,dtype,gap", [
+    (1536, 4, 4, "bf16", 0), (40, 7, 4, "bf16", 8), (33, 5, 4, "bf16", 0), (64, 3, 3, "f32", 4), (20, 9, 2, "f32", 1),
+    (24, 3, 1, "bf16", 0), (5, 1, 4, "f32", 0), (200, 130, 4, "bf16", 5)])
+@pytest.mark.parametrize("silu", [True, False])
+def test_conv_update(ssm, dim, batch, width, dtype, gap, silu):
+    gen = torch.Generator().manual_seed(11)
+    x, w, b = rnd(gen, batch, dim, dtype=dtype), rnd(gen, dim, width, scale=0.5), rnd(gen, dim, scale=0.3)
+    pool, buf = gapped_pool(gen, batch + 4, dim, width - 1, dtype, gap)
+    out = rnd(gen, batch, dim, dtype=dtype)
+    slots = np.random.default_rng(1).permutation(batch + 4)[:batch].tolist()
+    if batch > 3:
+        slots[1], slots[2] = -7, batch + 4
+    xs, old, ref = f64(x), f64(pool), f64(out)
+    err, ref_pool = np.zeros_like(ref), old.copy()
+    for r, s in enumerate(slots):
+        if 0 <= s < len(old):
+            taps = np.concatenate([old[s], xs[r][:, None]], 1)
+            ref[r], err[r] = sp.conv_token(taps, f64(w), f64(b), silu)
+            ref_pool[s] = taps[:, 1:]
+        elif s >= 0:
+            ref[r] = np.nan
+    before = f64(buf)
+    got = ssm.causal_conv1d_update(x, w, pool, slots=i32(slots), bias=b, silu=silu, out=out)
+    sp.check(f64(got), ref, err, dtype, "out")
+    assert np.array_equal(f64(pool), ref_pool)
+    if gap:
+        assert np.array_equal(f64(buf)[:, -gap:], before[:, -gap:])
+
+
+# ------------------------------------------------------------------------ the scan
+
+def _scan_inputs(gen, rows, dim, heads, groups, N, dtype, prompts=True, z=True, D=True, bias=True, softplus=True):
+    # `rows`: packed tokens (time last) or token rows (first)
+    shape = (lambda *s: (*s, rows)) if prompts else (lambda *s: (rows, *s))
+    p = dict(u=rnd(gen, *shape(dim), dtype=dtype), delta=rnd(gen, *shape(heads), dtype=dtype, scale=0.7),
+             B=rnd(gen, *shape(groups, N), dtype=dtype), C=rnd(gen, *shape(groups, N), dtype=dtype),
+             z=rnd(gen, *shape(dim), dtype=dtype) if z else None, D=rnd(gen, dim) if D else None,
+             delta_bias=rnd(gen, heads, scale=0.5) - 2.0 if bias else None, softplus=softplus)
+    if heads == dim:
+        p["A"] = -(torch.rand(dim, N, generator=gen) * 8 + 0.1).cuda()
+    else:
+        p["A"] = -(torch.rand(heads, generator=gen) * 8 + 0.1).cuda()
+    if not softplus:
+        # dt itself: not negative
+        p["delta"] = p["delta"].abs()
+        p["delta_bias"] = p["delta_bias"].abs() if bias else None
+    return p
+
+
+def _plain(p):
+    return {k: f64(v) if isinstance(v, torch.Tensor) else v for k, v in p.items()}
+
+
+def _call(ssm, p, cu, states, out, **kw):
+    return ssm.selective_scan_packed(p["u"], p["delta"], p["A"], p["B"], p["C"], cu, states, D=p["D"], z=p["z"],
+                                     delta_bias=p["delta_bias"], softplus=p["softplus"], out=out, **kw)
+
+
+def _chunk(ssm, p, n_seq, max_seqlen=0):
+    """Whether the call cuts sequences: the workspace says so."""
+    io = ssm.SSM_BF16 if p["u"].dtype == torch.bfloat16 else ssm.SSM_F32
+    d = ssm.make_dims(n_seq, p["u"].shape[0], p["u"].shape[1], p["B"].shape[1], p["delta"].shape[0], p["B"].shape[0], io)
+    return ssm.ssm_selective_scan_packed_workspace_size(d, max_seqlen)
+
+
+SCAN = [
+    # lens, dim, heads, groups, N, dtype, head, tail, gap, shift, kw
+    ([64, 32, 96], 64, 64, 1, 16, "bf16", 0, 0, 0, False, {}),                       # aligned rows
+    ([5, 1, 17, 0, 44], 40, 40, 1, 16, "bf16", 0, 0, 0, False, {}),                  # 67 tokens
+    ([1], 16, 16, 1, 16, "f32", 0, 0, 0, False, {}),
+    ([33, 40, 7], 130, 130, 1, 16, "f32", 3, 5, 4, False, {}),                       # a ragged second tile
+    ([21, 3], 24, 24, 2, 8, "bf16", 0, 0, 0, False, dict(z=False)),
+    ([21, 30], 300, 300, 1, 8, "f32", 0, 1, 2, False, dict(D=False, bias=False)),
+    ([50, 2, 30], 72, 72, 3, 32, "bf16", 0, 6, 0, True, {}),
+    ([31, 64], 40, 40, 1, 64, "bf16", 1, 0, 0, False, dict(z=False, D=False)),
+    ([19, 40], 36, 36, 2, 128, "f32", 0, 0, 0, False, {}),
+    ([40, 24, 72], 128, 2, 1, 128, "bf16", 0, 0, 0, False, {}),                      # heads
+    ([13, 50], 96, 6, 2, 128, "bf16", 0, 2, 0, False, {}),                           # heads and groups, 65 tokens
+    ([13, 50], 33, 11, 1, 64, "f32", 0, 0, 0, True, dict(z=False)),                  # heads of three channels
+    ([20, 9, 3], 48, 3, 1, 16, "bf16", 0, 0, 0, False, {}),
+    ([20, 9, 3], 64, 4, 1, 32, "f32", 0, 0, 0, False, dict(softplus=False)),
+    ([25, 39], 64, 4, 2, 8, "bf16", 0, 0, 0, False, {}),
+    ([20, 12], 32, 32, 1, 16, "bf16", 0, 0, 0, False, dict(softplus=False, bias=False)),
+    ([2, 3, 1] * 30, 50, 50, 1, 16, "bf16", 0, 0, 0, False, {}),                     # many short prompts
+]
+
+
+@pytest.mark.parametrize("case", SCAN, ids=range(len(SCAN)))
+def test_scan_packed(ssm, case):
+    lens, dim, heads, groups, N, dtype, head, tail, gap, shift, kw = case
+    gen = torch.Generator().manual_seed(21)
+    cu, total, bounds = packing(lens, head, tail)
+    n = len(lens)
+    p = _scan_inputs(gen, total, dim, heads, groups, N, dtype, **kw)
+    states, buf = gapped_pool(gen, n + 2, dim, N, "f32", gap)
+    out = rnd(gen, dim, total, dtype=dtype)
+    if shift:
+        p = {k: unaligned(v) if k in ("u", "delta", "B", "C", "z") and v is not None else v for k, v in p.items()}
+        out = unaligned(out)
+    rng = np.random.default_rng(2)
+    slots, has = rng.permutation(n + 2)[:n].tolist(), rng.integers(0, 2, n).tolist()
+    ref, err, ref_pool, pool_err = sp.scan_packed(_plain(p), bounds, slots, has, f64(states), f64(out))
+    for k in ("u", "delta", "B", "C", "z"):
+        if p[k] is not None:
+            p[k][..., :head] = float("nan")
+            p[k][..., bounds[-1][1]:] = float("nan")
+    before = f64(buf)
+    flags = torch.tensor(has, dtype=torch.uint8).cuda()
+    got = _call(ssm, p, i32(cu), states, out, slots=i32(slots), has_state=flags, max_seqlen=max(lens))
+    sp.check(f64(got), ref, err, dtype, "out")
+    sp.check(f64(states), ref_pool, pool_err, "f32", "states")
+    if gap:
+        assert np.array_equal(f64(buf)[:, -gap:], before[:, -gap:])
+
+
+CUT = [
+    # lens, dim, heads, groups, N, dtype, tail
+    ([1500], 32, 32, 1, 16, "bf16", 4),
+    ([1501], 48, 48, 1, 16, "f32", 0),
+    ([300, 900, 1, 0, 129, 128, 640], 36, 36, 2, 16, "bf16", 0),      # cut and uncut sequences, whole chunks
+    ([1203], 32, 2, 1, 128, "bf16", 1),
+    ([700, 90], 24, 24, 1, 8, "f32", 0),
+    ([40, 800], 20, 20, 1, 32, "bf16", 0),
+    ([640, 333], 16, 16, 1, 64, "f32", 0),
+]
+
+
+@pytest.mark.parametrize("case", CUT, ids=range(len(CUT)))
+def test_scan_packed_cut_sequences(ssm, case):
+    """Few long sequences: chunks that run at the same time and join their states."""
+    lens, dim, heads, groups, N, dtype, tail = case
+    gen = torch.Generator().manual_seed(22)
+    cu, total, bounds = packing(lens, 0, tail)
+    n = len(lens)
+    p = _scan_inputs(gen, total, dim, heads, groups, N, dtype)
+    assert _chunk(ssm, p, n, max(lens)) > 0, "this case is here for the cut path"
+    states, out = rnd(gen, n, dim, N), rnd(gen, dim, total, dtype=dtype)
+    has = [(i + 1) % 2 for i in range(n)]
+    # chunks of at most 2 * 128 tokens at these sizes; the bound takes the longest, at every 32nd token's worth
+    ref, err, ref_pool, pool_err = sp.scan_packed(_plain(p), bounds, list(range(n)), has, f64(states), f64(out), chunk=128)
+    flags = torch.tensor(has, dtype=torch.bool).cuda()
+    start = states.clone()
+    got = _call(ssm, p, i32(cu), states, out, has_state=flags, max_seqlen=max(lens))
+    sp.check(f64(got), ref, err, dtype, "out")
+    sp.check(f64(states), ref_pool, pool_err, "f32", "states")
+    # the same bits again
+    again, out2 = start.clone(), out.clone()
+    _call(ssm, p, i32(cu), again, out2, has_state=flags, max_seqlen=max(lens))
+    assert torch.equal(again, states) and torch.equal(out2, out)
+
+
+def test_scan_packed_hint_is_only_a_hint(ssm):
+    """A max_seqlen that is too small, zero or too large: right results all the same."""
+    gen = torch.Generator().manual_seed(23)
+    lens = [700, 30]
+    cu, total, bounds = packing(lens)
+    p = _scan_inputs(gen, total, 24, 24, 1, 16, "f32")
+    states = rnd(gen, 2, 24, 16)
+    out = rnd(gen, 24, total)
+    ref, err, ref_pool, pool_err = sp.scan_packed(_plain(p), bounds, [0, 1], [1, 1], f64(states), f64(out), chunk=128)
+    flags = torch.ones(2, dtype=torch.uint8).cuda()
+    for hint in (0, 1, 30, 700, 10 ** 9):
+        s = states.clone()
+        got = _call(ssm, p, i32(cu), s, None, has_state=flags, max_seqlen=hint)
+        sp.check(f64(got), ref, err, "f32", "out")
+        sp.check(f64(s), ref_pool, pool_err, "f32", "states")
+
+
+@pytest.mark.parametrize("long", [False, True])
+def test_scan_packed_padding_and_bad_slots(ssm, long):
+    gen = torch.Generator().manual_seed(24)
+    lens = [900, 20, 1000, 30, 7] if long else [9, 20, 4, 30, 7]
+    cu, total, bounds = packing(lens, 0, 2)
+    p = _scan_inputs(gen, total, 32, 32, 1, 16, "bf16")
+    assert (_chunk(ssm, p, 5, max(lens)) > 0) == long
+    states, out = rnd(gen, 4, 32, 16), rnd(gen, 32, total, dtype="bf16")
+    slots, has = [4, 1, -1, 2 ** 31 - 1, 0], [1] * 5
+    ref, err, ref_pool, pool_err = sp.scan_packed(_plain(p), bounds, slots, has, f64(states), f64(out), chunk=128 if long else 0)
+    got = _call(ssm, p, i32(cu), states, out, slots=i32(slots), has_state=torch.ones(5, dtype=torch.uint8).cuda(),
+                max_seqlen=max(lens))
+    sp.check(f64(got), ref, err, "bf16", "out")
+    sp.check(f64(states), ref_pool, pool_err, "f32", "states")
+
+
+def test_scan_packed_neighbours_do_not_meet(ssm):
+    """NaN and infinities in one sequence stay there, in aligned and unaligned rows, cut or not."""
+    for lens in ([30, 34, 64], [30, 33, 20], [400, 301, 800]):
+        gen = torch.Generator().manual_seed(25)
+        cu, total, bounds = packing(lens)
+        p = _scan_inputs(gen, total, 16, 16, 1, 16, "bf16")
+        states = rnd(gen, 3, 16, 16)
+        ref, err, ref_pool, pool_err = sp.scan_packed(_plain(p), bounds, [0, 1, 2], [0] * 3, f64(states), np.zeros((16, total)),
+                                                      chunk=128)
+        lo, hi = bounds[1]
+        for k, bad in (("u", float("inf")), ("B", float("nan")), ("C", float("nan")), ("z", float("nan")), ("delta", 1e30)):
+            p[k][..., lo:hi] = bad
+        got = f64(_call(ssm, p, i32(cu), states, None))
+        for i in (0, 2):
+            a, b = bounds[i]
+            sp.check(got[:, a:b], ref[:, a:b], err[:, a:b], "bf16", "out")
+            sp.check(f64(states)[i], ref_pool[i], pool_err[i], "f32", "states")
+
+
+@pytest.mark.parametrize("case", [
+    # dim, heads, groups, N, batch, dtype, gap, kw
+    (64, 64, 1, 16, 3, "bf16", 0, {}), (70, 70, 1, 16, 5, "f32", 4, {}), (48, 48, 2, 8, 4, "bf16", 8, dict(z=False)),
+    (40, 40, 1, 32, 6, "f32", 0, dict(D=False, bias=False)), (24, 24, 3, 64, 2, "bf16", 0, {}),
+    (36, 36, 1, 128, 5, "f32", 0, {}), (128, 2, 1, 128, 5, "bf16", 0, {}), (96, 6, 2, 64, 7, "bf16", 0, {}),
+    (33, 11, 1, 16, 5, "f32", 12, dict(softplus=False)), (1536, 1536, 1, 16, 300, "bf16", 0, {}),
+], ids=str)
+def test_state_update_slots(ssm, case):
+    dim, heads, groups, N, batch, dtype, gap, kw = case
+    gen = torch.Generator().manual_seed(31)
+    p = _scan_inputs(gen, batch, dim, heads, groups, N, dtype, prompts=False, **kw)
+    states, buf = gapped_pool(gen, batch + 3, dim, N, "f32", gap)
+    out = rnd(gen, batch, dim, dtype=dtype)
+    slots = np.random.default_rng(3).permutation(batch + 3)[:batch].tolist()
+    if batch > 3:
+        slots[0], slots[2] = -1, batch + 3
+    ref, err, ref_pool, pool_err = sp.scan_tokens(_plain(p), slots, f64(states), f64(out))
+    before = f64(buf)
+    got = ssm.selective_state_update_slots(states, p["u"], p["delta"], p["A"], p["B"], p["C"], slots=i32(slots), D=p["D"],
+                                           z=p["z"], delta_bias=p["delta_bias"], softplus=p["softplus"], out=out)
+    sp.check(f64(got), ref, err, dtype, "out")
+    sp.check(f64(states), ref_pool, pool_err, "f32", "states")
+    if gap:
+        assert np.array_equal(f64(buf)[:, -gap:], before[:, -gap:])
+
+
+# ----------------------------------------------------------------------- the slots
+
+@pytest.mark.parametrize("shape,slot_dim,dtype,view", [
+    ((6, 40), 0, torch.float32, None), ((6, 5, 33), 0, torch.bfloat16, None), ((3, 9, 7, 3), 1, torch.bfloat16, None),
+    ((2, 70, 4096 + 24), 1, torch.float32, None), ((2, 9, 5000), 1, torch.uint8, None), ((8, 1), 0, torch.uint8, None),
+    ((4, 9, 24, 16), 1, torch.float32, "gap"), ((9, 4, 50), 1, torch.bfloat16, "inner"),
+    ((1, 9, 12289), 1, torch.bfloat16, "shift")], ids=str)
+def test_slots_copy(ssm, shape, slot_dim, dtype, view):
+    gen = torch.Generator().manual_seed(41)
+    pool = torch.randint(0, 255, shape, generator=gen, dtype=torch.uint8).cuda().to(dtype)
+    whole = pool
+    if view == "gap":          # one of two tensors' worth per slot
+        whole = torch.randn(*shape[:-1], 2 * shape[-1], generator=gen).cuda()
+        whole = whole.view(shape[0], shape[1], 2, -1)
+        pool = whole[:, :, 0].view(shape)
+    elif view == "inner":      # the layers of a slot side by side
+        whole = torch.randn(shape[1], shape[0], *shape[2:], generator=gen).cuda().to(dtype)
+        pool = whole.transpose(0, 1)
+        shape = tuple(pool.shape)
+    elif view == "shift":
+        pool = unaligned(pool)
+        whole = pool
+    n = shape[slot_dim]
+    rng = np.random.default_rng(5)
+    # a swap, a chain, a fork, a clear, a copy onto itself, and pairs that are skipped
+    perm = rng.permutation(n).tolist()
+    a = perm + [perm[0]] * 6
+    pairs = [(a[0], a[1]), (a[1], a[0]), (-1, a[2])]
+    if n > 6:
+        pairs += [(a[0], a[3]), (a[3], a[4]), (a[4], a[5]), (a[6], a[6])]
+    pairs += [(n, a[2]), (a[0], -1), (a[0], n), (2 ** 31 - 1, 0), (0, -2 ** 31)]
+    before = pool.clone()
+    ref = before.clone()
+    idx = (slice(None),) * slot_dim
+    for s, d in pairs:
+        if s < n and 0 <= d < n:
+            ref[idx + (d,)] = before[idx + (s,)] if s >= 0 else 0
+    other = whole[:, :, 1].clone() if view == "gap" else None
+    got = ssm.state_slots_copy(pool, i32([s for s, _ in pairs]), i32([d for _, d in pairs]), slot_dim=slot_dim)
+    assert got is pool
+    assert torch.equal(got.contiguous().view(torch.uint8), ref.contiguous().view(torch.uint8))
+    if other is not None:
+        assert torch.equal(whole[:, :, 1], other)
+
+
+@pytest.mark.parametrize("row,dtype", [(16, torch.float32), (7, torch.bfloat16)])
+def test_slots_copy_permutes_a_large_pool(ssm, row, dtype):
+    """As many pairs as a call takes, a random permutation: every source is read before it is written."""
+    n = 4096
+    pool = torch.randn(2, n, row, generator=torch.Generator().manual_seed(42)).to(dtype).cuda()
+    perm = torch.randperm(n, generator=torch.Generator().manual_seed(43))
+    ref = pool[:, perm.cuda()].clone()
+    ssm.state_slots_copy(pool, perm.int().cuda(), torch.arange(n, dtype=torch.int32).cuda(), slot_dim=1)
+    assert torch.equal(pool, ref)
+
+
+# ------------------------------------------------------------- together, as they are used
+
+def test_prompts_then_tokens_then_a_fork(ssm):
+    """Prompts in two halves, then tokens one by one, then a fork that goes on: the same as the whole
+    sequence at once, within the bounds of both."""
+    gen = torch.Generator().manual_seed(51)
+    dim, N, width, lens = 48, 16, 4, [37, 20, 64]
+    steps, half = 6, [19, 20, 1]
+    n = len(lens)
+    cu, total, bounds = packing([a + steps for a in lens])
+    x = rnd(gen, dim, total)
+    w, b = rnd(gen, dim, width, scale=0.5), rnd(gen, dim, scale=0.3)
+    p = _scan_inputs(gen, total, dim, dim, 1, N, "f32")
+    slots, pool_n = [4, 0, 2], 6
+    conv_pool, states = rnd(gen, pool_n, dim, width - 1), rnd(gen, pool_n, dim, N)
+    u_ref, u_err, _ = sp.conv_packed(f64(x), f64(w), f64(b), True, bounds, slots, [0] * n, f64(conv_pool), np.zeros((dim, total)))
+    plain = _plain(p)
+    plain["u"] = u_ref
+    ref, err, ref_pool, pool_err = sp.scan_packed(plain, bounds, slots, [0] * n, f64(states), np.zeros((dim, total)))
+    # what u's own error moves: the recurrence is linear in u
+    mag = dict(plain, u=np.abs(u_err), B=np.abs(plain["B"]), C=np.abs(plain["C"]), D=np.abs(plain["D"]),
+               z=np.full_like(plain["z"], 1e9))
+    moved, _, moved_pool, _ = sp.scan_packed(mag, bounds, slots, [0] * n, np.zeros((pool_n, dim, N)), np.zeros((dim, total)))
+    err = err + moved / 1e9 * np.maximum(np.abs(sp.silu(plain["z"])), 0.0) * 2
+    pool_err = pool_err + 2 * np.abs(moved_pool)
+
+    def cut(t, parts):
+        return torch.cat([t[..., lo:hi] for lo, hi in parts], -1).contiguous()
+
+    def prompts(parts, has):
+        pcu, ptotal, pb = packing([hi - lo for lo, hi in parts])
+        q = {k: cut(v, parts) if k in ("delta", "B", "C", "z") else v for k, v in p.items()}
+        flags = torch.tensor([has] * n, dtype=torch.uint8).cuda()
+        u = ssm.causal_conv1d_packed(cut(x, parts), w, i32(pcu), conv_pool, slots=i32(slots), has_state=flags, bias=b)
+        o = ssm.selective_scan_packed(u, q["delta"], q["A"], q["B"], q["C"], i32(pcu), states, slots=i32(slots), has_state=flags,
+                                      D=q["D"], z=q["z"], delta_bias=q["delta_bias"])
+        for (lo, hi), (a, c) in zip(parts, pb):
+            sp.check(f64(o)[:, a:c], ref[:, lo:hi], err[:, lo:hi], "f32", "prompt")
+
+    prompts([(lo, lo + h) for (lo, _), h in zip(bounds, half)], 0)
+    prompts([(lo + h, hi - steps) for (lo, hi), h in zip(bounds, half)], 1)
+
+    def token(k, at, check=True):
+        t = [hi - steps + k for _, hi in bounds] + [0]           # a padding row behind the live ones
+        rows = at + [-1]
+        u = ssm.causal_conv1d_update(x[:, t].t().contiguous(), w, conv_pool, slots=i32(rows), bias=b)
+        o = ssm.selective_state_update_slots(states, u, p["delta"][:, t].t().contiguous(), p["A"],
+                                             p["B"][:, :, t].permute(2, 0, 1).contiguous(),
+                                             p["C"][:, :, t].permute(2, 0, 1).contiguous(), slots=i32(rows), D=p["D"],
+                                             z=p["z"][:, t].t().contiguous(), delta_bias=p["delta_bias"])
+        for r in range(n):
+            sp.check(f64(o)[r], ref[:, t[r]], err[:, t[r]], "f32", f"token {k}")
+        return o
+
+    for k in range(steps - 2):
+        token(k, slots)
+    # fork every sequence into free slots; both go on alike, bit for bit
+    forks = [1, 3, 5]
+    for pool in (conv_pool, states):
+        ssm.state_slots_copy(pool, i32(slots), i32(forks))
+    first = [token(k, slots) for k in (steps - 2, steps - 1)]
+    second = [token(k, forks) for k in (steps - 2, steps - 1)]
+    assert all(torch.equal(f[:n], s[:n]) for f, s in zip(first, second))
+    assert torch.equal(states[slots], states[forks]) and torch.equal(conv_pool[slots], conv_pool[forks])
+    sp.check(f64(states)[slots], ref_pool[slots], pool_err[slots], "f32", "states")
+    # free the first ones
+    ssm.state_slots_copy(states, i32([-1] * n), i32(slots))
+    assert not states[slots].any() and states[forks].any()
+
+
+def test_graph_replay_reads_what_changed(ssm):
+    """A decode step captured once and replayed with other slots, tokens and a shorter batch."""
+    gen = torch.Generator().manual_seed(61)
+    dim, N, width, batch = 64, 16, 4, 6
+    w, b = rnd(gen, dim, width, scale=0.5), rnd(gen, dim, scale=0.3)
+    p = _scan_inputs(gen, batch, dim, dim, 1, N, "bf16", prompts=False)
+    conv_pool, states = rnd(gen, 9, dim, width - 1, dtype="bf16"), rnd(gen, 9, dim, N)
+    x, slots = rnd(gen, batch, dim, dtype="bf16"), i32([0, 1, 2, 3, 4, 5])
+    u, out = torch.zeros_like(x), torch.zeros_like(x)
+    src, dst = i32([0]), i32([8])
+
+    def step():
+        ssm.causal_conv1d_update(x, w, conv_pool, slots=slots, bias=b, out=u)
+        ssm.selective_state_update_slots(states, u, p["delta"], p["A"], p["B"], p["C"], slots=slots, D=p["D"], z=p["z"],
+                                         delta_bias=p["delta_bias"], out=out)
+        ssm.state_slots_copy(states, src, dst)
+
+    saved = conv_pool.clone(), states.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for new_slots, pair in (([5, 3, 7, -1, -1, -1], (3, 2)), ([8, 1, 0, 2, -1, 6], (1, 4))):
+        conv_pool.copy_(saved[0])
+        states.copy_(saved[1])
+        slots.copy_(i32(new_slots))
+        src.fill_(pair[0])
+        dst.fill_(pair[1])
+        x.copy_(rnd(gen, batch, dim, dtype="bf16"))
+        u.zero_()
+        out.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone(), conv_pool.clone(), states.clone()
+        conv_pool.copy_(saved[0])
+        states.copy_(saved[1])
+        u.zero_()
+        out.fill_(3.0)
+        step()
+        assert all(torch.equal(a, c) for a, c in zip(got, (out, conv_pool, states)))
+        assert torch.equal(out[[i for i, s in enumerate(new_slots) if s < 0]],
+                           torch.full_like(out, 3.0)[:new_slots.count(-1)])
+
+
+def test_packed_graph_with_other_lengths(ssm):
+    """Prompts captured once, cut path included, and replayed with other lengths in the same buffer."""
+    gen = torch.Generator().manual_seed(62)
+    dim, N, total = 32, 16, 1200
+    p = _scan_inputs(gen, total, dim, dim, 1, N, "bf16")
+    w = rnd(gen, dim, 4)
+    assert _chunk(ssm, p, 3) > 0
+    cu = i32([0, 400, 800, 1200])
+    conv_pool, states = rnd(gen, 3, dim, 3, dtype="bf16"), rnd(gen, 3, dim, N)
+    u, out = torch.zeros_like(p["u"]), torch.zeros_like(p["u"])
+
+    def run():
+        ssm.causal_conv1d_packed(p["u"], w, cu, conv_pool, out=u)
+        _call(ssm, dict(p, u=u), cu, states, out)
+
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for bounds in ([0, 1, 1200, 1200], [5, 700, 703, 1100]):
+        cu.copy_(i32(bounds))
+        u.zero_(), out.zero_(), states.zero_(), conv_pool.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = u.clone(), out.clone(), states.clone(), conv_pool.clone()
+        u.zero_(), out.zero_(), states.zero_(), conv_pool.zero_()
+        run()
+        assert all(torch.equal(a, c) for a, c in zip(got, (u, out, states, conv_pool)))
+        assert out[:, bounds[0]:bounds[-1]].any() and not out[:, :bounds[0]].any() and not out[:, bounds[-1]:].any()
+
+
+def test_on_another_stream(ssm):
+    """Calls on a stream of their own, several at once, each with its own workspace."""
+    gen = torch.Generator().manual_seed(63)
+    p = _scan_inputs(gen, 1500, 32, 32, 1, 16, "bf16")
+    cu = i32([0, 1500])
+    want_s = torch.zeros(1, 32, 16).cuda()
+    want = _call(ssm, p, cu, want_s, None)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    pools = [torch.zeros(1, 32, 16).cuda() for _ in streams]
+    torch.cuda.synchronize()
+    got = [_call(ssm, p, cu, s, None, stream=st) for s, st in zip(pools, streams)]
+    got.append(_call(ssm, p, cu, torch.zeros(1, 32, 16).cuda(), None, stream=torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got) and all(torch.equal(s, want_s) for s in pools)
+
+
+def test_offsets_past_32_bits(ssm):
+    """A slot that starts more than 2^31 elements into its pool."""
+    gen = torch.Generator().manual_seed(64)
+    dim, N, stride = 16, 16, 2 ** 30 // 4
+    buf = torch.empty(9 * stride + dim * N, device="cuda")
+    states = torch.as_strided(buf, (10, dim, N), (stride, N, 1))
+    small = torch.zeros(10, dim, N, device="cuda")
+    states.zero_()
+    p = _scan_inputs(gen, 40, dim, dim, 1, N, "bf16")
+    q = _scan_inputs(gen, 2, dim, dim, 1, N, "bf16", prompts=False)
+    for pool in (states, small):
+        _call(ssm, p, i32([0, 21, 40]), pool, None, slots=i32([9, 8]))
+        ssm.selective_state_update_slots(pool, q["u"], q["delta"], q["A"], q["B"], q["C"], slots=i32([9, 8]))
+        ssm.state_slots_copy(pool, i32([9]), i32([0]))
+        ssm.state_slots_copy(pool, i32([0, -1]), i32([8, 9]))
+    assert torch.equal(states, small) and small[8].any()
+    del buf, states
+    x = rnd(gen, 2, 16, dtype="bf16")
+    buf = torch.empty(2 ** 31 + 4096, dtype=torch.bfloat16, device="cuda")
+    far = torch.as_strided(buf, (2, 16, 3), (2 ** 31 + 64, 3, 1))
+    near = torch.zeros(2, 16, 3, dtype=torch.bfloat16, device="cuda")
+    far.zero_()
+    w = rnd(gen, 16, 4)
+    for pool in (far, near):
+        ssm.causal_conv1d_update(x, w, pool)
+        ssm.causal_conv1d_packed(x.t().contiguous(), w, i32([0, 1, 2]), pool, slots=i32([1, 0]),
+                                 has_state=torch.ones(2, dtype=torch.uint8).cuda())
+    assert torch.equal(far, near) and near[1].any()
+
+
+def test_empty_calls(ssm):
+    z = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
+    w = z(8, 4)
+    pool, states = z(3, 8, 3) + 1, z(3, 8, 16) + 1
+    # no sequences
+    assert ssm.causal_conv1d_packed(z(8, 5), w, i32([0]), pool).shape == (8, 5)
+    ssm.selective_scan_packed(z(8, 5), z(8, 5), z(8, 16), z(1, 16, 5), z(1, 16, 5), i32([0]), states)
+    # no rows
+    ssm.causal_conv1d_update(z(0, 8), w, pool)
+    ssm.selective_state_update_slots(states, z(0, 8), z(0, 8), z(8, 16), z(0, 1, 16), z(0, 1, 16))
+    ssm.state_slots_copy(states, i32([]), i32([]))
+    torch.cuda.synchronize()
+    assert (pool == 1).all() and (states == 1).all()
+    # no tokens: a sequence that goes on keeps its state, a new one is zeros
+    flags = torch.tensor([1, 0], dtype=torch.uint8).cuda()
+    ssm.causal_conv1d_packed(z(8, 0), w, i32([0, 0, 0]), pool, has_state=flags)
+    ssm.selective_scan_packed(z(8, 0), z(8, 0), z(8, 16), z(1, 16, 0), z(1, 16, 0), i32([0, 0, 0]), states, has_state=flags)
+    torch.cuda.synchronize()
+    for t in (pool, states):
+        assert (t[0] == 1).all() and (t[1] == 0).all() and (t[2] == 1).all()
+
+
+def test_bounds_out_of_order_stay_inside(ssm):
+    """cu_seqlens that run backwards or past the buffer are clamped: other memory stays as it was."""
+    gen = torch.Generator().manual_seed(65)
+    dim, N, total = 24, 16, 64
+    p = _scan_inputs(gen, total, dim, dim, 1, N, "bf16")
+    guard = torch.full((3, dim, total), 7.0, dtype=torch.bfloat16, device="cuda")
+    states, conv_pool = rnd(gen, 4, dim, N), rnd(gen, 4, dim, 3, dtype="bf16")
+    w = rnd(gen, dim, 4)
+    for cu in ([0, 50, 20, 10 ** 9], [-5, 3, -(2 ** 31), 40], [2 ** 31 - 1, 0, 64, 64]):
+        _call(ssm, p, i32(cu), states, guard[1])
+        ssm.causal_conv1d_packed(p["u"], w, i32(cu), conv_pool, out=guard[1])
+        torch.cuda.synchronize()
+        assert (guard[0] == 7).all() and (guard[2] == 7).all()
