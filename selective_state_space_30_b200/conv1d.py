@@ -3,16 +3,16 @@
 from __future__ import annotations
 
 from . import _abi
-from ._tensors import io_code, launch, need, need_cuda
+from ._tensors import io_code, launch, need, need_cuda, ptr
 
 
 def _checked(x, w, bias):
     import torch
-    need_cuda("x", x, 3)
+    dev = need_cuda("x", x, 3)
     if w.dim() != 2:
         raise ValueError("w must have shape (dim, width)")
-    need("w", w, torch.float32, (x.shape[1], w.shape[1]), x.device)
-    need("bias", bias, torch.float32, (x.shape[1],), x.device)
+    need("w", w, torch.float32, (x.shape[1], w.shape[1]), dev)
+    need("bias", bias, torch.float32, (x.shape[1],), dev)
     return (*x.shape, w.shape[1], io_code(x))
 
 
@@ -21,13 +21,13 @@ def causal_conv1d_fwd(x, w, bias=None, silu: bool = True, out=None, stream=None)
     bf16 or fp32, w (dim, width) and bias fp32."""
     import torch
     batch, dim, seqlen, width, io = _checked(x, w, bias)
-    need("out", out, x.dtype, x.shape, x.device)
+    need("out", out, x.dtype, x.shape, x.get_device())
 
-    def call(out, raw):
-        out = torch.empty_like(x) if out is None else out
-        _abi.ssm_causal_conv1d_fwd(batch, dim, seqlen, width, io, x, w, bias, silu, out, raw)
-        return out
-    return launch(call, x.device, stream, out)
+    def call(raw):
+        o = torch.empty_like(x) if out is None else out
+        _abi.ssm_causal_conv1d_fwd(batch, dim, seqlen, width, io, x, w, bias, silu, o, raw)
+        return o
+    return launch(call, x.get_device(), stream)
 
 
 def causal_conv1d_bwd(x, w, dout, bias=None, silu: bool = True, workspace=None, stream=None) -> dict:
@@ -36,20 +36,24 @@ def causal_conv1d_bwd(x, w, dout, bias=None, silu: bool = True, workspace=None, 
     is allocated with torch unless given."""
     import torch
     batch, dim, seqlen, width, io = _checked(x, w, bias)
-    need("dout", dout, x.dtype, x.shape, x.device)
-    if workspace is not None and (workspace.device != x.device or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous tensor on {x.device}")
+    dev = x.get_device()
+    need("dout", dout, x.dtype, x.shape, dev)
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
 
-    def call(workspace, raw):
-        if workspace is None:
+    def call(raw):
+        ws = workspace
+        if ws is None:
             nbytes = _abi.ssm_causal_conv1d_bwd_workspace_size(batch, dim, seqlen, width, io)
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-        g = {"dx": torch.empty_like(x), "dw": torch.empty_like(w),
-             "dbias": torch.empty((dim,), dtype=torch.float32, device=x.device)}
-        _abi.ssm_causal_conv1d_bwd(batch, dim, seqlen, width, io, x, w, bias, silu, dout, g["dx"], g["dw"], g["dbias"],
-                                   workspace, workspace.numel() * workspace.element_size(), raw)
-        return g
-    return launch(call, x.device, stream, workspace)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        dx, dw, dbias = torch.empty_like(x), torch.empty_like(w), w.new_empty(dim)
+        lib = _abi._lib or _abi.load_library()
+        _abi._check(lib.ssm_causal_conv1d_bwd(
+            batch, dim, seqlen, width, io, x.data_ptr(), w.data_ptr(), ptr(bias), 1 if silu else 0, dout.data_ptr(),
+            dx.data_ptr(), dw.data_ptr(), dbias.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), raw),
+            "ssm_causal_conv1d_bwd")
+        return {"dx": dx, "dw": dw, "dbias": dbias}
+    return launch(call, dev, stream)
 
 
 _fn_cls = None

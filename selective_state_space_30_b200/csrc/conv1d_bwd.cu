@@ -5,8 +5,8 @@
 //   dv[t] = dout[t] act'(v[t]),   silu'(v) = s (1 + v (1 - s)), s = 1 / (1 + exp(-v))
 //   dx[t] = sum_k w[k] dv[t+W-1-k],   dw[k] = sum_{b,t} dv[t] x[t-W+1+k],   dbias = sum_{b,t} dv[t]
 //
-// HBM-bound: x and dout are read once and dx is written once.  A warp walks a stretch of one
-// row from its end to its start, 32 16-byte pieces at a time: the inputs before a piece come
+// HBM-bound: x and dout are read once and dx is written once.  A warp walks a stretch of two
+// rows from its end to its start, 32 16-byte pieces at a time: the inputs before a piece come
 // from the lane below, the dv behind it from the lane above, and lane 31's from the tile before.
 // dw and dbias stay in registers for the stretch; each warp writes one partial and a second
 // kernel adds the partials in a fixed order, so the gradients repeat bit for bit.
@@ -15,14 +15,13 @@
 
 #include <cstdint>
 
-#include "scan_kernel.cuh"   // ex2_approx, rcp_approx
+#include "scan_kernel.cuh"   // f32x2 operations, ex2_approx, rcp_approx
 #include "ssm_scan.h"
 
 namespace {
 
 constexpr int kMaxWidth = 4;
 constexpr int kWarps = 8;
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct ConvBwd {
     const void *x, *dout;
@@ -41,143 +40,278 @@ template <typename T> __device__ __forceinline__ T from_f(float v);
 template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// Tokens [t, t + V) of a row; those outside [0, L) read as zero and are not accessed.
+// dv of two tokens
+template <bool SILU>
+__device__ __forceinline__ float2 dact2(float2 v, float2 g) {
+    if (!SILU) return g;
+    const float2 a = ssm::mul2(v, ssm::dup2(-ssm::kLog2e));
+    const float2 q = ssm::add2(make_float2(ssm::ex2_approx(a.x), ssm::ex2_approx(a.y)), ssm::dup2(1.f));
+    const float2 s = make_float2(ssm::rcp_approx(q.x), ssm::rcp_approx(q.y));
+    const float2 c = ssm::fma2(s, ssm::dup2(-1.f), ssm::dup2(1.f));
+    return ssm::mul2(ssm::mul2(g, s), ssm::fma2(v, c, ssm::dup2(1.f)));
+}
+
+// One 16-byte piece of x and of dout, and of x the 8 (bf16) or 16 (fp32) bytes before it.
 template <typename T>
-__device__ __forceinline__ void load_tokens(const T* row, int64_t t, int64_t L, float* v) {
-    constexpr int V = 16 / sizeof(T);
-    const T* p = row + t;
-    if (t >= 0 && t + V <= L && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
-        if constexpr (sizeof(T) == 4) {
-            v[0] = __uint_as_float(q.x); v[1] = __uint_as_float(q.y);
-            v[2] = __uint_as_float(q.z); v[3] = __uint_as_float(q.w);
-        } else {
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+struct Piece {
+    static constexpr int PW = sizeof(T) == 2 ? 2 : 4;
+    uint4 x, g;
+    uint32_t before[PW];
+};
+
+template <typename T, int CNT>
+__device__ __forceinline__ void unpack(const uint32_t* w, float* v) {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        for (int i = 0; i < CNT; ++i) v[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < CNT / 2; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+}
+
+// Tokens t .. of a row as 32-bit words; those outside [0, L) read as zero and are not accessed.
+template <typename T, int WORDS>
+__device__ __forceinline__ void gather(const T* row, int64_t t, int64_t L, uint32_t* w) {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            w[i] = t + i >= 0 && t + i < L ? __float_as_uint(row[t + i]) : 0u;
+        } else {
+            const unsigned short* r = reinterpret_cast<const unsigned short*>(row);
+            const int64_t a = t + 2 * i;
+            const uint32_t lo = a >= 0 && a < L ? r[a] : 0u, hi = a + 1 >= 0 && a + 1 < L ? r[a + 1] : 0u;
+            w[i] = lo | hi << 16;
+        }
+    }
+}
+
+// As load_piece, for rows that start on the 16-byte grid: lanes behind the row's end hold zeros.
+template <typename T>
+__device__ __forceinline__ Piece<T> load_aligned(const T* x, const T* go, bool in, bool before) {
+    Piece<T> p = {};
+    if (in) {
+        p.x = __ldg(reinterpret_cast<const uint4*>(x));
+        p.g = __ldg(reinterpret_cast<const uint4*>(go));
+        if (before) {
+            if constexpr (sizeof(T) == 2) {
+                const uint2 q = __ldg(reinterpret_cast<const uint2*>(x - 4));
+                p.before[0] = q.x; p.before[1] = q.y;
+            } else {
+                const uint4 q = __ldg(reinterpret_cast<const uint4*>(x - 4));
+                p.before[0] = q.x; p.before[1] = q.y; p.before[2 % Piece<T>::PW] = q.z; p.before[3 % Piece<T>::PW] = q.w;
+            }
+        }
+    }
+    return p;
+}
+
+// The lane's pieces of a tile; lane 0's earlier tokens too (the others take theirs from the lane
+// below).  `whole`: the tile lies inside the row, on the 16-byte grid (t > 0 is then at least V).
+template <typename T>
+__device__ __forceinline__ Piece<T> load_piece(const T* x, const T* go, int64_t t, int64_t L, bool whole, int lane) {
+    constexpr int V = 16 / sizeof(T), PW = Piece<T>::PW;
+    Piece<T> p;
+#pragma unroll
+    for (int i = 0; i < PW; ++i) p.before[i] = 0u;
+    if (whole) {
+        p.x = __ldg(reinterpret_cast<const uint4*>(x + t));
+        p.g = __ldg(reinterpret_cast<const uint4*>(go + t));
+        if (lane == 0 && t > 0) {
+#pragma unroll
+            for (int i = 0; i < PW; i += 2) {
+                const uint2 q = __ldg(reinterpret_cast<const uint2*>(x + t - V / 2 * (PW / 2)) + i / 2);
+                p.before[i] = q.x;
+                p.before[i + 1] = q.y;
             }
         }
     } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = t + e >= 0 && t + e < L ? to_f<T>(p[e]) : 0.f;
+        uint32_t w[4];
+        gather<T, 4>(x, t, L, w);
+        p.x = make_uint4(w[0], w[1], w[2], w[3]);
+        gather<T, 4>(go, t, L, w);
+        p.g = make_uint4(w[0], w[1], w[2], w[3]);
+        if (lane == 0) gather<T, PW>(x, t - 4, L, p.before);
     }
+    return p;
 }
 
-// dv of one token
-__device__ __forceinline__ float dact(float v, float g, int silu) {
-    if (!silu) return g;
-    const float s = ssm::rcp_approx(1.f + ssm::ex2_approx(-kLog2e * v));
-    return g * s * fmaf(v, 1.f - s, 1.f);
-}
-
-template <typename T, int W>
-__global__ void __launch_bounds__(32 * kWarps) conv1d_bwd_kernel(const ConvBwd p) {
-    constexpr int V = 16 / sizeof(T), H = W - 1;
+// A warp walks two rows, of neighbouring channels: they are the two halves of every f32x2
+// operation, so that a value sits in one register pair for all the taps that meet it.  (Rows off
+// the 16-byte grid have their pieces at different tokens; the arithmetic is the same.)
+// ALIGNED: every row of x, dout and dx starts on the 16-byte grid.
+template <typename T, int W, bool ALIGNED, bool SILU>
+__global__ void __launch_bounds__(32 * kWarps, 2) conv1d_bwd_kernel(const ConvBwd p) {
+    constexpr int V = 16 / sizeof(T), H = W - 1, PW = Piece<T>::PW;
     const int lane = threadIdx.x & 31;
     const int64_t id = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (id >= p.rows * p.n_seg) return;
-    const int64_t r = id / p.n_seg, seg = id % p.n_seg, d = r % p.dim, L = p.seqlen;
-    const T* x = static_cast<const T*>(p.x) + r * L;
-    const T* go = static_cast<const T*>(p.dout) + r * L;
-    T* dx = static_cast<T*>(p.dx) + r * L;
-    // pieces sit on dx's 16-byte grid: the row's first one may start up to V-1 tokens early
-    const int m = (int)((reinterpret_cast<uintptr_t>(dx) & 15u) / sizeof(T));
-    float w[W], dw[W], db = 0.f;
+    const int64_t pairs = (p.dim + 1) / 2, batch = p.rows / p.dim;
+    if (id >= batch * pairs * p.n_seg) return;
+    const int64_t seg = id % p.n_seg, b = id / p.n_seg / pairs, d0 = id / p.n_seg % pairs * 2, L = p.seqlen;
+    const bool both = d0 + 1 < p.dim;                 // an odd last channel pairs with itself and writes once
+    const int64_t d[2] = {d0, both ? d0 + 1 : d0};
+    const T *x[2], *go[2];
+    T* dx[2];
+    int m[2];
+    bool grid[2];
+    int64_t tiles[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int64_t row = (b * p.dim + d[r]) * L;
+        x[r] = static_cast<const T*>(p.x) + row;
+        go[r] = static_cast<const T*>(p.dout) + row;
+        dx[r] = static_cast<T*>(p.dx) + row;
+        // pieces sit on dx's 16-byte grid: the row's first one may start up to V-1 tokens early
+        m[r] = ALIGNED ? 0 : (int)((reinterpret_cast<uintptr_t>(dx[r]) & 15u) / sizeof(T));
+        grid[r] = ((reinterpret_cast<uintptr_t>(x[r]) ^ reinterpret_cast<uintptr_t>(dx[r])) & 15u) == 0 &&
+                  ((reinterpret_cast<uintptr_t>(go[r]) ^ reinterpret_cast<uintptr_t>(dx[r])) & 15u) == 0;
+        // the row's own tiles end where its tokens do, which may be one tile earlier than another row's
+        tiles[r] = (L + m[r] + 32 * V - 1) / (32 * V);
+    }
+    const int64_t all = tiles[0] > tiles[1] ? tiles[0] : tiles[1];
+    const int64_t tile0 = seg * p.tiles_per_seg, tile1 = tile0 + p.tiles_per_seg < all ? tile0 + p.tiles_per_seg : all;
+    float2 w[W], dw[W], db = ssm::dup2(0.f);
 #pragma unroll
     for (int k = 0; k < W; ++k) {
-        w[k] = __ldg(p.w + d * W + k);
-        dw[k] = 0.f;
+        w[k] = make_float2(__ldg(p.w + d[0] * W + k), __ldg(p.w + d[1] * W + k));
+        dw[k] = ssm::dup2(0.f);
     }
-    const float bias = p.bias ? __ldg(p.bias + d) : 0.f;
-    const int64_t first = seg * p.tiles_per_seg;
-    const int64_t end = first + p.tiles_per_seg < p.tiles ? first + p.tiles_per_seg : p.tiles;
-
+    const float2 bias = p.bias ? make_float2(__ldg(p.bias + d[0]), __ldg(p.bias + d[1])) : ssm::dup2(0.f);
+    auto load = [&](int r, int64_t tile) {
+        if constexpr (ALIGNED) {
+            const int64_t t = (tile * 32 + lane) * V;
+            return load_aligned<T>(x[r] + t, go[r] + t, t < L, lane == 0 && t > 0);
+        }
+        const int64_t t = tile * 32 * V - m[r];
+        if (tile >= tiles[r]) return Piece<T>{};      // this row ends a tile before the other
+        return load_piece<T>(x[r], go[r], t + lane * V, L, grid[r] && t >= 0 && t + 32 * V <= L, lane);
+    };
+    Piece<T> next[2] = {};
+    if (tile1 > tile0) {
+        next[0] = load(0, tile1 - 1);
+        next[1] = load(1, tile1 - 1);
+    }
     // dv of the W-1 tokens behind the stretch, on lanes 0 .. W-2, then on every lane
-    float behind[H > 0 ? H : 1];
+    float2 behind[H > 0 ? H : 1];
     {
-        const int64_t t = end * 32 * V - m + lane;
-        float g = 0.f;
-        if (lane < H && t < L) {
-            float v = bias;
+        float g[2] = {0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < W; ++k) {
-                const int64_t s = t - H + k;
-                if (s >= 0) v = fmaf(w[k], to_f<T>(x[s]), v);
-            }
-            g = dact(v, to_f<T>(go[t]), p.silu);
-        }
+        for (int r = 0; r < 2; ++r) {
+            const int64_t t = tile1 * 32 * V - m[r] + lane;
+            if (lane < H && t < L) {
+                float v = r ? bias.y : bias.x;
 #pragma unroll
-        for (int k = 0; k < H; ++k) behind[k] = __shfl_sync(0xffffffffu, g, k);
-    }
-    for (int64_t tile = end - 1; tile >= first; --tile) {
-        const int64_t t = (tile * 32 + lane) * V - m;
-        float xv[H + V], dv[V + H];                   // tokens t - H .. t + V - 1; t .. t + V + H - 1
-        load_tokens<T>(x, t, L, xv + H);
-        load_tokens<T>(go, t, L, dv);
-#pragma unroll
-        for (int k = 0; k < H; ++k) {
-            xv[k] = __shfl_up_sync(0xffffffffu, xv[V + k], 1);
-            const int64_t s = t - H + k;
-            if (lane == 0) xv[k] = s >= 0 && s < L ? to_f<T>(x[s]) : 0.f;
-        }
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            float v = bias;
-#pragma unroll
-            for (int k = 0; k < W; ++k) v = fmaf(w[k], xv[e + k], v);
-            dv[e] = dact(v, dv[e], p.silu);
-        }
-#pragma unroll
-        for (int k = 0; k < H; ++k) {
-            dv[V + k] = __shfl_down_sync(0xffffffffu, dv[k], 1);
-            if (lane == 31) dv[V + k] = behind[k];
-            behind[k] = __shfl_sync(0xffffffffu, dv[k], 0);
-        }
-        float o[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            float a = 0.f;
-#pragma unroll
-            for (int k = 0; k < W; ++k) {
-                a = fmaf(w[k], dv[e + H - k], a);
-                dw[k] = fmaf(dv[e], xv[e + k], dw[k]);
-            }
-            db += dv[e];
-            o[e] = a;
-        }
-        if (t >= 0 && t + V <= L) {
-            uint4 q;
-            if constexpr (sizeof(T) == 4) {
-                q = make_uint4(__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]), __float_as_uint(o[3]));
-            } else {
-                uint32_t u[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
-                    u[i] = *reinterpret_cast<const uint32_t*>(&b2);
+                for (int k = 0; k < W; ++k) {
+                    const int64_t s = t - H + k;
+                    if (s >= 0) v = fmaf(r ? w[k].y : w[k].x, to_f<T>(x[r][s]), v);
                 }
-                q = make_uint4(u[0], u[1], u[2], u[3]);
+                g[r] = dact2<SILU>(ssm::dup2(v), ssm::dup2(to_f<T>(go[r][t]))).x;
             }
-            *reinterpret_cast<uint4*>(dx + t) = q;
-        } else {
+        }
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (t + e >= 0 && t + e < L) dx[t + e] = from_f<T>(o[e]);
+        for (int k = 0; k < H; ++k)
+            behind[k] = make_float2(__shfl_sync(0xffffffffu, g[0], k), __shfl_sync(0xffffffffu, g[1], k));
+    }
+    for (int64_t tile = tile1 - 1; tile >= tile0; --tile) {
+        const Piece<T> cur[2] = {next[0], next[1]};
+        if (tile > tile0) {
+            next[0] = load(0, tile - 1);
+            next[1] = load(1, tile - 1);
+        }
+        // tokens t - 4 .. t + V - 1 of x; t .. t + V + H - 1 of dv
+        float2 xv[4 + V], dv[V + H];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const uint32_t xw[4] = {cur[r].x.x, cur[r].x.y, cur[r].x.z, cur[r].x.w};
+            const uint32_t gw[4] = {cur[r].g.x, cur[r].g.y, cur[r].g.z, cur[r].g.w};
+            uint32_t bw[PW];
+#pragma unroll
+            for (int i = 0; i < PW; ++i) {
+                bw[i] = __shfl_up_sync(0xffffffffu, xw[4 - PW + i], 1);
+                if (lane == 0) bw[i] = cur[r].before[i];
+            }
+            float xb[4], xc[V], gc[V];
+            unpack<T, 4>(bw, xb);
+            unpack<T, V>(xw, xc);
+            unpack<T, V>(gw, gc);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) (r ? xv[e].y : xv[e].x) = xb[e];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                (r ? xv[4 + e].y : xv[4 + e].x) = xc[e];
+                (r ? dv[e].y : dv[e].x) = gc[e];
+            }
+        }
+        const float2* xh = xv + 4 - H;                // xh[e + k] meets w[k] at token e
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            float2 v = bias;
+#pragma unroll
+            for (int k = 0; k < W; ++k) v = ssm::fma2(w[k], xh[e + k], v);
+            dv[e] = dact2<SILU>(v, dv[e]);
+            db = ssm::add2(db, dv[e]);
+#pragma unroll
+            for (int k = 0; k < W; ++k) dw[k] = ssm::fma2(dv[e], xh[e + k], dw[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+            dv[V + k] = make_float2(__shfl_down_sync(0xffffffffu, dv[k].x, 1), __shfl_down_sync(0xffffffffu, dv[k].y, 1));
+            if (lane == 31) dv[V + k] = behind[k];
+            behind[k] = make_float2(__shfl_sync(0xffffffffu, dv[k].x, 0), __shfl_sync(0xffffffffu, dv[k].y, 0));
+        }
+        float2 o[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            o[e] = ssm::mul2(w[H], dv[e]);
+#pragma unroll
+            for (int k = 0; k < H; ++k) o[e] = ssm::fma2(w[k], dv[e + H - k], o[e]);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int64_t t = (tile * 32 + lane) * V - m[r];
+            if (r && !both) break;
+            if (ALIGNED ? t < L : t >= 0 && t + V <= L) {
+                uint32_t u[4];
+                if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(r ? o[i].y : o[i].x);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const __nv_bfloat162 b2 = r ? __floats2bfloat162_rn(o[2 * i].y, o[2 * i + 1].y)
+                                                    : __floats2bfloat162_rn(o[2 * i].x, o[2 * i + 1].x);
+                        u[i] = *reinterpret_cast<const uint32_t*>(&b2);
+                    }
+                }
+                *reinterpret_cast<uint4*>(dx[r] + t) = make_uint4(u[0], u[1], u[2], u[3]);
+            } else if (!ALIGNED) {
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    if (t + e >= 0 && t + e < L) dx[r][t + e] = from_f<T>(r ? o[e].y : o[e].x);
+            }
         }
     }
 #pragma unroll
     for (int s = 16; s >= 1; s >>= 1) {
-        db += __shfl_xor_sync(0xffffffffu, db, s);
+        db = ssm::add2(db, make_float2(__shfl_xor_sync(0xffffffffu, db.x, s), __shfl_xor_sync(0xffffffffu, db.y, s)));
 #pragma unroll
-        for (int k = 0; k < W; ++k) dw[k] += __shfl_xor_sync(0xffffffffu, dw[k], s);
+        for (int k = 0; k < W; ++k)
+            dw[k] = ssm::add2(dw[k], make_float2(__shfl_xor_sync(0xffffffffu, dw[k].x, s),
+                                                 __shfl_xor_sync(0xffffffffu, dw[k].y, s)));
     }
     if (lane == 0) {
-        float* o = p.part + (((r / p.dim) * p.n_seg + seg) * p.dim + d) * (W + 1);
+        float* o = p.part + ((b * p.n_seg + seg) * p.dim + d0) * (W + 1);
 #pragma unroll
-        for (int k = 0; k < W; ++k) o[k] = dw[k];
-        o[W] = db;
+        for (int k = 0; k < W; ++k) o[k] = dw[k].x;
+        o[W] = db.x;
+        if (both) {
+#pragma unroll
+            for (int k = 0; k < W; ++k) o[W + 1 + k] = dw[k].y;
+            o[2 * W + 1] = db.y;
+        }
     }
 }
 
@@ -205,13 +339,13 @@ struct Plan {
     int64_t tiles, tiles_per_seg, n_seg;
 };
 
-// Rows are cut into stretches where there are too few of them to fill the machine (64 warps on
-// each of 148 SMs); the shape alone decides, so the sums' order is the shape's.
+// Rows are cut into stretches where there are too few pairs of them to fill the machine (32 warps
+// on each of 148 SMs); the shape alone decides, so the sums' order is the shape's.
 Plan plan_of(int64_t batch, int64_t dim, int64_t seqlen, int io_dtype) {
     const int64_t V = io_dtype == SSM_BF16 ? 8 : 4;
     Plan q;
     q.tiles = (seqlen + V - 1 + 32 * V - 1) / (32 * V);
-    const int64_t rows = batch * dim, want = 148 * 64;
+    const int64_t rows = batch * ((dim + 1) / 2), want = 148 * 32;
     int64_t n = rows > 0 ? (want + rows - 1) / rows : 1;
     if (n > q.tiles) n = q.tiles;
     if (n < 1) n = 1;
@@ -233,20 +367,24 @@ int check_shape(int64_t batch, int64_t dim, int64_t seqlen, int32_t width, int32
 }
 
 template <typename T, int W>
-int launch(const ConvBwd& p, cudaStream_t s) {
-    const int64_t ctas = (p.rows * p.n_seg + kWarps - 1) / kWarps;
+int launch(const ConvBwd& p, bool aligned, cudaStream_t s) {
+    const int64_t ctas = (p.rows / p.dim * ((p.dim + 1) / 2) * p.n_seg + kWarps - 1) / kWarps;
     if (ctas > 0x7FFFFFFF) return SSM_ERR_UNSUPPORTED;
-    conv1d_bwd_kernel<T, W><<<(unsigned)ctas, 32 * kWarps, 0, s>>>(p);
+    const unsigned g = (unsigned)ctas;
+    if (aligned && p.silu) conv1d_bwd_kernel<T, W, true, true><<<g, 32 * kWarps, 0, s>>>(p);
+    else if (aligned) conv1d_bwd_kernel<T, W, true, false><<<g, 32 * kWarps, 0, s>>>(p);
+    else if (p.silu) conv1d_bwd_kernel<T, W, false, true><<<g, 32 * kWarps, 0, s>>>(p);
+    else conv1d_bwd_kernel<T, W, false, false><<<g, 32 * kWarps, 0, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }
 
 template <typename T>
-int launch_t(const ConvBwd& p, int width, cudaStream_t s) {
+int launch_t(const ConvBwd& p, int width, bool aligned, cudaStream_t s) {
     switch (width) {
-        case 1: return launch<T, 1>(p, s);
-        case 2: return launch<T, 2>(p, s);
-        case 3: return launch<T, 3>(p, s);
-        case 4: return launch<T, 4>(p, s);
+        case 1: return launch<T, 1>(p, aligned, s);
+        case 2: return launch<T, 2>(p, aligned, s);
+        case 3: return launch<T, 3>(p, aligned, s);
+        case 4: return launch<T, 4>(p, aligned, s);
         default: return SSM_ERR_UNSUPPORTED;
     }
 }
@@ -283,7 +421,9 @@ extern "C" int ssm_causal_conv1d_bwd(int64_t batch, int64_t dim, int64_t seqlen,
         p.rows = batch * dim; p.dim = dim; p.seqlen = seqlen;
         p.tiles = q.tiles; p.tiles_per_seg = q.tiles_per_seg; p.n_seg = q.n_seg;
         p.silu = silu ? 1 : 0;
-        const int r = io_dtype == SSM_BF16 ? launch_t<__nv_bfloat16>(p, width, s) : launch_t<float>(p, width, s);
+        const bool aligned = seqlen * (int64_t)esz % 16 == 0 && aligned_to(x, 16) && aligned_to(dout, 16) && aligned_to(dx, 16);
+        const int r = io_dtype == SSM_BF16 ? launch_t<__nv_bfloat16>(p, width, aligned, s)
+                                            : launch_t<float>(p, width, aligned, s);
         if (r != SSM_OK) return r;
         n_part = batch * q.n_seg;
     }

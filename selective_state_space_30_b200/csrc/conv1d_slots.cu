@@ -11,7 +11,9 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
+#include "pair.cuh"
 #include "scan_kernel.cuh"   // silu1
 #include "slots.h"
 #include "ssm_scan.h"
@@ -21,6 +23,7 @@ namespace {
 constexpr int kMaxWidth = 4;
 constexpr int kThreads = 256;
 constexpr int kMaxGridY = 65535;
+constexpr int kTapRows = 256;     // rows whose taps a CTA keeps in shared memory
 
 template <typename T> __device__ __forceinline__ float to_f(T v);
 template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
@@ -69,9 +72,11 @@ struct PackedConv {
     int64_t head_ctas;       // CTAs of the sequences' first tokens, ahead of the others
     unsigned head_tiles;     // channel tiles of those
     unsigned time_tiles;     // time tiles of the others
-    int tx;                  // 16-byte pieces of a row that a CTA covers (a power of two)
+    int log_tx;              // 16-byte pieces of a row that a CTA covers, a power of two
     int rows_per_thread;
     int silu;
+    int w_vec;               // w is 16-byte aligned
+    int aligned;             // so is every row of x and out
 };
 
 // The 16 bytes at p, where they lie inside [lo, hi); elements outside read as zero.
@@ -92,7 +97,7 @@ __device__ __forceinline__ uint4 load_piece(const unsigned char* p, const unsign
 // which need the slot's history, and the slot's new history.  One thread reads the old history
 // and writes the new one, so no other CTA's read can meet the write.
 template <typename T, int W>
-__device__ __forceinline__ void sequence_heads(const PackedConv& p, int64_t bid) {
+__device__ __forceinline__ void sequence_heads(const PackedConv& p, unsigned bid) {
     const int64_t seq = bid / p.head_tiles;
     const int64_t d = (int64_t)(bid % p.head_tiles) * kThreads + threadIdx.x;
     if (d >= p.dim) return;
@@ -143,35 +148,130 @@ __device__ __forceinline__ void sequence_heads(const PackedConv& p, int64_t bid)
     }
 }
 
+// One row's piece and what becomes of it: xw holds its four words behind the PW words before it;
+// `mask`: the tokens to write, `nan`: those of them whose slot is bad.
+template <int PW>
+struct RowPiece {
+    uint32_t xw[PW + 4];
+    unsigned char* out;
+    int64_t d;
+    unsigned mask, nan;
+};
+
+template <typename T, int W>
+__device__ __forceinline__ void load_taps(const PackedConv& p, int64_t d, float (&w)[W]) {
+    if (W == 4 && p.w_vec) {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(p.w) + d);
+        w[0] = q.x; w[1 % W] = q.y; w[2 % W] = q.z; w[3 % W] = q.w;
+    } else {
+#pragma unroll
+        for (int k = 0; k < W; ++k) w[k] = __ldg(p.w + d * W + k);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_piece(unsigned char* out, unsigned mask, unsigned nan, float* o) {
+    constexpr int V = 16 / sizeof(T);
+    if (mask == 0u) return;
+    if (nan != 0u) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            if ((nan >> e) & 1u) o[e] = __int_as_float(0x7FC00000);
+    }
+    if (mask == (1u << V) - 1u) {
+        *reinterpret_cast<uint4*>(out) = pack<T>(o);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            if ((mask >> e) & 1u) reinterpret_cast<T*>(out)[e] = from_f<T>(o[e]);
+    }
+}
+
+// The outputs of two rows' pieces.  The rows are the two halves of every f32x2 operation: a value
+// then sits in one register pair for all taps, where pairs of neighbouring tokens would need a
+// copy of it for every other tap (170 -> 102 us for 32768 tokens x 4096 channels in bf16).
+template <typename T, int W, int PW, bool SILU>
+__device__ __forceinline__ void conv_pieces(const uint32_t (&x0)[PW + 4], const uint32_t (&x1)[PW + 4],
+                                            const ssm::pair_t* w, ssm::pair_t bias, float* o0, float* o1) {
+    constexpr int V = 16 / sizeof(T), ES = (int)sizeof(T), E = (PW + 4) * 4 / ES;
+    ssm::pair_t xv[E];
+#pragma unroll
+    for (int k = 0; k < PW + 4; ++k) {
+        if constexpr (sizeof(T) == 4) {
+            xv[k] = ssm::pk(__uint_as_float(x0[k]), __uint_as_float(x1[k]));
+        } else {
+            xv[2 * k] = ssm::pk(__uint_as_float(x0[k] << 16), __uint_as_float(x1[k] << 16));
+            xv[2 * k + 1] = ssm::pk(__uint_as_float(x0[k] & 0xFFFF0000u), __uint_as_float(x1[k] & 0xFFFF0000u));
+        }
+    }
+    const ssm::pair_t* xh = xv + E - V - (W - 1);                 // xh[e + k] meets w[k] at token e
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        ssm::pair_t v = bias;
+#pragma unroll
+        for (int k = 0; k < W; ++k) v = ssm::pfma(w[k], xh[e + k], v);
+        if (SILU) v = ssm::psilu(v);
+        const float2 h = ssm::halves(v);
+        o0[e] = h.x;
+        o1[e] = h.y;
+    }
+}
+
 // Role 2: every other token.  A CTA covers tx pieces of a row and walks rows; the 16-byte pieces
 // follow each row's own alignment, so odd row lengths move whole pieces too.  Bit t of `live`
 // says that token t0 + t has its W-1 earlier inputs in its own sequence; it is made once per CTA
 // and serves every row.
-template <typename T, int W>
-__device__ __forceinline__ void sequence_bodies(const PackedConv& p, int64_t bid) {
+template <typename T, int W, bool SILU>
+__device__ __forceinline__ void sequence_bodies(const PackedConv& p, unsigned bid) {
     constexpr int V = 16 / sizeof(T), ES = (int)sizeof(T);
     constexpr int kWords = (kThreads * V + 2 * V + 31) / 32 + 1;
     __shared__ unsigned live[kWords], bad[kWords];
-    const int64_t tile = bid % p.time_tiles, rt = bid / p.time_tiles;
-    const int tx = p.tx, ty = kThreads / tx;
+    __shared__ __align__(16) float2 tap_pairs[kTapRows / 2 * (W + 1)];
+    const unsigned tile = bid % p.time_tiles, rt = bid / p.time_tiles;
+    const int tx = 1 << p.log_tx, ty = kThreads >> p.log_tx;
     const int64_t span = (int64_t)tx * V;
     const int64_t t0 = tile * span - V;                 // token of bit 0: a piece may start up to V-1 tokens early
     const int bits = (int)span + V;
     for (int i = threadIdx.x; i < kWords; i += kThreads) live[i] = bad[i] = 0u;
-    __syncthreads();
-    // sequences that meet [t0, t0 + bits): the bounds rise, so a binary search finds the first.
-    // Bounds out of order mark the wrong tokens at most, each inside the buffer.
-    int64_t a = 0, b = p.n_seq;
-    while (a < b) {
-        const int64_t m = (a + b) / 2;
-        if (__ldg(p.cu + m + 1) <= t0) a = m + 1;
-        else b = m;
+    if (p.aligned && tx >= 32) {
+        const int per = kTapRows / 2 / ty;                        // pairs that a thread row may walk
+        const int64_t d0 = (int64_t)rt * p.rows_per_thread * ty;
+        for (int i = threadIdx.x; i < p.rows_per_thread * ty * (W + 1); i += kThreads) {
+            const int row = i / (W + 1), k = i % (W + 1);
+            const int r = row / ty, y = row % ty;                 // r-th row of thread row y
+            // a pair's second row is its first where the channels end between them
+            int64_t d = d0 + row;
+            if (d >= p.dim) d -= ty;
+            if (d < p.dim) {
+                const float v = k < W ? __ldg(p.w + d * W + k) : p.bias ? __ldg(p.bias + d) : 0.f;
+                float2* q = tap_pairs + (y * per + r / 2) * (W + 1) + k;
+                (r & 1 ? q->y : q->x) = v;
+            }
+        }
     }
+    __syncthreads();
+    // Sequences that meet [t0, t0 + bits).  Up to a few per thread are simply all looked at; with
+    // more, the bounds rise, so a binary search finds the first.  Bounds out of order mark the wrong
+    // tokens at most, each inside the buffer.
+    int64_t a = 0;
+    if (p.n_seq > 4 * kThreads) {
+        int64_t b = p.n_seq;
+        while (a < b) {
+            const int64_t m = (a + b) / 2;
+            if (__ldg(p.cu + m + 1) <= t0) a = m + 1;
+            else b = m;
+        }
+    }
+    bool met_bad = false;
     for (int64_t s = a + threadIdx.x; s < p.n_seq; s += kThreads) {
         const ssm::TokenRange r = ssm::token_range(p.cu, s, p.total);
-        if (r.lo >= t0 + bits) break;
+        if (r.lo >= t0 + bits) {
+            if (p.n_seq > 4 * kThreads) break;
+            continue;
+        }
         const ssm::SlotKind kind = ssm::slot_kind(p.slots ? __ldg(p.slots + s) : (int)s, p.n_slots);
         if (kind == ssm::kSlotPad) continue;
+        met_bad = met_bad || kind == ssm::kSlotBad;
         int64_t lo = r.lo + (W - 1) - t0, hi = r.hi - t0;
         lo = lo < 0 ? 0 : lo;
         hi = hi > bits ? bits : hi;
@@ -185,81 +285,193 @@ __device__ __forceinline__ void sequence_bodies(const PackedConv& p, int64_t bid
             }
         }
     }
-    __syncthreads();
-    const int px = threadIdx.x % tx, py = threadIdx.x / tx;
+    const bool any_bad = __syncthreads_or(met_bad);
+    const int px = threadIdx.x & (tx - 1), py = threadIdx.x >> p.log_tx, lane = threadIdx.x & 31;
     const unsigned char* lo = static_cast<const unsigned char*>(p.x);
     const unsigned char* hi = lo + p.dim * p.total * ES;
-    // out pieces follow out's alignment; where x's differs the inputs are read by elements
-    for (int i = 0; i < p.rows_per_thread; ++i) {
-        const int64_t d = (rt * p.rows_per_thread + i) * ty + py;
-        if (d >= p.dim) break;
-        unsigned char* orow = static_cast<unsigned char*>(p.out) + d * p.total * ES;
-        const unsigned char* xrow = lo + d * p.total * ES;
+    const int64_t row_bytes = p.total * ES;
+    constexpr unsigned sel = (1u << V) - 1u;
+    // the W-1 inputs before a piece, as the 32-bit words that end it: the lane below holds them
+    constexpr int PW = W == 1 ? 0 : sizeof(T) == 4 ? W - 1 : W / 2;
+    const bool edge = px == 0 || lane == 0;
+    const int64_t dr = (int64_t)rt * p.rows_per_thread * ty + py;
+    const int64_t step = ty * row_bytes;
+    if (p.aligned && tx >= 32) {
+        // Every row starts on the 16-byte grid, so one mask serves all rows and a warp's pieces are
+        // of one row.  Lanes behind the last token and rows behind the last one repeat the last
+        // piece and write nothing; so do a row's first tokens, whose earlier inputs sequence_heads has.
+        const int left = ((int)p.dim - (int)dr + ty - 1) >> (31 - __clz(ty));
+        const int rows = left < p.rows_per_thread ? left : p.rows_per_thread;
+        if (rows <= 0) return;
+        int64_t t = tile * span + (int64_t)px * V;
+        const int bit = px * V + V;
+        const unsigned mask = __funnelshift_r(live[bit >> 5], live[(bit >> 5) + 1], bit & 31) & sel;
+        const unsigned nan = any_bad ? __funnelshift_r(bad[bit >> 5], bad[(bit >> 5) + 1], bit & 31) & mask : 0u;
+        const bool whole = __all_sync(0xffffffffu, mask == sel && nan == 0u);
+        if (__all_sync(0xffffffffu, mask == 0u)) return;
+        if (t > p.total - V) t = p.total - V;
+        const bool past = t > 0;
+        // The rows' taps and biases in shared memory, as pairs of the rows that are worked on
+        // together: [pair][tap, then bias] of (row, row + ty), the last of an odd count twice.
+        // (Loaded per row they cost a third of the instructions.)
+        const float2* taps = tap_pairs + py * (kTapRows / 2 / ty) * (W + 1);
+        auto rows_of = [&](auto all_written) {
+            const unsigned char* xp = lo + dr * row_bytes + t * ES;
+            unsigned char* op = static_cast<unsigned char*>(p.out) + dr * row_bytes + t * ES;
+            struct In {
+                uint4 q;
+                uint32_t b[PW > 0 ? PW : 1];                      // the words before (L1: the neighbour's)
+            };
+            auto load = [&](const unsigned char* q) {
+                In in = {};
+                in.q = __ldg(reinterpret_cast<const uint4*>(q));
+                if (PW > 0 && past) {
+                    if constexpr (PW == 2) {
+                        const uint2 v = __ldg(reinterpret_cast<const uint2*>(q) - 1);
+                        in.b[0] = v.x; in.b[1 % PW] = v.y;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < PW; ++k) in.b[k] = __ldg(reinterpret_cast<const uint32_t*>(q) + k - PW);
+                    }
+                }
+                return in;
+            };
+            // two rows at a time, the next two already on their way
+            In next[2] = {load(xp), load(xp + (rows > 1 ? step : 0))};
+            for (int i0 = 0; i0 < rows; i0 += 2, taps += W + 1) {
+                const In cur[2] = {next[0], next[1]};
+                const bool two = i0 + 1 < rows;
+                xp += 2 * step;
+                if (i0 + 2 < rows) {
+                    next[0] = load(xp);
+                    next[1] = load(xp + (i0 + 3 < rows ? step : 0));
+                }
+                uint32_t xw[2][PW + 4];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                    for (int k = 0; k < PW; ++k) xw[r][k] = cur[r].b[k];
+                    xw[r][PW] = cur[r].q.x; xw[r][PW + 1] = cur[r].q.y; xw[r][PW + 2] = cur[r].q.z; xw[r][PW + 3] = cur[r].q.w;
+                }
+                ssm::pair_t w2[W + 1];
+#pragma unroll
+                for (int k = 0; k <= W; ++k) w2[k] = *reinterpret_cast<const ssm::pair_t*>(taps + k);
+                float o0[V], o1[V];
+                conv_pieces<T, W, PW, SILU>(xw[0], xw[1], w2, w2[W], o0, o1);
+                if constexpr (decltype(all_written)::value) {
+                    *reinterpret_cast<uint4*>(op) = pack<T>(o0);
+                    if (two) *reinterpret_cast<uint4*>(op + step) = pack<T>(o1);
+                } else {
+                    store_piece<T>(op, mask, nan, o0);
+                    store_piece<T>(op + step, two ? mask : 0u, nan, o1);
+                }
+                op += 2 * step;
+            }
+        };
+        if (whole) rows_of(std::true_type{});
+        else rows_of(std::false_type{});
+        return;
+    }
+    unsigned char* const out0 = static_cast<unsigned char*>(p.out) + dr * row_bytes;
+    const unsigned char* const x0 = lo + dr * row_bytes;
+    // pieces follow out's 16-byte grid; where x's differs the inputs are read by elements.  Every
+    // lane runs every row (shuffles); rows past the last read nothing.  Several rows' pieces are
+    // loaded before the first is used.
+    constexpr int U = 4;
+    for (int i0 = 0; i0 < p.rows_per_thread; i0 += U) {
+      uint4 piece[U];
+#pragma unroll
+      for (int r = 0; r < U; ++r) {
+        const int i = i0 + r;
+        const bool row_ok = i < p.rows_per_thread && dr + (int64_t)i * ty < p.dim;
+        const unsigned char* orow = out0 + i * step;
+        const int64_t t = tile * span + (int64_t)px * V - (int)((reinterpret_cast<uintptr_t>(orow) & 15u) / ES);
+        const unsigned char* xp = x0 + i * step + t * ES;
+        // neighbours need the piece even where this lane writes nothing
+        if (!row_ok || t >= p.total) {
+            piece[r] = make_uint4(0u, 0u, 0u, 0u);
+        } else if ((reinterpret_cast<uintptr_t>(xp) & 15u) == 0) {
+            piece[r] = load_piece<T>(xp, lo, hi);
+        } else {
+            float v[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const unsigned char* q = xp + e * ES;
+                v[e] = q >= lo && q < hi ? to_f<T>(*reinterpret_cast<const T*>(q)) : 0.f;
+            }
+            piece[r] = pack<T>(v);
+        }
+      }
+      RowPiece<PW> rp[2];
+#pragma unroll
+      for (int r = 0; r < U; ++r) {
+        const int i = i0 + r;
+        const int64_t d = dr + (int64_t)i * ty;
+        const bool row_ok = i < p.rows_per_thread && d < p.dim;
+        unsigned char* orow = out0 + i * step;
         const int m = (int)((reinterpret_cast<uintptr_t>(orow) & 15u) / ES);
         const int64_t t = tile * span + (int64_t)px * V - m;     // first token of the piece
-        const int bit = (int)(t - t0);
-        const unsigned sel = (1u << V) - 1u;
-        const unsigned mask = __funnelshift_r(live[bit >> 5], live[(bit >> 5) + 1], bit & 31) & sel;
-        if (mask == 0u) continue;
-        const unsigned nan = __funnelshift_r(bad[bit >> 5], bad[(bit >> 5) + 1], bit & 31) & mask;
-        float xv[2 * V];                                          // tokens t - V .. t + V - 1
-        const unsigned char* xp = xrow + t * ES;
-        if ((reinterpret_cast<uintptr_t>(xp) & 15u) == 0) {
-            unpack<T>(load_piece<T>(xp - 16, lo, hi), xv);
-            unpack<T>(load_piece<T>(xp, lo, hi), xv + V);
-        } else {
+        const int bit = px * V - m + V;
+        RowPiece<PW>& q = rp[r & 1];
+        q.mask = row_ok ? __funnelshift_r(live[bit >> 5], live[(bit >> 5) + 1], bit & 31) & sel : 0u;
+        q.nan = any_bad ? __funnelshift_r(bad[bit >> 5], bad[(bit >> 5) + 1], bit & 31) & q.mask : 0u;
+        q.out = orow + t * ES;
+        q.d = row_ok ? d : 0;
+        const unsigned char* xp = x0 + i * step + t * ES;
+        uint32_t(&xw)[PW + 4] = q.xw;
+        xw[PW] = piece[r].x; xw[PW + 1] = piece[r].y; xw[PW + 2] = piece[r].z; xw[PW + 3] = piece[r].w;
 #pragma unroll
-            for (int e = 0; e < V + W - 1; ++e) {
-                const unsigned char* q = xp + (e - (W - 1)) * ES;
-                xv[V - (W - 1) + e] = q >= lo && q < hi ? to_f<T>(*reinterpret_cast<const T*>(q)) : 0.f;
+        for (int k = 0; k < PW; ++k) {
+            xw[k] = __shfl_up_sync(0xffffffffu, xw[4 + k], 1);
+            if (edge && q.mask != 0u) {
+                const unsigned char* b = xp + (k - PW) * 4;
+                if constexpr (sizeof(T) == 4) {
+                    xw[k] = b >= lo ? *reinterpret_cast<const uint32_t*>(b) : 0u;
+                } else {
+                    const uint32_t b0 = b >= lo ? *reinterpret_cast<const unsigned short*>(b) : 0u;
+                    const uint32_t b1 = b + 2 >= lo ? *reinterpret_cast<const unsigned short*>(b + 2) : 0u;
+                    xw[k] = b0 | b1 << 16;
+                }
             }
         }
-        float w[W];
+        if ((r & 1) && (rp[0].mask | rp[1].mask) != 0u) {
+            float wa[W], wb[W], o0[V], o1[V];
+            ssm::pair_t w[W];
+            load_taps<T, W>(p, rp[0].d, wa);
+            load_taps<T, W>(p, rp[1].d, wb);
 #pragma unroll
-        for (int k = 0; k < W; ++k) w[k] = __ldg(p.w + d * W + k);
-        const float bs = p.bias ? __ldg(p.bias + d) : 0.f;
-        float o[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            float v = bs;
-#pragma unroll
-            for (int k = 0; k < W; ++k) v = fmaf(w[k], xv[V + e - (W - 1) + k], v);
-            o[e] = p.silu ? ssm::silu1(v) : v;
-            if ((nan >> e) & 1u) o[e] = __int_as_float(0x7FC00000);
+            for (int k = 0; k < W; ++k) w[k] = ssm::pk(wa[k], wb[k]);
+            const ssm::pair_t bias = p.bias ? ssm::pk(__ldg(p.bias + rp[0].d), __ldg(p.bias + rp[1].d)) : ssm::pk(0.f);
+            conv_pieces<T, W, PW, SILU>(rp[0].xw, rp[1].xw, w, bias, o0, o1);
+            store_piece<T>(rp[0].out, rp[0].mask, rp[0].nan, o0);
+            store_piece<T>(rp[1].out, rp[1].mask, rp[1].nan, o1);
         }
-        if (mask == sel) {
-            *reinterpret_cast<uint4*>(orow + t * ES) = pack<T>(o);
-        } else {
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                if ((mask >> e) & 1u) reinterpret_cast<T*>(orow)[t + e] = from_f<T>(o[e]);
-        }
+      }
     }
 }
 
-template <typename T, int W>
-__global__ void __launch_bounds__(kThreads) conv1d_packed_kernel(const PackedConv p) {
-    if (blockIdx.x < p.head_ctas) sequence_heads<T, W>(p, blockIdx.x);
-    else sequence_bodies<T, W>(p, blockIdx.x - p.head_ctas);
-}
-
-// width 1: no history, so role 1 has nothing to do
-template <typename T>
-__global__ void __launch_bounds__(kThreads) conv1d_packed_kernel_w1(const PackedConv p) {
-    sequence_bodies<T, 1>(p, blockIdx.x);
+template <typename T, int W, bool SILU>
+__global__ void __launch_bounds__(kThreads, 4) conv1d_packed_kernel(const PackedConv p) {
+    if constexpr (W > 1) {                              // width 1 keeps no history
+        if (blockIdx.x < p.head_ctas) {
+            sequence_heads<T, W>(p, blockIdx.x);
+            return;
+        }
+    }
+    sequence_bodies<T, W, SILU>(p, blockIdx.x - (unsigned)p.head_ctas);
 }
 
 template <typename T, int W>
 int launch_packed(PackedConv p, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
     const int64_t pieces = (p.total + V - 1 + V - 1) / V;   // of a row, its first one up to V-1 tokens early
-    p.tx = 16;
-    while (p.tx < 128 && p.tx < pieces) p.tx *= 2;
-    const int ty = kThreads / p.tx;
-    const int64_t tt = p.total > 0 ? (pieces + p.tx - 1) / p.tx : 0;
+    p.log_tx = 4;
+    while (p.log_tx < 7 && 1 << p.log_tx < pieces) ++p.log_tx;
+    const int tx = 1 << p.log_tx, ty = kThreads / tx;
+    const int64_t tt = p.total > 0 ? (pieces + tx - 1) / tx : 0;
     // enough rows per CTA to carry the making of the mask, as long as 8 CTAs per SM remain
-    int rows = 1;
-    while (rows < 16 && tt * ((p.dim + ty - 1) / ty) / (2 * rows) >= 148 * 8) rows *= 2;
+    int rows = 4;
+    while (rows * ty < kTapRows && rows < 64 && tt * ((p.dim + ty - 1) / ty) / (2 * rows) >= 148 * 8) rows *= 2;
     p.rows_per_thread = rows;
     const int64_t rtiles = (p.dim + (int64_t)ty * rows - 1) / ((int64_t)ty * rows);
     const int64_t head_tiles = (p.dim + kThreads - 1) / kThreads;
@@ -269,8 +481,8 @@ int launch_packed(PackedConv p, cudaStream_t s) {
     if (ctas == 0) return SSM_OK;
     p.head_tiles = (unsigned)head_tiles;
     p.time_tiles = (unsigned)(tt > 0 ? tt : 1);
-    if constexpr (W > 1) conv1d_packed_kernel<T, W><<<(unsigned)ctas, kThreads, 0, s>>>(p);
-    else conv1d_packed_kernel_w1<T><<<(unsigned)ctas, kThreads, 0, s>>>(p);
+    if (p.silu) conv1d_packed_kernel<T, W, true><<<(unsigned)ctas, kThreads, 0, s>>>(p);
+    else conv1d_packed_kernel<T, W, false><<<(unsigned)ctas, kThreads, 0, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }
 
@@ -295,6 +507,7 @@ struct TokenConv {
     const int* slots;
     int64_t batch, dim, n_slots, slot_stride;
     int silu;
+    int w_vec;
 };
 
 // C channels per thread, of one row: 16 bytes of x and out and W-1 times 16 bytes of the slot
@@ -303,6 +516,20 @@ template <typename T, int W, int C>
 __global__ void __launch_bounds__(128) conv1d_update_kernel(const TokenConv p) {
     const int64_t d = ((int64_t)blockIdx.x * 128 + threadIdx.x) * C;
     if (d >= p.dim) return;
+    // the taps and the bias of the thread's channels, ahead of the slot's chain of loads
+    float w[C * W], bias[C];
+    if (C * W % 4 == 0 && p.w_vec) {
+#pragma unroll
+        for (int k = 0; k < C * W; k += 4) {
+            const float4 q = __ldg(reinterpret_cast<const float4*>(p.w + d * W + k));
+            w[k] = q.x; w[(k + 1) % (C * W)] = q.y; w[(k + 2) % (C * W)] = q.z; w[(k + 3) % (C * W)] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < C * W; ++k) w[k] = __ldg(p.w + d * W + k);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) bias[c] = p.bias ? __ldg(p.bias + d + c) : 0.f;
     for (int64_t b = blockIdx.y; b < p.batch; b += gridDim.y) {
         const int slot = p.slots ? __ldg(p.slots + b) : (int)b;
         const ssm::SlotKind kind = ssm::slot_kind(slot, p.n_slots);
@@ -331,11 +558,10 @@ __global__ void __launch_bounds__(128) conv1d_update_kernel(const TokenConv p) {
         }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const float* wr = p.w + (d + c) * W;
-            float v = p.bias ? __ldg(p.bias + d + c) : 0.f;
+            float v = bias[c];
 #pragma unroll
-            for (int k = 0; k < W - 1; ++k) v = fmaf(__ldg(wr + k), h[c * (W - 1) + k], v);
-            v = fmaf(__ldg(wr + W - 1), x[c], v);
+            for (int k = 0; k < W - 1; ++k) v = fmaf(w[c * W + k], h[c * (W - 1) + k], v);
+            v = fmaf(w[c * W + W - 1], x[c], v);
             o[c] = p.silu ? ssm::silu1(v) : v;
             if (kind == ssm::kSlotBad) o[c] = __int_as_float(0x7FC00000);
         }
@@ -409,6 +635,8 @@ extern "C" int ssm_causal_conv1d_packed_fwd(int64_t dim, int64_t total, int64_t 
     p.cu = cu_seqlens; p.slots = slots; p.has_state = has_state;
     p.dim = dim; p.total = total; p.n_seq = n_seq; p.n_slots = n_slots; p.slot_stride = slot_stride;
     p.silu = silu ? 1 : 0;
+    p.w_vec = aligned_to(w, 16);
+    p.aligned = total * (int64_t)esz % 16 == 0 && aligned_to(x, 16) && aligned_to(out, 16);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return io_dtype == SSM_BF16 ? launch_packed_t<__nv_bfloat16>(p, width, s) : launch_packed_t<float>(p, width, s);
 }
@@ -430,6 +658,7 @@ extern "C" int ssm_causal_conv1d_update(int64_t batch, int64_t dim, int32_t widt
     TokenConv p{};
     p.x = x; p.w = w; p.bias = bias; p.out = out; p.states = states; p.slots = slots;
     p.batch = batch; p.dim = dim; p.n_slots = n_slots; p.slot_stride = slot_stride; p.silu = silu ? 1 : 0;
+    p.w_vec = aligned_to(w, 16);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return io_dtype == SSM_BF16 ? launch_update_t<__nv_bfloat16>(p, width, vec, s)
                                 : launch_update_t<float>(p, width, vec, s);

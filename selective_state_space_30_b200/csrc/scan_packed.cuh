@@ -58,24 +58,33 @@ struct PackedParams {
 
 template <typename T, int N, bool HEAD, bool ALIGNED>
 struct PackedCfg {
+    static constexpr bool kAligned = ALIGNED;
     static constexpr int ESZ = sizeof(T);
     static constexpr int V = 16 / ESZ;                  // elements per 16-byte piece
-    static constexpr int TB = 64 / ESZ;                 // steps per block
-    static constexpr int S = 8;                         // states per lane
+    static constexpr int RB = 64;                       // bytes of a row's block
+    static constexpr int TB = RB / ESZ;                 // steps per block
+    static constexpr int S = N <= 32 ? 4 : 8;                   // states per lane
     static constexpr int TPC = N / S;                   // lanes per channel
     static constexpr int CPL = N == 128 ? 4 : 2;        // channels per lane
     static constexpr int LG = 32 / TPC;                 // lane groups of a warp
     static constexpr int CW = LG * CPL;                 // channels per warp
-    static constexpr int W = N == 8 ? 2 : 4;            // warps
+    static constexpr int W = N == 8 ? 2 : 4;  // warps
     static constexpr int CT = W * CW;                   // channels per tile
     static constexpr int NT = 32 * W;
+    static constexpr int CTAS = N <= 32 ? 4 : 2;        // per SM, at least
     static constexpr int WT = CPL * 4 >= TPC ? 4 : 8;   // steps per window
-    static constexpr int PIECES = ALIGNED ? 4 : 5;      // 16-byte pieces that hold a row's block
-    static constexpr int PITCH = 80;                    // bytes of a staged row: five pieces, so rows start in different banks
+    static constexpr int PA = RB / 16;                  // 16-byte pieces of a row's block
+    static constexpr int PIECES = ALIGNED ? PA : PA + 1;    // that hold it
+    // bytes of a staged row.  Eight rows' pieces read at once have to lie in different banks:
+    // aligned rows swap their pieces by bits of the row, the others are an odd number of pieces long
+    static constexpr int PITCH = ALIGNED ? RB : RB + 16;
+    __device__ static constexpr int piece_off(int row, int piece) {
+        return row * PITCH + (ALIGNED ? piece ^ (row >> 1 & 3) : piece) * 16;
+    }
     static constexpr int R_U = 0, R_Z = CT, R_DT = 2 * CT, R_B = 3 * CT, R_C = 3 * CT + N, ROWS = 3 * CT + 2 * N;
     static constexpr int STAGE = ROWS * PITCH;
     // steps of a prologue or epilogue item (one channel's)
-    static constexpr int PS = CW * TB / 8 >= 32 ? 8 : 4;
+    static constexpr int PS = CW * TB >= 256 ? 8 : 4;
     static constexpr int ITEMS = CW * TB / PS / 32;     // per lane
     static constexpr int OFF_BC = 2 * STAGE;            // fp32 [step][B of all states | C of all states]
     static constexpr int OFF_Q = OFF_BC + TB * 2 * N * 4;   // per warp: [step][channel] (dt or decay, dt u), then y
@@ -98,32 +107,34 @@ template <typename T> __device__ __forceinline__ int skew(const void* p) {
     return (int)((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
 }
 
-// CNT elements of a staged row, from element e on.
-template <typename T, bool ALIGNED, int CNT>
-__device__ __forceinline__ void read_row(const unsigned char* row, int e, float (&v)[CNT]) {
-    if constexpr (sizeof(T) == 4) {
-        if constexpr (ALIGNED) {
+// CNT elements of a staged row, from element e on (aligned: a multiple of CNT).
+template <class Cf, int CNT>
+__device__ __forceinline__ void read_row(const unsigned char* stage, int row, int e, float (&v)[CNT]) {
+    constexpr int V = Cf::V;
+    if constexpr (Cf::ESZ == 4) {
+        if constexpr (Cf::kAligned) {
 #pragma unroll
             for (int i = 0; i < CNT; i += 4) {
-                const float4 q = *reinterpret_cast<const float4*>(row + (e + i) * 4);
+                const float4 q = *reinterpret_cast<const float4*>(stage + Cf::piece_off(row, (e + i) / V));
                 v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < CNT; ++i) v[i] = *reinterpret_cast<const float*>(row + (e + i) * 4);
+            for (int i = 0; i < CNT; ++i) v[i] = *reinterpret_cast<const float*>(stage + Cf::piece_off(row, 0) + (e + i) * 4);
         }
     } else {
         uint32_t w[CNT / 2];
-        if constexpr (ALIGNED) {
+        if constexpr (Cf::kAligned) {
+            const unsigned char* p = stage + Cf::piece_off(row, e / V);
             if constexpr (CNT == 8) {
-                const uint4 q = *reinterpret_cast<const uint4*>(row + e * 2);
+                const uint4 q = *reinterpret_cast<const uint4*>(p);
                 w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
             } else {
-                const uint2 q = *reinterpret_cast<const uint2*>(row + e * 2);
+                const uint2 q = *reinterpret_cast<const uint2*>(p + e % V * 2);
                 w[0] = q.x; w[1] = q.y;
             }
         } else {
-            const uint32_t* p = reinterpret_cast<const uint32_t*>(row + ((e * 2) & ~3));
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(stage + Cf::piece_off(row, 0) + ((e * 2) & ~3));
             const int sh = (e & 1) * 16;
             uint32_t lo = p[0];
 #pragma unroll
@@ -141,16 +152,17 @@ __device__ __forceinline__ void read_row(const unsigned char* row, int e, float 
     }
 }
 
-template <typename T, bool ALIGNED, int CNT>
-__device__ __forceinline__ void write_row(unsigned char* row, int e, const float (&v)[CNT]) {
-    if constexpr (sizeof(T) == 4) {
-        if constexpr (ALIGNED) {
+template <class Cf, int CNT>
+__device__ __forceinline__ void write_row(unsigned char* stage, int row, int e, const float (&v)[CNT]) {
+    constexpr int V = Cf::V;
+    if constexpr (Cf::ESZ == 4) {
+        if constexpr (Cf::kAligned) {
 #pragma unroll
             for (int i = 0; i < CNT; i += 4)
-                *reinterpret_cast<float4*>(row + (e + i) * 4) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                *reinterpret_cast<float4*>(stage + Cf::piece_off(row, (e + i) / V)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         } else {
 #pragma unroll
-            for (int i = 0; i < CNT; ++i) *reinterpret_cast<float*>(row + (e + i) * 4) = v[i];
+            for (int i = 0; i < CNT; ++i) *reinterpret_cast<float*>(stage + Cf::piece_off(row, 0) + (e + i) * 4) = v[i];
         }
     } else {
         uint32_t w[CNT / 2];
@@ -159,13 +171,14 @@ __device__ __forceinline__ void write_row(unsigned char* row, int e, const float
             const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
             w[i] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        if constexpr (ALIGNED) {
-            if constexpr (CNT == 8) *reinterpret_cast<uint4*>(row + e * 2) = make_uint4(w[0], w[1], w[2], w[3]);
-            else *reinterpret_cast<uint2*>(row + e * 2) = make_uint2(w[0], w[1]);
+        if constexpr (Cf::kAligned) {
+            unsigned char* p = stage + Cf::piece_off(row, e / V);
+            if constexpr (CNT == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+            else *reinterpret_cast<uint2*>(p + e % V * 2) = make_uint2(w[0], w[1]);
         } else {
+            unsigned short* p = reinterpret_cast<unsigned short*>(stage + Cf::piece_off(row, 0)) + e;
 #pragma unroll
-            for (int i = 0; i < CNT; ++i)
-                *reinterpret_cast<unsigned short*>(row + (e + i) * 2) = (unsigned short)(w[i / 2] >> (16 * (i & 1)));
+            for (int i = 0; i < CNT; ++i) p[i] = (unsigned short)(w[i / 2] >> (16 * (i & 1)));
         }
     }
 }
@@ -187,7 +200,7 @@ template <typename T, int N, bool HEAD, bool ALIGNED, bool LOCAL>
 __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk, unsigned char* smem) {
     using Cf = PackedCfg<T, N, HEAD, ALIGNED>;
     constexpr int S = Cf::S, TPC = Cf::TPC, CPL = Cf::CPL, CW = Cf::CW, CT = Cf::CT, TB = Cf::TB, V = Cf::V;
-    constexpr int ESZ = Cf::ESZ, NT = Cf::NT, PITCH = Cf::PITCH, WT = Cf::WT, PS = Cf::PS;
+    constexpr int ESZ = Cf::ESZ, NT = Cf::NT, WT = Cf::WT, PS = Cf::PS;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int lg = lane / TPC, j = lane % TPC;
     const int64_t L = p.total;
@@ -217,14 +230,15 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
     // is cut.
     auto stage_rows = [&](int stage, int r0, const unsigned char* base, int rows, int64_t tb, const unsigned char* lo,
                           const unsigned char* hi) {
-        unsigned char* sb = smem + stage * Cf::STAGE + r0 * PITCH;
+        unsigned char* sb = smem + stage * Cf::STAGE;
         if constexpr (ALIGNED) {
-            const int g = tid & 3;
+            const int g = tid % Cf::PA;
             const int64_t ts = tb + g * V;
             if (ts < tk.t1 && ts + V > tk.t0) {
-                const unsigned dst = ssm::smem_u32(sb + g * 16);
+                const unsigned dst = ssm::smem_u32(sb);
                 const unsigned char* src = base + ts * ESZ;
-                for (int r = tid >> 2; r < rows; r += NT / 4) cp16(dst + r * PITCH, src + (int64_t)r * L * ESZ, 16);
+                for (int r = tid / Cf::PA; r < rows; r += NT / Cf::PA)
+                    cp16(dst + Cf::piece_off(r0 + r, g), src + (int64_t)r * L * ESZ, 16);
             }
         } else {
             for (int i = tid; i < rows * Cf::PIECES; i += NT) {
@@ -234,7 +248,7 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
                 const int64_t ts = tb + g * V - m;
                 if (ts < tk.t1 && ts + V > tk.t0) {
                     const unsigned char* src = row + ts * ESZ;
-                    unsigned char* dst = sb + r * PITCH + g * 16;
+                    unsigned char* dst = sb + Cf::piece_off(r0 + r, g);
                     if (src >= lo) {
                         const int64_t left = hi - src;
                         cp16(ssm::smem_u32(dst), src, left < 16 ? (int)left : 16);
@@ -335,6 +349,7 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
         // the chunk's steps of the block: [lo, hi)
         const int lo = tk.t0 > tb ? (int)(tk.t0 - tb) : 0;
         const int hi = tk.t1 - tb < TB ? (int)(tk.t1 - tb) : TB;
+        const bool whole = lo == 0 && hi == TB;
         unsigned char* sb = smem + (kb & 1) * Cf::STAGE;
         cp_wait_all();
         __syncthreads();   // the block is staged, and every warp is done with the block before
@@ -348,9 +363,9 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
             const unsigned char* src = r < N ? Bb : Cb;
             const int m = ALIGNED ? 0 : skew<T>(src + (int64_t)(r < N ? r : r - N) * L * ESZ);
             float v[CV];
-            read_row<T, ALIGNED, CV>(sb + (Cf::R_B + r) * PITCH, m + e0, v);
+            read_row<Cf, CV>(sb, Cf::R_B + r, m + e0, v);
 #pragma unroll
-            for (int e = 0; e < CV; ++e) bc[(e0 + e) * 2 * N + r] = e0 + e >= lo && e0 + e < hi ? v[e] : 0.f;
+            for (int e = 0; e < CV; ++e) bc[(e0 + e) * 2 * N + r] = whole || (e0 + e >= lo && e0 + e < hi) ? v[e] : 0.f;
         }
         // prologue: dt (or the decay) and dt u of the warp's channels
 #pragma unroll
@@ -362,8 +377,8 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
             float x[PS], uv[PS];
             const int mu = ALIGNED ? 0 : skew<T>(ub + (int64_t)lc * L * ESZ);
             const int md = ALIGNED ? 0 : skew<T>(db + (int64_t)dr * L * ESZ);
-            read_row<T, ALIGNED, PS>(sb + (Cf::R_U + lc) * PITCH, mu + e0, uv);
-            read_row<T, ALIGNED, PS>(sb + (Cf::R_DT + dr) * PITCH, md + e0, x);
+            read_row<Cf, PS>(sb, Cf::R_U + lc, mu + e0, uv);
+            read_row<Cf, PS>(sb, Cf::R_DT + dr, md + e0, x);
             const float bias = s_bias[lc];
             const float ah = HEAD ? s_a[lc] : 0.f;
 #pragma unroll
@@ -371,9 +386,11 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
                 const float2 xb = add2(make_float2(x[e], x[e + 1]), dup2(bias));
                 float2 dt = p.softplus ? ssm::softplus2(xb) : xb;
                 float2 du = mul2(dt, make_float2(uv[e], uv[e + 1]));
-                // steps outside the chunk: no decay, no input
-                if (!(e0 + e >= lo && e0 + e < hi)) { dt.x = 0.f; du.x = 0.f; }
-                if (!(e0 + e + 1 >= lo && e0 + e + 1 < hi)) { dt.y = 0.f; du.y = 0.f; }
+                if (!whole) {
+                    // steps outside the chunk: no decay, no input
+                    if (!(e0 + e >= lo && e0 + e < hi)) { dt.x = 0.f; du.x = 0.f; }
+                    if (!(e0 + e + 1 >= lo && e0 + e + 1 < hi)) { dt.y = 0.f; du.y = 0.f; }
+                }
                 if constexpr (HEAD) dt = make_float2(ex2_approx(dt.x * ah), ex2_approx(dt.y * ah));
                 q[(e0 + e) * CW + c] = make_float2(dt.x, du.x);
                 q[(e0 + e + 1) * CW + c] = make_float2(dt.y, du.y);
@@ -456,8 +473,8 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
                 const int lc = warp * CW + c;
                 const int64_t ro = (int64_t)lc * L * ESZ;
                 float uv[PS], zv[PS], o[PS];
-                read_row<T, ALIGNED, PS>(sb + (Cf::R_U + lc) * PITCH, (ALIGNED ? 0 : skew<T>(ub + ro)) + e0, uv);
-                if (zb) read_row<T, ALIGNED, PS>(sb + (Cf::R_Z + lc) * PITCH, (ALIGNED ? 0 : skew<T>(zb + ro)) + e0, zv);
+                read_row<Cf, PS>(sb, Cf::R_U + lc, (ALIGNED ? 0 : skew<T>(ub + ro)) + e0, uv);
+                if (zb) read_row<Cf, PS>(sb, Cf::R_Z + lc, (ALIGNED ? 0 : skew<T>(zb + ro)) + e0, zv);
                 const float2 D2 = dup2(s_D[lc]);
 #pragma unroll
                 for (int e = 0; e < PS; e += 2) {
@@ -467,7 +484,7 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
                     o[e] = y.x;
                     o[e + 1] = y.y;
                 }
-                write_row<T, ALIGNED, PS>(sb + (Cf::R_DT + lc) * PITCH, (ALIGNED ? 0 : skew<T>(ob + ro)) + e0, o);
+                write_row<Cf, PS>(sb, Cf::R_DT + lc, (ALIGNED ? 0 : skew<T>(ob + ro)) + e0, o);
             }
             __syncwarp();
             // to global memory, a row's pieces on neighbouring lanes
@@ -476,7 +493,7 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
                 if (lc >= tk.nch) continue;
                 unsigned char* row = ob + (int64_t)lc * L * ESZ;
                 const int e0 = g * V - (ALIGNED ? 0 : skew<T>(row));     // first step of the piece
-                const unsigned char* src = sb + (Cf::R_DT + lc) * PITCH + g * 16;
+                const unsigned char* src = sb + Cf::piece_off(Cf::R_DT + lc, g);
                 unsigned char* dst = row + (tb + e0) * ESZ;
                 if (e0 >= lo && e0 + V <= hi) {
                     *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
@@ -513,19 +530,43 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
     }
 }
 
-// Finds the sequence that holds chunk x (each sequence has ceil(length / chunk) chunks, at least
-// one).  Returns false behind the last chunk.  All threads of the CTA call it.
-__device__ __forceinline__ bool find_chunk(const PackedParams& p, int64_t x, int64_t* sh, int nt, int64_t& seq, int64_t& k) {
-    // sh: [0] sequence, [1] chunk, [2] chunks before, [4 ..] warp sums
+// Finds the x-th work item of the call; all threads of the CTA call it.  Returns false behind the
+// last one.  Items go by sequence, the long ones first so that no long one starts last: sequences
+// are ranked by the bucket of their length (two per octave) and within it by number.  Cut
+// sequences have ceil(length / chunk) items each, at least one, and keep their own order, which
+// their chunks' places in the workspace follow.
+__device__ __forceinline__ bool find_item(const PackedParams& p, int64_t x, int64_t* sh, int nt, int64_t& seq, int64_t& k) {
+    // sh: [0] sequence, [1] item of it, [2 ..] warp sums, [8 ..] counts of the buckets
+    constexpr int kBuckets = 64;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt / 32;
+    const bool cut = p.chunk > 0;
+    unsigned* count = reinterpret_cast<unsigned*>(sh + 2 + 32);
+    auto bucket = [&](int64_t len) {
+        if (len <= 0) return kBuckets - 1;
+        const int e = 31 - __clz((int)len);
+        const int half = e > 0 ? (int)(len >> (e - 1)) & 1 : 0;
+        return kBuckets - 2 - 2 * e - half;             // the longest come first
+    };
+    int want = 0;
+    if (!cut && p.n_seq > 1) {
+        for (int i = tid; i < kBuckets; i += nt) count[i] = 0u;
+        __syncthreads();
+        for (int64_t i = tid; i < p.n_seq; i += nt) {
+            const TokenRange r = token_range(p.cu, i, p.total);
+            atomicAdd(count + bucket(r.hi - r.lo), 1u);
+        }
+        __syncthreads();
+        while (want < kBuckets - 1 && x >= (int64_t)count[want]) x -= count[want++];
+    }
     int64_t before = 0;
     if (tid == 0) sh[0] = -1;
     for (int64_t i0 = 0; i0 < p.n_seq; i0 += nt) {
         const int64_t i = i0 + tid;
         int64_t n = 0;
         if (i < p.n_seq) {
-            const ssm::TokenRange r = ssm::token_range(p.cu, i, p.total);
-            n = r.hi > r.lo ? (r.hi - r.lo + p.chunk - 1) / p.chunk : 1;
+            const TokenRange r = token_range(p.cu, i, p.total);
+            const int64_t len = r.hi - r.lo;
+            n = cut ? (len > 0 ? (len + p.chunk - 1) / p.chunk : 1) : p.n_seq == 1 || bucket(len) == want;
         }
         int64_t inc = n;
 #pragma unroll
@@ -534,12 +575,12 @@ __device__ __forceinline__ bool find_chunk(const PackedParams& p, int64_t x, int
             if (lane >= m) inc += v;
         }
         __syncthreads();
-        if (lane == 31) sh[4 + warp] = inc;
+        if (lane == 31) sh[2 + warp] = inc;
         __syncthreads();
         int64_t base = before, all = before;
         for (int w = 0; w < nw; ++w) {
-            if (w < warp) base += sh[4 + w];
-            all += sh[4 + w];
+            if (w < warp) base += sh[2 + w];
+            all += sh[2 + w];
         }
         if (n > 0 && x >= base + inc - n && x < base + inc) {
             sh[0] = i;
@@ -555,7 +596,7 @@ __device__ __forceinline__ bool find_chunk(const PackedParams& p, int64_t x, int
 }
 
 template <typename T, int N, bool HEAD, bool ALIGNED>
-__global__ void __launch_bounds__(PackedCfg<T, N, HEAD, ALIGNED>::NT)
+__global__ void __launch_bounds__(PackedCfg<T, N, HEAD, ALIGNED>::NT, PackedCfg<T, N, HEAD, ALIGNED>::CTAS)
 scan_packed_kernel(const PackedParams p) {
     using Cf = PackedCfg<T, N, HEAD, ALIGNED>;
     extern __shared__ __align__(16) unsigned char packed_smem[];
@@ -567,11 +608,10 @@ scan_packed_kernel(const PackedParams p) {
     tk.ci0 = (int64_t)(tile % p.tiles_per_group) * Cf::CT;
     tk.d0 = tk.g * p.group_dim + tk.ci0;
     tk.nch = (int)(p.group_dim - tk.ci0 < Cf::CT ? p.group_dim - tk.ci0 : Cf::CT);
-    int64_t seq = x;
-    tk.k = 0;
+    int64_t seq;
     tk.chunk_id = x;
-    if (p.chunk > 0 && !find_chunk(p, x, reinterpret_cast<int64_t*>(smem), Cf::NT, seq, tk.k)) return;
-    const ssm::TokenRange r = ssm::token_range(p.cu, seq, p.total);
+    if (!find_item(p, x, reinterpret_cast<int64_t*>(smem), Cf::NT, seq, tk.k)) return;
+    const TokenRange r = token_range(p.cu, seq, p.total);
     tk.t0 = r.lo + tk.k * p.chunk;
     tk.t1 = p.chunk > 0 && r.hi - tk.t0 > p.chunk ? tk.t0 + p.chunk : r.hi;
     tk.last = tk.t1 == r.hi;

@@ -18,7 +18,10 @@
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kStage = 96 * 1024;      // bytes of shared memory a CTA stages at most: two CTAs per SM
+// Bytes a CTA stages at most where its pairs' 16-byte pieces fit in as many: with 32 KB seven CTAs
+// fit an SM, whose reads and writes overlap
+constexpr int kStage = 32 * 1024;
+constexpr int kStageMost = 192 * 1024;
 constexpr int kMaxPairs = 4096;
 constexpr int kMaxSlice = 4096;
 
@@ -40,25 +43,26 @@ __global__ void __launch_bounds__(kThreads) slots_copy_kernel(const CopyParams p
     unsigned char* base = p.pool + layer * p.layer_stride + c0;
     const int bytes = (int)(p.slot_bytes - c0 < p.slice ? p.slot_bytes - c0 : p.slice);
     const int n = bytes / 16, pitch = p.slice;
-    for (int i = threadIdx.x; i < p.n_pairs * n; i += kThreads) {
-        const int pr = i / n, q = i % n;
+    // lanes side by side along a slice (a power of two of them), pairs across
+    const int lanes = p.slice / 16, q = threadIdx.x & (lanes - 1);
+    const int first = q < n ? threadIdx.x / lanes : p.n_pairs, step = kThreads / lanes;
+    base += q * 16;
+    uint4* mine = reinterpret_cast<uint4*>(stage) + q;
+    for (int pr = first; pr < p.n_pairs; pr += step) {
         const int s = __ldg(p.src + pr);
-        uint4* to = reinterpret_cast<uint4*>(stage + pr * pitch) + q;
+        uint4* to = mine + pr * (pitch / 16);
         if (s >= 0 && s < p.n_slots)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ssm::smem_u32(to)),
-                         "l"(base + s * p.slot_stride + q * 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ssm::smem_u32(to)), "l"(base + s * p.slot_stride)
                          : "memory");
         else
             *to = make_uint4(0u, 0u, 0u, 0u);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    for (int i = threadIdx.x; i < p.n_pairs * n; i += kThreads) {
-        const int pr = i / n, q = i % n;
+    for (int pr = first; pr < p.n_pairs; pr += step) {
         const int s = __ldg(p.src + pr), d = __ldg(p.dst + pr);
         if (d >= 0 && d < p.n_slots && s < p.n_slots)
-            *reinterpret_cast<uint4*>(base + d * p.slot_stride + q * 16) =
-                *(reinterpret_cast<const uint4*>(stage + pr * pitch) + q);
+            *reinterpret_cast<uint4*>(base + d * p.slot_stride) = *(mine + pr * (pitch / 16));
     }
 }
 
@@ -150,7 +154,7 @@ extern "C" int ssm_state_slots_copy(void* pool, int64_t n_layers, int64_t n_slot
     const int extra = vec ? 0 : 16;
     int slice = kMaxSlice;
     while (slice > 16 && (slice + extra) * n_pairs > kStage) slice /= 2;
-    if ((slice + extra) * n_pairs > 2 * kStage) return SSM_ERR_UNSUPPORTED;
+    if ((slice + extra) * n_pairs > kStageMost) return SSM_ERR_UNSUPPORTED;
     while (slice > 512 && n_layers * ((slot_bytes + slice - 1) / slice) < 148 * 4) slice /= 2;
     p.slice = slice;
     p.slices = (slot_bytes + slice - 1) / slice;
@@ -159,11 +163,11 @@ extern "C" int ssm_state_slots_copy(void* pool, int64_t n_layers, int64_t n_slot
     const int smem = (int)((slice + extra) * n_pairs);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (vec) {
-        if (cudaFuncSetAttribute(slots_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kStage) != cudaSuccess)
+        if (cudaFuncSetAttribute(slots_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageMost) != cudaSuccess)
             return SSM_ERR_CUDA;
         slots_copy_kernel<<<(unsigned)ctas, kThreads, smem, s>>>(p);
     } else {
-        if (cudaFuncSetAttribute(slots_copy_bytes_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kStage) !=
+        if (cudaFuncSetAttribute(slots_copy_bytes_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageMost) !=
             cudaSuccess)
             return SSM_ERR_CUDA;
         const unsigned char* lo = p.pool;

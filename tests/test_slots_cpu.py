@@ -77,7 +77,7 @@ def test_scan_packed_refusals(ssm):
     size = ssm.ssm_selective_scan_packed_workspace_size
     long = dims(batch=1, total=4096)
     need = size(long)
-    assert need >= 4096 // 512 * 32 * 17 * 4
+    assert need >= 4096 // 256 * 32 * 17 * 4
     assert size(long, 200) == 0 and size(dims()) == 0 and size(long, 4096) == need
     assert rc(dims=long) == ssm.SSM_ERR_INVALID_ARG
     assert rc(dims=long, ws=A16, nws=need - 1) == ssm.SSM_ERR_INVALID_ARG
@@ -162,25 +162,29 @@ def test_front_end_refusals(ssm):
 
 def test_tensor_checks():
     import torch
-    from selective_state_space_30_b200._tensors import inner_contiguous, io_code, need, need_pool
-    t = torch.zeros(4, 6)
-    need("t", None, torch.float32, (1,), t.device)
-    need("t", t, torch.float32, (4, 6), t.device)
-    for args, word in (((torch.float64, (4, 6)), "float64"), ((torch.float32, (6, 4)), "shape")):
+    from selective_state_space_30_b200._tensors import inner_contiguous, io_code, need, pool_stride
+    t, f32 = torch.zeros(4, 6), torch.float32
+    here = t.get_device()          # -1: the checks of a device go by its number
+    need("t", None, f32, (1,), here)
+    need("t", t, f32, (4, 6), here)
+    for dtype, shape, word in ((torch.float64, (4, 6), "float64"), (f32, (6, 4), "shape")):
         with pytest.raises(ValueError, match=word):
-            need("t", t, *args, t.device)
+            need("t", t, dtype, shape, here)
     with pytest.raises(ValueError, match="contiguous"):
-        need("t", t.t(), torch.float32, (6, 4), t.device)
-    with pytest.raises(ValueError, match="on meta"):
-        need("t", t, torch.float32, (4, 6), torch.device("meta"))
+        need("t", t.t(), f32, (6, 4), here)
+    with pytest.raises(ValueError, match="cuda:1"):
+        need("t", t, f32, (4, 6), 1)
     with pytest.raises(ValueError):
         io_code(t.double())
-    pool = torch.zeros(5, 4, 10)[:, :, :6]
-    with pytest.raises(ValueError, match="slot of p"):
-        need_pool("p", pool, torch.float32, (4, 6), t.device)
-    apart = torch.zeros(5, 40)[:, :24].view(5, 4, 6)
-    need_pool("p", apart, torch.float32, (4, 6), t.device)
-    assert inner_contiguous(torch.zeros(3, 5, 4).transpose(0, 1), 2) and not inner_contiguous(pool, 1)
+    assert pool_stride("p", torch.zeros(5, 4, 6), f32, 4, 6, here) == 24
+    assert pool_stride("p", torch.zeros(5, 40)[:, :24].view(5, 4, 6), f32, 4, 6, here) == 40
+    assert pool_stride("p", torch.zeros(1, 40)[:, :24].view(1, 4, 6), f32, 4, 6, here) == 24
+    cut = torch.zeros(5, 4, 10)[:, :, :6]
+    for pool, dtype, word in ((cut, f32, "slot of p"), (torch.zeros(5, 4, 7), f32, "shape"), (torch.zeros(5, 24), f32, "shape"),
+                              (torch.zeros(5, 4, 6), torch.bfloat16, "bfloat16")):
+        with pytest.raises(ValueError, match=word):
+            pool_stride("p", pool, dtype, 4, 6, here)
+    assert inner_contiguous(torch.zeros(3, 5, 4).transpose(0, 1), 2) and not inner_contiguous(cut, 1)
 
 
 # ------------------------------------------------- the fp64 forms against the oracle
