@@ -54,6 +54,7 @@ struct PackedParams {
     int64_t n_chunks;        // chunks the workspace has room for
     unsigned tiles_per_group, n_tiles;
     int softplus, phase, state_vec;
+    int grid16;              // every row starts on the 16-byte grid
 };
 
 template <typename T, int N, bool HEAD, bool ALIGNED>
@@ -185,13 +186,13 @@ __device__ __forceinline__ void write_row(unsigned char* stage, int row, int e, 
 
 // What a CTA works on: one channel tile of one chunk of one sequence.
 struct Task {
-    int64_t g, ci0, d0;      // group, first channel within it, first channel
+    int g, ci0, d0;          // group, first channel within it, first channel
     int nch;                 // channels of the tile
-    int64_t t0, t1;          // tokens
-    int64_t chunk_id;        // of the workspace
-    int64_t k;               // chunk of its sequence
+    int t0, t1;              // tokens
+    int chunk_id;            // of the workspace
+    int k;                   // chunk of its sequence
+    int slot;
     bool last;
-    int64_t slot;
     bool has;                // starts from the slot's state
 };
 
@@ -204,8 +205,9 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int lg = lane / TPC, j = lane % TPC;
     const int64_t L = p.total;
-    const int64_t h_lo = HEAD ? tk.d0 / p.head_dim : tk.d0;           // first delta row of the tile
-    const int n_dt = HEAD ? (int)((tk.d0 + tk.nch - 1) / p.head_dim - h_lo + 1) : tk.nch;
+    const int head_dim = (int)p.head_dim;
+    const int h_lo = HEAD ? tk.d0 / head_dim : tk.d0;                 // first delta row of the tile
+    const int n_dt = HEAD ? (tk.d0 + tk.nch - 1) / head_dim - h_lo + 1 : tk.nch;
     float* bc = reinterpret_cast<float*>(smem + Cf::OFF_BC);
     float2* q = reinterpret_cast<float2*>(smem + Cf::OFF_Q + warp * Cf::Q_WARP);
     float* s_bias = reinterpret_cast<float*>(smem + Cf::OFF_PAR);
@@ -213,30 +215,30 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
     float* s_a = s_D + CT;
 
     // the first step of block 0 sits on the 16-byte grid of an aligned row
-    const int64_t tb0 = tk.t0 & ~(int64_t)(V - 1);
-    const int nblk = (int)((tk.t1 - tb0 + TB - 1) / TB);
+    const int tb0 = tk.t0 & ~(V - 1);
+    const int nblk = (tk.t1 - tb0 + TB - 1) / TB;
 
-    const unsigned char* ub = static_cast<const unsigned char*>(p.u) + tk.d0 * L * ESZ;
-    const unsigned char* zb = p.z ? static_cast<const unsigned char*>(p.z) + tk.d0 * L * ESZ : nullptr;
-    const unsigned char* db = static_cast<const unsigned char*>(p.delta) + h_lo * L * ESZ;
-    const unsigned char* Bb = static_cast<const unsigned char*>(p.B) + tk.g * N * L * ESZ;
-    const unsigned char* Cb = static_cast<const unsigned char*>(p.C) + tk.g * N * L * ESZ;
-    unsigned char* ob = static_cast<unsigned char*>(p.out) + tk.d0 * L * ESZ;
+    const unsigned char* ub = static_cast<const unsigned char*>(p.u) + (int64_t)tk.d0 * L * ESZ;
+    const unsigned char* zb = p.z ? static_cast<const unsigned char*>(p.z) + (int64_t)tk.d0 * L * ESZ : nullptr;
+    const unsigned char* db = static_cast<const unsigned char*>(p.delta) + (int64_t)h_lo * L * ESZ;
+    const unsigned char* Bb = static_cast<const unsigned char*>(p.B) + (int64_t)tk.g * N * L * ESZ;
+    const unsigned char* Cb = static_cast<const unsigned char*>(p.C) + (int64_t)tk.g * N * L * ESZ;
+    unsigned char* ob = static_cast<unsigned char*>(p.out) + (int64_t)tk.d0 * L * ESZ;
 
     // Copies of `rows` rows of a tensor (first row at `base`) into staged rows r0 .. of a stage.
     // A piece is copied if it holds a token of the chunk; others keep what the stage held, and
     // nothing computed from them is used.  `lo`, `hi`: the tensor's bytes; a piece that starts
     // before them (a base off the 16-byte grid) is copied by elements, one that ends behind them
     // is cut.
-    auto stage_rows = [&](int stage, int r0, const unsigned char* base, int rows, int64_t tb, const unsigned char* lo,
+    auto stage_rows = [&](int stage, int r0, const unsigned char* base, int rows, int tb, const unsigned char* lo,
                           const unsigned char* hi) {
         unsigned char* sb = smem + stage * Cf::STAGE;
         if constexpr (ALIGNED) {
             const int g = tid % Cf::PA;
-            const int64_t ts = tb + g * V;
+            const int ts = tb + g * V;
             if (ts < tk.t1 && ts + V > tk.t0) {
                 const unsigned dst = ssm::smem_u32(sb);
-                const unsigned char* src = base + ts * ESZ;
+                const unsigned char* src = base + (int64_t)ts * ESZ;
                 for (int r = tid / Cf::PA; r < rows; r += NT / Cf::PA)
                     cp16(dst + Cf::piece_off(r0 + r, g), src + (int64_t)r * L * ESZ, 16);
             }
@@ -245,9 +247,9 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
                 const int r = i / Cf::PIECES, g = i % Cf::PIECES;
                 const unsigned char* row = base + (int64_t)r * L * ESZ;
                 const int m = skew<T>(row);
-                const int64_t ts = tb + g * V - m;
+                const int ts = tb + g * V - m;
                 if (ts < tk.t1 && ts + V > tk.t0) {
-                    const unsigned char* src = row + ts * ESZ;
+                    const unsigned char* src = row + (int64_t)ts * ESZ;
                     unsigned char* dst = sb + Cf::piece_off(r0 + r, g);
                     if (src >= lo) {
                         const int64_t left = hi - src;
@@ -263,7 +265,7 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
     };
     auto bytes_of = [&](int64_t rows) { return rows * L * ESZ; };
     auto issue = [&](int kb) {
-        const int64_t tb = tb0 + (int64_t)kb * TB;
+        const int tb = tb0 + kb * TB;
         const int st = kb & 1;
         auto put = [&](int r0, const unsigned char* base, int rows, const void* t, int64_t t_rows) {
             const unsigned char* lo = static_cast<const unsigned char*>(t);
@@ -280,8 +282,8 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
     __syncthreads();
     if (nblk > 0) issue(0);
     for (int c = tid; c < CT; c += NT) {
-        const int64_t d = tk.d0 + (c < tk.nch ? c : 0);
-        const int64_t hd = HEAD ? d / p.head_dim : d;
+        const int d = tk.d0 + (c < tk.nch ? c : 0);
+        const int hd = HEAD ? d / head_dim : d;
         s_bias[c] = p.bias ? __ldg(p.bias + hd) : 0.f;
         s_D[c] = p.D ? __ldg(p.D + d) : 0.f;
         if constexpr (HEAD) s_a[c] = __ldg(p.A + hd) * kLog2e;
@@ -309,7 +311,7 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
             const float* hr = p.ws_h + (c0 * p.dim + d) * N + j * S;
 #pragma unroll
             for (int s = 0; s < S / 2; ++s) h[c][s] = __ldcg(reinterpret_cast<const float2*>(hr) + s);
-            for (int64_t i = 1; i < tk.k; ++i) {
+            for (int i = 1; i < tk.k; ++i) {
                 const float pr = __ldcg(p.ws_p + (c0 + i) * p.dim + d);
                 const float* hi = p.ws_h + ((c0 + i) * p.dim + d) * N + j * S;
 #pragma unroll
@@ -326,7 +328,7 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
                 }
             }
         } else if (!LOCAL && tk.has) {
-            const float* hr = p.states + tk.slot * p.slot_stride + d * N + j * S;
+            const float* hr = p.states + (int64_t)tk.slot * p.slot_stride + d * N + j * S;
             if (p.state_vec) {
 #pragma unroll
                 for (int s = 0; s < S / 2; s += 2) {
@@ -345,10 +347,10 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
     }
 
     for (int kb = 0; kb < nblk; ++kb) {
-        const int64_t tb = tb0 + (int64_t)kb * TB;
+        const int tb = tb0 + kb * TB;
         // the chunk's steps of the block: [lo, hi)
-        const int lo = tk.t0 > tb ? (int)(tk.t0 - tb) : 0;
-        const int hi = tk.t1 - tb < TB ? (int)(tk.t1 - tb) : TB;
+        const int lo = tk.t0 > tb ? tk.t0 - tb : 0;
+        const int hi = tk.t1 - tb < TB ? tk.t1 - tb : TB;
         const bool whole = lo == 0 && hi == TB;
         unsigned char* sb = smem + (kb & 1) * Cf::STAGE;
         cp_wait_all();
@@ -373,7 +375,7 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
             const int idx = lane + 32 * it, c = idx % CW, e0 = idx / CW * PS;
             const int lc = warp * CW + c;
             const int cl = lc < tk.nch ? lc : 0;
-            const int dr = HEAD ? (int)((tk.d0 + cl) / p.head_dim - h_lo) : lc;
+            const int dr = HEAD ? (tk.d0 + cl) / head_dim - h_lo : lc;
             float x[PS], uv[PS];
             const int mu = ALIGNED ? 0 : skew<T>(ub + (int64_t)lc * L * ESZ);
             const int md = ALIGNED ? 0 : skew<T>(db + (int64_t)dr * L * ESZ);
@@ -494,7 +496,7 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
                 unsigned char* row = ob + (int64_t)lc * L * ESZ;
                 const int e0 = g * V - (ALIGNED ? 0 : skew<T>(row));     // first step of the piece
                 const unsigned char* src = sb + Cf::piece_off(Cf::R_DT + lc, g);
-                unsigned char* dst = row + (tb + e0) * ESZ;
+                unsigned char* dst = row + (int64_t)(tb + e0) * ESZ;
                 if (e0 >= lo && e0 + V <= hi) {
                     *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
                 } else {
@@ -512,7 +514,7 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
         if (!ok[c]) continue;
         const int64_t d = tk.d0 + warp * CW + lg * CPL + c;
         if (!LOCAL && tk.last) {
-            float* hr = p.states + tk.slot * p.slot_stride + d * N + j * S;
+            float* hr = p.states + (int64_t)tk.slot * p.slot_stride + d * N + j * S;
             if (p.state_vec) {
 #pragma unroll
                 for (int s = 0; s < S / 2; s += 2)
@@ -522,10 +524,10 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
                 for (int s = 0; s < S / 2; ++s) { hr[2 * s] = h[c][s].x; hr[2 * s + 1] = h[c][s].y; }
             }
         } else if (LOCAL || tk.k == 0) {
-            float* hr = p.ws_h + (tk.chunk_id * p.dim + d) * N + j * S;
+            float* hr = p.ws_h + ((int64_t)tk.chunk_id * p.dim + d) * N + j * S;
 #pragma unroll
             for (int s = 0; s < S / 2; ++s) __stcg(reinterpret_cast<float2*>(hr) + s, h[c][s]);
-            if (LOCAL && j == 0) __stcg(p.ws_p + tk.chunk_id * p.dim + d, acc[c]);
+            if (LOCAL && j == 0) __stcg(p.ws_p + (int64_t)tk.chunk_id * p.dim + d, acc[c]);
         }
     }
 }
@@ -540,6 +542,38 @@ __device__ __forceinline__ bool find_item(const PackedParams& p, int64_t x, int6
     constexpr int kBuckets = 64;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt / 32;
     const bool cut = p.chunk > 0;
+    if (p.n_seq <= 32) {
+        // few sequences, one per lane: every warp finds the item by itself, by exact length
+        int64_t len = -1;
+        if (lane < p.n_seq) {
+            const TokenRange r = token_range(p.cu, lane, p.total);
+            len = r.hi - r.lo;
+        }
+        int first, n;                                   // the lane's sequence has items [first, first + n)
+        if (cut) {
+            n = len > 0 ? (int)((len + p.chunk - 1) / p.chunk) : len == 0;
+            int inc = n;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, inc, m);
+                if (lane >= m) inc += v;
+            }
+            first = inc - n;
+        } else {
+            n = len >= 0;
+            first = 0;
+            const int l = (int)len;
+            for (int i = 0; i < (int)p.n_seq; ++i) {
+                const int v = __shfl_sync(0xffffffffu, l, i);
+                first += v > l || (v == l && i < lane);
+            }
+        }
+        const unsigned mine = __ballot_sync(0xffffffffu, n > 0 && x >= first && x < (int64_t)first + n);
+        if (mine == 0u) return false;
+        seq = __ffs(mine) - 1;
+        k = x - __shfl_sync(0xffffffffu, first, (int)seq);
+        return true;
+    }
     unsigned* count = reinterpret_cast<unsigned*>(sh + 2 + 32);
     auto bucket = [&](int64_t len) {
         if (len <= 0) return kBuckets - 1;
@@ -595,44 +629,52 @@ __device__ __forceinline__ bool find_item(const PackedParams& p, int64_t x, int6
     return seq >= 0;
 }
 
+// What this launch does with the x-th item: fills in the task's tokens, slot and chunk (its channels
+// are set), or, for a bad slot, writes the outputs' NaN.  All threads of the CTA call it.
+enum Run { kRunNone, kRunFull, kRunLocal };
+template <typename T>
+__device__ __forceinline__ Run find_run(const PackedParams& p, int64_t x, int64_t* sh, int nt, Task& tk) {
+    int64_t seq, k;
+    tk.chunk_id = (int)x;
+    if (!find_item(p, x, sh, nt, seq, k)) return kRunNone;
+    const TokenRange r = token_range(p.cu, seq, p.total);
+    const int64_t t0 = r.lo + k * p.chunk;
+    tk.k = (int)k;
+    tk.t0 = (int)t0;
+    tk.t1 = (int)(p.chunk > 0 && r.hi - t0 > p.chunk ? t0 + p.chunk : r.hi);
+    tk.last = tk.t1 == r.hi;
+    tk.slot = p.slots ? __ldg(p.slots + seq) : (int)seq;
+    tk.has = p.has_state && __ldg(p.has_state + seq) != 0;
+    const SlotKind kind = slot_kind(tk.slot, p.n_slots);
+    if (kind == kSlotPad) return kRunNone;
+    if (kind == kSlotBad) {
+        if (p.phase == (tk.k > 0 ? 2 : 1)) {
+            const int64_t n = tk.t1 - tk.t0;
+            for (int64_t i = threadIdx.x; i < n * tk.nch; i += nt)
+                static_cast<T*>(p.out)[(tk.d0 + i / n) * p.total + tk.t0 + i % n] = T(__int_as_float(0x7FC00000));
+        }
+        return kRunNone;
+    }
+    // launch 1: first chunks in full, middle ones for their end state; launch 2: the later ones in full
+    if (p.phase == 1) return tk.k == 0 ? kRunFull : tk.last ? kRunNone : kRunLocal;
+    return tk.k > 0 ? kRunFull : kRunNone;
+}
+
 template <typename T, int N, bool HEAD, bool ALIGNED>
 __global__ void __launch_bounds__(PackedCfg<T, N, HEAD, ALIGNED>::NT, PackedCfg<T, N, HEAD, ALIGNED>::CTAS)
 scan_packed_kernel(const PackedParams p) {
     using Cf = PackedCfg<T, N, HEAD, ALIGNED>;
     extern __shared__ __align__(16) unsigned char packed_smem[];
     unsigned char* smem = packed_smem;
-    Task tk;
-    const int64_t x = blockIdx.x / p.n_tiles;
     const unsigned tile = blockIdx.x % p.n_tiles;
-    tk.g = tile / p.tiles_per_group;
-    tk.ci0 = (int64_t)(tile % p.tiles_per_group) * Cf::CT;
-    tk.d0 = tk.g * p.group_dim + tk.ci0;
-    tk.nch = (int)(p.group_dim - tk.ci0 < Cf::CT ? p.group_dim - tk.ci0 : Cf::CT);
-    int64_t seq;
-    tk.chunk_id = x;
-    if (!find_item(p, x, reinterpret_cast<int64_t*>(smem), Cf::NT, seq, tk.k)) return;
-    const TokenRange r = token_range(p.cu, seq, p.total);
-    tk.t0 = r.lo + tk.k * p.chunk;
-    tk.t1 = p.chunk > 0 && r.hi - tk.t0 > p.chunk ? tk.t0 + p.chunk : r.hi;
-    tk.last = tk.t1 == r.hi;
-    tk.slot = p.slots ? __ldg(p.slots + seq) : (int)seq;
-    tk.has = p.has_state && __ldg(p.has_state + seq) != 0;
-    const ssm::SlotKind kind = ssm::slot_kind((int)tk.slot, p.n_slots);
-    if (kind == ssm::kSlotPad) return;
-    if (kind == ssm::kSlotBad) {
-        if (p.phase == (tk.k > 0 ? 2 : 1)) {
-            const int64_t n = tk.t1 - tk.t0;
-            for (int64_t i = threadIdx.x; i < n * tk.nch; i += Cf::NT)
-                static_cast<T*>(p.out)[(tk.d0 + i / n) * p.total + tk.t0 + i % n] = T(__int_as_float(0x7FC00000));
-        }
-        return;
-    }
-    if (p.phase == 1) {
-        if (tk.k == 0) run_chunk<T, N, HEAD, ALIGNED, false>(p, tk, smem);
-        else if (!tk.last) run_chunk<T, N, HEAD, ALIGNED, true>(p, tk, smem);
-    } else if (tk.k > 0) {
-        run_chunk<T, N, HEAD, ALIGNED, false>(p, tk, smem);
-    }
+    Task tk;
+    tk.g = (int)(tile / p.tiles_per_group);
+    tk.ci0 = (int)(tile % p.tiles_per_group) * Cf::CT;
+    tk.d0 = tk.g * (int)p.group_dim + tk.ci0;
+    tk.nch = (int)p.group_dim - tk.ci0 < Cf::CT ? (int)p.group_dim - tk.ci0 : Cf::CT;
+    const Run run = find_run<T>(p, blockIdx.x / p.n_tiles, reinterpret_cast<int64_t*>(smem), Cf::NT, tk);
+    if (run == kRunFull) run_chunk<T, N, HEAD, ALIGNED, false>(p, tk, smem);
+    else if (run == kRunLocal) run_chunk<T, N, HEAD, ALIGNED, true>(p, tk, smem);
 }
 
 template <typename T, int N, bool HEAD, bool ALIGNED>

@@ -1,0 +1,573 @@
+// The scan over packed prompts on the tensor cores, for the per-head layout with head dim 64,
+// dstate 128 and bf16 I/O: the chunked form ("Agent 229: SSM optimization patterns" page, section 2
+// "Mamba-2 SSD" and section 9 "Chunked Computation") over sequences that start and end anywhere.
+//
+// One CTA runs one head through its tokens, Q = 128 at a time (a block).  With a_t = dt_t A log2 e,
+// X, B, C the block's u, B, C rows, H (N x P) the state at its start, and s(i, j) the sum of a over
+// the steps after j up to i:
+//
+//   S  = B^T X',  X'_j = 2^s(end, j) dt_j x_j       (N x P)     H <- 2^s(end, start) H + S
+//   G  = C B^T,   M = G o [2^s(i, j) dt_j]_{j <= i}   (Q x Q)
+//   Y  = M X + diag(2^s(i, start)) (C H)             (Q x P)     out = (Y + D x) silu(z)
+//
+// Steps outside the sequence have dt = 0 and their rows of B, C and X are zeroed in shared memory,
+// so that no value there, NaN included, reaches a product.
+//
+// Precision.  B, C and X are bf16 and enter exactly.  X' is split into three bf16 terms (24 bits),
+// so the state is summed as exactly as in fp32; M and H into two (16 bits, 2^-17 of each product),
+// far inside the rounding of the bf16 outputs.  Sums of a that are subtracted from one another
+// lose their small differences, so every s(i, j) is added up from terms of its own: the steps left
+// in j's 32-step stretch, whole stretches between, and the steps of i's stretch; within one
+// stretch it is a difference of two sums of at most 32 terms.
+//
+// Bound: the phases between the products, which threads compute (M, X', the outputs), one CTA of
+// 16 warps per SM; the products of a block take about 1.2 of its microseconds.  Tiles arrive by
+// 16-byte asynchronous copies into the 128-byte swizzle that the tensor cores read, each as soon as
+// its place is free: X a block ahead in a second buffer, B once G and S are done, C once C H is.
+// Rows off the 16-byte grid are shifted into place through registers.
+//
+// Every wait for the tensor cores is bounded; one that ran out ends the CTA's work with NaN in the
+// rest of its outputs.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "pair.cuh"
+#include "scan_packed.cuh"
+#include "ssd_packed.h"
+#include "tcgen05.cuh"
+
+namespace ssm {
+namespace packed {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kQ = 128, kP = 64, kN = 128;
+constexpr int kThreads = 512;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColG = 0, kColY = 128, kColCH = 192, kColS = 256;
+constexpr uint64_t kWaitNs = 500000000ull;
+
+// shared memory (bytes from a 1024-aligned base); a tile is two 64-step halves of rows of 128 bytes
+constexpr int OFF_C = 0;                       // 128 states
+constexpr int OFF_B = 32 * 1024;
+constexpr int OFF_X = 64 * 1024;               // two buffers of 64 channels
+constexpr int OFF_M = 96 * 1024;               // X' (three terms), then M (two terms of 32 KB)
+constexpr int OFF_H = 160 * 1024;              // two terms of 128 x 64
+constexpr int OFF_Z = 192 * 1024;              // z, then the outputs
+constexpr int OFF_DEC = 208 * 1024;            // two blocks' Decay
+constexpr int OFF_BAR = OFF_DEC + 2 * 4096;
+constexpr int kSmem = OFF_BAR + 256 + 1024;    // and room to align the base
+
+// A block's decay, in log2 units: over the 32-step stretches of its 128 steps
+struct Decay {
+    float head[kQ];       // from the stretch's start through the step
+    float near[kQ];       // log2 dt_j less that: with head_i, the weight of j for i of the same stretch
+    float far[kQ];        // log2 dt_j and the steps from behind j to the stretch's end: for later stretches
+    float w[kQ];          // 2^s(end, j) dt_j
+    float stretch[4];     // whole stretches
+};
+static_assert(sizeof(Decay) <= 4096, "fits its place");
+
+// Four pairs of values (columns c0 .. c0 + 7 of row r) as sums of K bf16 terms, into K tiles `step`
+// bytes apart.
+template <int K>
+__device__ __forceinline__ void store_split8(unsigned char* tile, int step, uint32_t r, uint32_t c0, pair_t (&v)[4]) {
+    const uint32_t off = tc::sw128_off(r, c0);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float2 f = halves(v[q]);
+            const __nv_bfloat162 t = __floats2bfloat162_rn(f.x, f.y);
+            w[q] = *reinterpret_cast<const uint32_t*>(&t);
+            if (k + 1 < K) v[q] = pfma(pk(__uint_as_float(w[q] << 16), __uint_as_float(w[q] & 0xFFFF0000u)), pk(-1.f), v[q]);
+        }
+        *reinterpret_cast<uint4*>(tile + k * step + off) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+struct Block {
+    int64_t tb;             // token of step 0
+    int64_t t0, t1;         // the task's tokens
+};
+
+// Stages ROWS rows (the first at `base`) of a block into a tile; steps outside the task are zero.
+// [lo, hi): the tensor.  `grid`: every row starts on the 16-byte grid, and so does step 0.
+template <int ROWS>
+__device__ __forceinline__ void stage_tile(unsigned char* tile, const unsigned short* base, int64_t L, const Block& k,
+                                           const unsigned short* lo, const unsigned short* hi, bool grid) {
+    // a thread's pieces: the same eight steps of every 32nd row, which the swizzle treats alike
+    const int r0 = threadIdx.x >> 4, q = threadIdx.x & 15;
+    unsigned char* dst = tile + (q >> 3) * (ROWS * 128) + tc::sw128_off(r0, (q & 7) * 8);
+    const int64_t t = k.tb + 8 * q, step = 32 * L;
+    const unsigned short* src = base + (int64_t)r0 * L + t;
+    if (t >= k.t0 && t + 8 <= k.t1 && grid) {
+#pragma unroll
+        for (int i = 0; i < ROWS / 32; ++i, src += step) cp16(smem_u32(dst + i * 4096), src, 16);
+    } else if (t >= k.t1 || t + 8 <= k.t0) {
+#pragma unroll
+        for (int i = 0; i < ROWS / 32; ++i) *reinterpret_cast<uint4*>(dst + i * 4096) = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+        const bool whole = t >= k.t0 && t + 8 <= k.t1;
+#pragma unroll
+        for (int i = 0; i < ROWS / 32; ++i, src += step) {
+            const uintptr_t m = reinterpret_cast<uintptr_t>(src) & 15u;
+            const unsigned short* a = src - m / 2;
+            uint32_t o[4] = {0u, 0u, 0u, 0u};
+            if (whole && a >= lo && a + 16 <= hi) {
+                const uint4 x = __ldg(reinterpret_cast<const uint4*>(a)), y = __ldg(reinterpret_cast<const uint4*>(a) + 1);
+                const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                // by whole words, then by half of one
+                uint32_t s[6];
+#pragma unroll
+                for (int e = 0; e < 6; ++e) s[e] = (m & 8) ? w[e + 2] : w[e];
+#pragma unroll
+                for (int e = 0; e < 5; ++e) s[e] = (m & 4) ? s[e + 1] : s[e];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = __funnelshift_r(s[e], s[e + 1], (unsigned)(m & 2) * 8);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (t + e >= k.t0 && t + e < k.t1) o[e / 2] |= (uint32_t)src[e] << (16 * (e & 1));
+            }
+            *reinterpret_cast<uint4*>(dst + i * 4096) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
+// The outputs, staged in the z tile, to global memory: each thread the pieces that it staged.
+__device__ __forceinline__ void store_out(const unsigned char* tile, unsigned short* base, int64_t L, const Block& k, bool grid) {
+    if (grid) {
+#pragma unroll
+        for (int i0 = 0; i0 < kP * 16; i0 += kThreads) {
+            const int i = i0 + threadIdx.x, r = i >> 4, q = i & 15;
+            const uint4 v = *reinterpret_cast<const uint4*>(tile + (q >> 3) * (kP * 128) + tc::sw128_off(r, (q & 7) * 8));
+            const int64_t t = k.tb + 8 * q;
+            unsigned short* dst = base + (int64_t)r * L + t;
+            if (t >= k.t0 && t + 8 <= k.t1) {
+                *reinterpret_cast<uint4*>(dst) = v;
+            } else {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (t + e >= k.t0 && t + e < k.t1) dst[e] = (unsigned short)(w[e / 2] >> (16 * (e & 1)));
+            }
+        }
+    } else {
+        // off the grid: by elements, neighbouring steps on neighbouring lanes
+        for (int i = threadIdx.x; i < kP * kQ; i += kThreads) {
+            const int r = i >> 7, c = i & 127;
+            const int64_t t = k.tb + c;
+            if (t >= k.t0 && t < k.t1)
+                base[(int64_t)r * L + t] =
+                    *reinterpret_cast<const unsigned short*>(tile + (c >> 6) * (kP * 128) + tc::sw128_off(r, c & 63));
+        }
+    }
+}
+
+// A block's decay, by one warp: four steps per lane, so eight lanes hold a stretch.
+__device__ __forceinline__ void block_decay(const PackedParams& p, const unsigned short* delta, const Block& k, float Ah,
+                                            float bias, int lane, Decay& o) {
+    float dt[4], pre[4], run = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int64_t t = k.tb + 4 * lane + e;
+        dt[e] = 0.f;
+        if (t >= k.t0 && t < k.t1) {
+            const float x = __uint_as_float((uint32_t)__ldg(delta + t) << 16) + bias;
+            dt[e] = p.softplus ? softplus1(x) : x;
+        }
+        run += dt[e] * Ah;
+        pre[e] = run;
+    }
+    // sums of the lanes before and behind within the stretch
+    float before = run, behind = run;
+#pragma unroll
+    for (int s = 1; s < 8; s <<= 1) {
+        const float u = __shfl_up_sync(0xffffffffu, before, s, 8), d = __shfl_down_sync(0xffffffffu, behind, s, 8);
+        if ((lane & 7) >= s) before += u;
+        if ((lane & 7) + s < 8) behind += d;
+    }
+    const float whole = __shfl_sync(0xffffffffu, before, 7, 8);
+    float up = __shfl_up_sync(0xffffffffu, before, 1, 8), down = __shfl_down_sync(0xffffffffu, behind, 1, 8);
+    if ((lane & 7) == 0) up = 0.f;
+    if ((lane & 7) == 7) down = 0.f;
+    float later = 0.f;                                   // the whole stretches behind this one
+#pragma unroll
+    for (int s = 3; s >= 1; --s) {
+        const float v = __shfl_sync(0xffffffffu, whole, 8 * s);
+        if (s > (lane >> 3)) later += v;
+    }
+    float suf = 0.f;
+#pragma unroll
+    for (int e = 3; e >= 0; --e) {
+        const int j = 4 * lane + e;
+        const float l = __log2f(dt[e]);                  // -inf where dt = 0: a weight of zero
+        o.head[j] = up + pre[e];
+        o.near[j] = l - (up + pre[e]);
+        o.far[j] = l + (suf + down);
+        o.w[j] = ex2_approx((suf + down) + later) * dt[e];
+        suf += dt[e] * Ah;
+    }
+    if ((lane & 7) == 0) o.stretch[lane >> 3] = whole;
+}
+
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Thread: TMEM lane and tile row `row`, and a quarter of that row's columns (32 of the 128 steps,
+// 16 of the 64 channels).  LOCAL: only the end state from zero and the product of the decays.
+template <bool LOCAL>
+__device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, unsigned char* smem) {
+    uint64_t* mb_s = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+    uint64_t* mb_y = mb_s + 1;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(mb_s + 2);
+    int* status = reinterpret_cast<int*>(mb_s + 3);
+    Decay* dec = reinterpret_cast<Decay*>(smem + OFF_DEC);
+    static_assert(OFF_DEC % 16 == 0, "vector reads of the decay");
+    unsigned char *sC = smem + OFF_C, *sB = smem + OFF_B, *sM = smem + OFF_M, *sH = smem + OFF_H, *sZ = smem + OFF_Z;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int quarter = warp & 3, part = warp >> 2;
+    const uint32_t row = (uint32_t)(32 * quarter + lane), j0 = (uint32_t)(32 * part), p0 = (uint32_t)(16 * part);
+    const int64_t L = p.total, h = tk.d0 / kP, d_first = tk.d0, g_first = tk.g;
+    const float Ah = __ldg(p.A + h) * kLog2e, bias = p.bias ? __ldg(p.bias + h) : 0.f;
+    const unsigned short *u = static_cast<const unsigned short*>(p.u), *z = static_cast<const unsigned short*>(p.z),
+                         *Bt = static_cast<const unsigned short*>(p.B), *Ct = static_cast<const unsigned short*>(p.C);
+    unsigned short* out = static_cast<unsigned short*>(p.out) + (int64_t)tk.d0 * L;
+    const unsigned short* delta = static_cast<const unsigned short*>(p.delta) + h * L;
+    const bool gate = !LOCAL && z != nullptr, grid = p.grid16 != 0;
+    const int64_t tb0 = grid ? tk.t0 & ~7 : tk.t0;
+    const int nblk = (int)((tk.t1 - tb0 + kQ - 1) / kQ);
+    auto block = [&](int c) { return Block{tb0 + (int64_t)c * kQ, tk.t0, tk.t1}; };
+    auto stage_x = [&](int c) {
+        if (c < nblk) stage_tile<kP>(smem + OFF_X + (c & 1) * 16384, u + d_first * L, L, block(c), u, u + p.dim * L, grid);
+        cp_commit();
+    };
+    auto stage_b = [&](int c) {
+        if (c < nblk) stage_tile<kN>(sB, Bt + g_first * kN * L, L, block(c), Bt, Bt + p.ngroups * kN * L, grid);
+        cp_commit();
+    };
+    auto stage_c = [&](int c) {
+        if (!LOCAL && c < nblk) stage_tile<kN>(sC, Ct + g_first * kN * L, L, block(c), Ct, Ct + p.ngroups * kN * L, grid);
+        cp_commit();
+    };
+    auto stage_z = [&](int c) {
+        if (gate && c < nblk) stage_tile<kP>(sZ, z + d_first * L, L, block(c), z, z + p.dim * L, grid);
+        cp_commit();
+    };
+
+    __syncthreads();
+    if (tid == 0) {
+        mbar_init(mb_s, 1);
+        mbar_init(mb_y, 1);
+        *status = SSM_OK;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) tc::alloc(tslot, kTmemCols);
+    // the order of these groups is the order of the waits below
+    stage_x(0);
+    stage_b(0);
+    stage_c(0);
+    stage_z(0);
+    if (warp == 1 && nblk > 0) block_decay(p, delta, block(0), Ah, bias, lane, dec[0]);
+
+    // the state: n = row, channels p0 .. p0 + 15
+    float H[16], Dv[LOCAL ? 1 : 8];                     // the skip weights of the channels it writes
+    const bool from_before = !LOCAL && tk.k > 0, from_slot = !LOCAL && tk.k == 0 && tk.has;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const int64_t d = d_first + p0 + k;
+        H[k] = 0.f;
+        if (from_slot) H[k] = p.states[(int64_t)tk.slot * p.slot_stride + d * kN + row];
+        if (from_before) H[k] = __ldcg(p.ws_h + ((int64_t)(tk.chunk_id - tk.k) * p.dim + d) * kN + row);
+        if constexpr (!LOCAL)
+            if ((k & 1) == 0) Dv[k / 2] = p.D ? __ldg(p.D + d + (lane & 1)) : 0.f;
+    }
+    if (from_before) {
+        // join the chunks before: the first holds a state, the later ones (decay, state from zero)
+        for (int i = 1; i < tk.k; ++i) {
+            const int64_t c = tk.chunk_id - tk.k + i;
+            const float pr = __ldcg(p.ws_p + c * p.dim + d_first);
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                H[k] = fmaf(pr, H[k], __ldcg(p.ws_h + (c * p.dim + d_first + p0 + k) * kN + row));
+        }
+    }
+    const bool start_state = from_slot || from_before;
+    auto store_state = [&]() {
+#pragma unroll
+        for (int k = 0; k < 16; k += 8) {
+            pair_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = pk(H[k + 2 * e], H[k + 2 * e + 1]);
+            store_split8<2>(sH, 16384, row, p0 + k, v);
+        }
+    };
+    if (start_state) store_state();
+    tc::fence_async_smem();
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tbase = *tslot, trow = tbase + ((uint32_t)(32 * quarter) << 16);
+
+    float total = 0.f;                                  // LOCAL: the sum of a over the task
+    int done = 0;                                       // blocks whose outputs are written
+    uint64_t* last_bar = nullptr;                       // thread 0: its latest commit
+    unsigned last_ph = 0;
+    for (int c = 0; c < nblk; ++c) {
+        const unsigned ph = (unsigned)c & 1u;
+        const Decay& dc = dec[c & 1];
+        const unsigned char* sX = smem + OFF_X + (c & 1) * 16384;
+        const bool with_state = c > 0 || start_state;
+        // copies in flight, the oldest first: X, B, C, z of this block, X of the next
+        stage_x(c + 1);
+        cp_wait<4>();
+        __syncthreads();                                // X is staged, and this block's decay
+        // ---- X', in three terms: two 8-step pieces of a channel per thread
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const uint32_t e = (uint32_t)tid + (uint32_t)r * kThreads, pp = e >> 4, s8 = (e & 15u) * 8u;
+            const uint32_t half = (s8 >> 6) * 8192;
+            const uint4 raw = *reinterpret_cast<const uint4*>(sX + half + tc::sw128_off(pp, s8 & 63u));
+            const uint32_t w4[4] = {raw.x, raw.y, raw.z, raw.w};
+            const ulonglong2* wj = reinterpret_cast<const ulonglong2*>(dc.w + s8);
+            const ulonglong2 wa = wj[0], wb = wj[1];
+            const pair_t w2[4] = {wa.x, wa.y, wb.x, wb.y};
+            pair_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[k] = pmul(pk(__uint_as_float(w4[k] << 16), __uint_as_float(w4[k] & 0xFFFF0000u)), w2[k]);
+            store_split8<3>(sM + half, 16384, pp, s8 & 63u, v);
+        }
+        cp_wait<2>();                                   // B and C
+        tc::fence_async_smem();
+        tc::fence_before();
+        __syncthreads();
+        if (tid == 0) {
+            tc::fence_after();
+            if constexpr (!LOCAL) {
+                constexpr uint32_t id = tc::idesc_bf16(128, 128, true, true);
+#pragma unroll
+                for (int kk = 0; kk < kN / 16; ++kk)
+                    tc::mma_bf16(tbase + kColG, tc::desc(sC + kk * 2048, 16384, 1024, tc::kSwizzle128),
+                                 tc::desc(sB + kk * 2048, 16384, 1024, tc::kSwizzle128), id, kk > 0 ? 1u : 0u);
+            }
+            constexpr uint32_t ids = tc::idesc_bf16(128, kP, false, false);
+#pragma unroll
+            for (int kk = 0; kk < kQ / 16; ++kk) {
+                const uint64_t ab = tc::desc(sB + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024, tc::kSwizzle128);
+#pragma unroll
+                for (int s = 0; s < 3; ++s)
+                    tc::mma_bf16(tbase + kColS, ab,
+                                 tc::desc(sM + s * 16384 + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024, tc::kSwizzle128), ids,
+                                 kk > 0 || s > 0 ? 1u : 0u);
+            }
+            tc::commit(mb_s);
+            last_bar = mb_s;
+            last_ph = ph;
+        }
+        if (warp == 1 && c + 1 < nblk) block_decay(p, delta, block(c + 1), Ah, bias, lane, dec[(c + 1) & 1]);
+        bool ok = mbar_wait(mb_s, ph, kWaitNs, status);
+        tc::fence_after();
+        // (a wait that ran out is voted on before anything overwrites what the products may still read)
+        if (__syncthreads_or(!ok)) break;
+        stage_b(c + 1);
+        if constexpr (!LOCAL) {
+            // ---- M: row i = row, steps j0 ..; a warp whose steps all come after its rows writes zeros
+            unsigned char* mt = sM + (j0 >> 6) * 16384;
+            if (part > quarter) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 8) {
+                    const uint32_t off = tc::sw128_off(row, (j0 & 63u) + k);
+                    *reinterpret_cast<uint4*>(mt + off) = make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4*>(mt + 32768 + off) = make_uint4(0u, 0u, 0u, 0u);
+                }
+            } else {
+                uint32_t gv[32];
+                tc::ld32(trow + kColG + j0, gv);
+                const bool same = part == quarter;
+                float ci = dc.head[row];
+                for (int s = part + 1; s < quarter; ++s) ci += dc.stretch[s];
+                const pair_t ci2 = pk(ci);
+                const float* cj = (same ? dc.near : dc.far) + j0;
+                tc::wait_ld();
+                tc::after_wait(gv);
+#pragma unroll
+                for (int k = 0; k < 32; k += 8) {
+                    const ulonglong2 ca = *reinterpret_cast<const ulonglong2*>(cj + k);
+                    const ulonglong2 cb = *reinterpret_cast<const ulonglong2*>(cj + k + 4);
+                    const pair_t c2[4] = {ca.x, ca.y, cb.x, cb.y};
+                    pair_t v[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        v[q] = pmul(pk(__uint_as_float(gv[k + 2 * q]), __uint_as_float(gv[k + 2 * q + 1])),
+                                    pex2(padd(ci2, c2[q])));
+                        if (same) {                     // of the stretch's own steps, those up to the row's
+                            const float2 f = halves(v[q]);
+                            const int j = k + 2 * q;
+                            v[q] = pk(j <= lane ? f.x : 0.f, j + 1 <= lane ? f.y : 0.f);
+                        }
+                    }
+                    store_split8<2>(mt, 32768, row, (j0 & 63u) + k, v);
+                }
+            }
+            cp_wait<2>();                               // z (X and B of the next block may be on their way)
+            tc::fence_async_smem();
+            tc::fence_before();
+            __syncthreads();
+            if (tid == 0) {
+                tc::fence_after();
+                constexpr uint32_t idy = tc::idesc_bf16(128, kP, false, false), idh = tc::idesc_bf16(128, kP, true, true);
+#pragma unroll
+                for (int kk = 0; kk < kQ / 16; ++kk) {
+                    const uint64_t bx = tc::desc(sX + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024, tc::kSwizzle128);
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+                        tc::mma_bf16(tbase + kColY,
+                                     tc::desc(sM + s * 32768 + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024, tc::kSwizzle128), bx,
+                                     idy, kk > 0 || s > 0 ? 1u : 0u);
+                }
+                if (with_state) {
+#pragma unroll
+                    for (int kk = 0; kk < kN / 16; ++kk) {
+                        const uint64_t a = tc::desc(sC + kk * 2048, 16384, 1024, tc::kSwizzle128);
+#pragma unroll
+                        for (int s = 0; s < 2; ++s)
+                            tc::mma_bf16(tbase + kColCH, a, tc::desc(sH + s * 16384 + kk * 2048, 16384, 1024, tc::kSwizzle128),
+                                         idh, kk > 0 || s > 0 ? 1u : 0u);
+                    }
+                }
+                tc::commit(mb_y);
+                last_bar = mb_y;
+                last_ph = ph;
+            }
+            ok = mbar_wait(mb_y, ph, kWaitNs, status);
+            tc::fence_after();
+            if (__syncthreads_or(!ok)) break;
+            stage_c(c + 1);
+            // ---- outputs of step row, channels p0 ..
+            {
+                uint32_t yv[16], cv[16];
+                tc::ld16(trow + kColY + p0, yv);
+                if (with_state) tc::ld16(trow + kColCH + p0, cv);
+                float e = dc.head[row];
+                for (int s = 0; s < quarter; ++s) e += dc.stretch[s];
+                e = ex2_approx(e);
+                tc::wait_ld();
+                tc::after_wait(yv);
+                if (with_state) tc::after_wait(cv);
+                const unsigned char* xt = sX + (row >> 6) * 8192;
+                unsigned char* zt = sZ + (row >> 6) * 8192;
+                // neighbouring lanes trade a channel, so that each has two steps of one: whole words of
+                // x, z and the outputs
+                const bool odd = lane & 1;
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                    float v0 = __uint_as_float(yv[k]), v1 = __uint_as_float(yv[k + 1]);
+                    if (with_state) {
+                        v0 = fmaf(e, __uint_as_float(cv[k]), v0);
+                        v1 = fmaf(e, __uint_as_float(cv[k + 1]), v1);
+                    }
+                    const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+                    const uint32_t at = tc::sw128_off(p0 + k + (odd ? 1u : 0u), row & 62u);
+                    const uint32_t xw = *reinterpret_cast<const uint32_t*>(xt + at);
+                    pair_t v = pfma(pk(Dv[k / 2]), pk(__uint_as_float(xw << 16), __uint_as_float(xw & 0xFFFF0000u)),
+                                    odd ? pk(got, v1) : pk(v0, got));
+                    uint32_t* zo = reinterpret_cast<uint32_t*>(zt + at);
+                    if (gate) {
+                        const uint32_t zw = *zo;
+                        v = pmul(v, psilu(pk(__uint_as_float(zw << 16), __uint_as_float(zw & 0xFFFF0000u))));
+                    }
+                    const float2 f = halves(v);
+                    const __nv_bfloat162 t = __floats2bfloat162_rn(f.x, f.y);
+                    *zo = *reinterpret_cast<const uint32_t*>(&t);
+                }
+            }
+        } else {
+            stage_c(c + 1);
+        }
+        // ---- the state
+        {
+            uint32_t sv[16];
+            tc::ld16(trow + kColS + p0, sv);
+            const float a = (dc.stretch[0] + dc.stretch[1]) + (dc.stretch[2] + dc.stretch[3]);
+            const float d = ex2_approx(a);
+            total += a;
+            tc::wait_ld();
+            tc::after_wait(sv);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) H[k] = fmaf(d, H[k], __uint_as_float(sv[k]));
+            if constexpr (!LOCAL) store_state();
+        }
+        tc::fence_async_smem();
+        tc::fence_before();
+        __syncthreads();
+        if constexpr (!LOCAL) store_out(sZ, out, L, block(c), grid);
+        if (!LOCAL && !grid) __syncthreads();           // others' outputs are still in the tile
+        stage_z(c + 1);
+        done = c + 1;
+    }
+    // a wait ran out: the products may still be under way, so wait (bounded) for the last batch
+    // before TMEM and shared memory go; the outputs that are missing become NaN
+    if (done < nblk) {
+        if (tid == 0 && last_bar) mbar_wait(last_bar, last_ph, kWaitNs, status);
+        if constexpr (!LOCAL) {
+            const int64_t a = tb0 + (int64_t)done * kQ > tk.t0 ? tb0 + (int64_t)done * kQ : tk.t0, n = tk.t1 - a;
+            for (int64_t i = tid; i < n * kP; i += kThreads) out[i / n * L + a + i % n] = 0x7FC0;
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) H[k] = __int_as_float(0x7FC00000);
+    }
+    cp_wait_all();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const int64_t d = d_first + p0 + k;
+        if (!LOCAL && tk.last) p.states[(int64_t)tk.slot * p.slot_stride + d * kN + row] = H[k];
+        else if (LOCAL || tk.k == 0) __stcg(p.ws_h + ((int64_t)tk.chunk_id * p.dim + d) * kN + row, H[k]);
+    }
+    if (LOCAL && tid < kP) __stcg(p.ws_p + (int64_t)tk.chunk_id * p.dim + d_first + tid, ex2_approx(total));
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 0) tc::dealloc(tbase, kTmemCols);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) ssd_packed_kernel(const PackedParams p) {
+    extern __shared__ __align__(1024) unsigned char ssd_smem[];
+    unsigned char* smem = ssd_smem + ((1024u - (smem_u32(ssd_smem) & 1023u)) & 1023u);
+    const unsigned h = blockIdx.x % p.n_tiles;
+    Task tk;
+    tk.d0 = (int)h * kP;
+    tk.g = tk.d0 / (int)p.group_dim;
+    tk.ci0 = tk.d0 - tk.g * (int)p.group_dim;
+    tk.nch = kP;
+    const Run run = find_run<bf16>(p, blockIdx.x / p.n_tiles, reinterpret_cast<int64_t*>(smem), kThreads, tk);
+    if (run == kRunFull) run_head<false>(p, tk, smem);
+    else if (run == kRunLocal) run_head<true>(p, tk, smem);
+}
+
+}  // namespace
+
+bool ssd_packed_covers(const ssm_dims_t& d) {
+    return d.io_dtype == SSM_BF16 && d.nheads != d.dim && d.dim / d.nheads == kP && d.dstate == kN && d.nheads % d.ngroups == 0;
+}
+
+int ssd_packed_launch(PackedParams& p, cudaStream_t s) {
+    const int64_t ctas = p.nheads * (p.chunk > 0 ? p.n_chunks : p.n_seq);
+    if (ctas > 0x7FFFFFFF) return SSM_ERR_UNSUPPORTED;
+    p.n_tiles = (unsigned)p.nheads;
+    if (cudaFuncSetAttribute(ssd_packed_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+        return SSM_ERR_CUDA;
+    for (p.phase = 1; p.phase <= (p.chunk > 0 ? 2 : 1); ++p.phase) {
+        ssd_packed_kernel<<<(unsigned)ctas, kThreads, kSmem, s>>>(p);
+        if (cudaGetLastError() != cudaSuccess) return SSM_ERR_CUDA;
+    }
+    return SSM_OK;
+}
+
+}  // namespace packed
+}  // namespace ssm

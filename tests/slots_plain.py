@@ -91,10 +91,34 @@ def spread(v, dim, axis=0):
     return np.repeat(v, dim // v.shape[axis], axis) if v.shape[axis] != dim else v
 
 
-def scan_packed(p, bounds, slots, has, pool, out, chunk=0):
+def tensor_err(p, h0, A, delta, bias, lo, hi, dim):
+    """What the tensor-core form adds to the errors of the recurrence: for every token of a sequence a bound
+    for y ahead of the gate, and one for the state behind it.  mag is the sum of the magnitudes that make up
+    the state.
+
+      * an MMA step adds 16 products and the accumulator, cut to the largest one's last bits: 2^-22 of the
+        magnitudes.  The state takes 24 steps a block, y 32, G 8.
+      * M and the state enter as two bf16 terms: 2^-18 of each product; X' as three: 2^-24 (in the steps')
+      * the decay between two steps of a stretch is 2^(difference of two sums of at most 32 terms a): off by
+        2 * 32 u max|sum|, relative
+    """
+    mag, state, y = np.abs(h0), 24 * 2.0 ** -22, []
+    a_abs = []
+    for t in range(lo, hi):
+        x = delta[:, t] + bias
+        dt = softplus(x) if p["softplus"] else x
+        a = np.abs(dt[:, None] * A) / np.log(2.0)
+        a_abs.append(a.max())
+        stretch = max(sum(a_abs[max(0, k - 31):k + 1]) for k in range(max(0, len(a_abs) - 32), len(a_abs)))
+        mag = np.exp(dt[:, None] * A) * mag + np.abs((dt * p["u"][:, t])[:, None] * spread(p["B"][:, :, t], dim))
+        y.append((2.0 ** -18 + 40 * 2.0 ** -22 + 64 * U * stretch) * (np.abs(spread(p["C"][:, :, t], dim)) * mag).sum(1))
+    return y, state * mag
+
+
+def scan_packed(p, bounds, slots, has, pool, out, chunk=0, tensor=False):
     """p: u, delta, A, B, C, D, z, delta_bias, softplus.  `chunk`: tokens of a chunk where sequences are cut;
     the join's product of decays comes from a sum of up to `chunk` dt, whose rounding (chunk u, relative)
-    moves exp(-x) by at most 0.37 chunk u, once per chunk."""
+    moves exp(-x) by at most 0.37 chunk u, once per chunk.  `tensor`: the shape runs on the tensor cores."""
     dim = p["u"].shape[0]
     out, pool, before = out.copy(), pool.copy(), pool
     err_out, err_pool = np.zeros_like(out), np.zeros_like(pool)
@@ -118,6 +142,11 @@ def scan_packed(p, bounds, slots, has, pool, out, chunk=0):
                 h, err, p["u"][:, t], delta[:, t], A, spread(p["B"][:, :, t], dim), spread(p["C"][:, :, t], dim), p["D"],
                 p["z"][:, t] if p["z"] is not None else None, bias, p["softplus"])
             top = np.maximum(top, np.abs(h)) if t > lo else np.abs(h)
+        if tensor:
+            more, state = tensor_err(p, before[slots[i]] if has[i] else np.zeros_like(h), A, delta, bias, lo, hi, dim)
+            for t, m in zip(range(lo, hi), more):
+                err_out[:, t] += m * (np.abs(silu(p["z"][:, t])) if p["z"] is not None else 1.0)
+            err = err + state
         pool[slots[i]], err_pool[slots[i]] = h, err
     return out, err_out, pool, err_pool
 

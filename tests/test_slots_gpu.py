@@ -196,6 +196,11 @@ def _chunk(ssm, p, n_seq, max_seqlen=0):
     return ssm.ssm_selective_scan_packed_workspace_size(d, max_seqlen)
 
 
+def _tensor(dim, heads, N, dtype, total, n):
+    """The calls that run on the tensor cores."""
+    return dtype == "bf16" and heads < dim and dim // heads == 64 and N == 128 and total >= 64 * n
+
+
 SCAN = [
     # lens, dim, heads, groups, N, dtype, head, tail, gap, shift, kw
     ([64, 32, 96], 64, 64, 1, 16, "bf16", 0, 0, 0, False, {}),                       # aligned rows
@@ -209,6 +214,11 @@ SCAN = [
     ([19, 40], 36, 36, 2, 128, "f32", 0, 0, 0, False, {}),
     ([40, 24, 72], 128, 2, 1, 128, "bf16", 0, 0, 0, False, {}),                      # heads
     ([13, 50], 96, 6, 2, 128, "bf16", 0, 2, 0, False, {}),                           # heads and groups, 65 tokens
+    # the tensor-core form: blocks of 128 steps
+    ([150, 1, 0, 128, 121], 128, 2, 2, 128, "bf16", 0, 0, 0, False, {}),             # groups, aligned rows
+    ([140, 260, 5], 64, 1, 1, 128, "bf16", 3, 4, 4, False, {}),                      # one head, rows off the grid
+    ([130, 129, 31], 128, 2, 1, 128, "bf16", 0, 0, 3, True, dict(z=False)),          # shifted bases
+    ([256, 40], 64, 1, 1, 128, "bf16", 8, 0, 0, False, dict(D=False, bias=False, softplus=False)),
     ([13, 50], 33, 11, 1, 64, "f32", 0, 0, 0, True, dict(z=False)),                  # heads of three channels
     ([20, 9, 3], 48, 3, 1, 16, "bf16", 0, 0, 0, False, {}),
     ([20, 9, 3], 64, 4, 1, 32, "f32", 0, 0, 0, False, dict(softplus=False)),
@@ -232,7 +242,8 @@ def test_scan_packed(ssm, case):
         out = unaligned(out)
     rng = np.random.default_rng(2)
     slots, has = rng.permutation(n + 2)[:n].tolist(), rng.integers(0, 2, n).tolist()
-    ref, err, ref_pool, pool_err = sp.scan_packed(_plain(p), bounds, slots, has, f64(states), f64(out))
+    ref, err, ref_pool, pool_err = sp.scan_packed(_plain(p), bounds, slots, has, f64(states), f64(out),
+                                                  tensor=_tensor(dim, heads, N, dtype, total, n))
     for k in ("u", "delta", "B", "C", "z"):
         if p[k] is not None:
             p[k][..., :head] = float("nan")
@@ -255,6 +266,8 @@ CUT = [
     ([700, 90], 24, 24, 1, 8, "f32", 0),
     ([40, 800], 20, 20, 1, 32, "bf16", 0),
     ([640, 333], 16, 16, 1, 64, "f32", 0),
+    ([1200, 77], 64, 1, 1, 128, "bf16", 3),                           # tensor cores, aligned rows
+    ([1111], 128, 2, 2, 128, "bf16", 0),                              # and off the grid
 ]
 
 
@@ -270,7 +283,8 @@ def test_scan_packed_cut_sequences(ssm, case):
     states, out = rnd(gen, n, dim, N), rnd(gen, dim, total, dtype=dtype)
     has = [(i + 1) % 2 for i in range(n)]
     # chunks of at most 2 * 128 tokens at these sizes; the bound takes the longest, at every 32nd token's worth
-    ref, err, ref_pool, pool_err = sp.scan_packed(_plain(p), bounds, list(range(n)), has, f64(states), f64(out), chunk=128)
+    ref, err, ref_pool, pool_err = sp.scan_packed(_plain(p), bounds, list(range(n)), has, f64(states), f64(out), chunk=128,
+                                                  tensor=_tensor(dim, heads, N, dtype, total, n))
     flags = torch.tensor(has, dtype=torch.bool).cuda()
     start = states.clone()
     got = _call(ssm, p, i32(cu), states, out, has_state=flags, max_seqlen=max(lens))
@@ -299,31 +313,34 @@ def test_scan_packed_hint_is_only_a_hint(ssm):
         sp.check(f64(s), ref_pool, pool_err, "f32", "states")
 
 
+@pytest.mark.parametrize("dim,heads,N", [(32, 32, 16), (64, 1, 128)])
 @pytest.mark.parametrize("long", [False, True])
-def test_scan_packed_padding_and_bad_slots(ssm, long):
+def test_scan_packed_padding_and_bad_slots(ssm, long, dim, heads, N):
     gen = torch.Generator().manual_seed(24)
     lens = [900, 20, 1000, 30, 7] if long else [9, 20, 4, 30, 7]
     cu, total, bounds = packing(lens, 0, 2)
-    p = _scan_inputs(gen, total, 32, 32, 1, 16, "bf16")
+    p = _scan_inputs(gen, total, dim, heads, 1, N, "bf16")
     assert (_chunk(ssm, p, 5, max(lens)) > 0) == long
-    states, out = rnd(gen, 4, 32, 16), rnd(gen, 32, total, dtype="bf16")
+    states, out = rnd(gen, 4, dim, N), rnd(gen, dim, total, dtype="bf16")
     slots, has = [4, 1, -1, 2 ** 31 - 1, 0], [1] * 5
-    ref, err, ref_pool, pool_err = sp.scan_packed(_plain(p), bounds, slots, has, f64(states), f64(out), chunk=128 if long else 0)
+    ref, err, ref_pool, pool_err = sp.scan_packed(_plain(p), bounds, slots, has, f64(states), f64(out), chunk=128 if long else 0,
+                                                  tensor=_tensor(dim, heads, N, "bf16", total, 5))
     got = _call(ssm, p, i32(cu), states, out, slots=i32(slots), has_state=torch.ones(5, dtype=torch.uint8).cuda(),
                 max_seqlen=max(lens))
     sp.check(f64(got), ref, err, "bf16", "out")
     sp.check(f64(states), ref_pool, pool_err, "f32", "states")
 
 
-def test_scan_packed_neighbours_do_not_meet(ssm):
+@pytest.mark.parametrize("dim,heads,N", [(16, 16, 16), (64, 1, 128)])
+def test_scan_packed_neighbours_do_not_meet(ssm, dim, heads, N):
     """NaN and infinities in one sequence stay there, in aligned and unaligned rows, cut or not."""
-    for lens in ([30, 34, 64], [30, 33, 20], [400, 301, 800]):
+    for lens in ([30, 34, 64], [30, 33, 20], [70, 66, 64], [70, 61, 90], [400, 301, 800]):
         gen = torch.Generator().manual_seed(25)
         cu, total, bounds = packing(lens)
-        p = _scan_inputs(gen, total, 16, 16, 1, 16, "bf16")
-        states = rnd(gen, 3, 16, 16)
-        ref, err, ref_pool, pool_err = sp.scan_packed(_plain(p), bounds, [0, 1, 2], [0] * 3, f64(states), np.zeros((16, total)),
-                                                      chunk=128)
+        p = _scan_inputs(gen, total, dim, heads, 1, N, "bf16")
+        states = rnd(gen, 3, dim, N)
+        ref, err, ref_pool, pool_err = sp.scan_packed(_plain(p), bounds, [0, 1, 2], [0] * 3, f64(states), np.zeros((dim, total)),
+                                                      chunk=128, tensor=_tensor(dim, heads, N, "bf16", total, 3))
         lo, hi = bounds[1]
         for k, bad in (("u", float("inf")), ("B", float("nan")), ("C", float("nan")), ("z", float("nan")), ("delta", 1e30)):
             p[k][..., lo:hi] = bad
