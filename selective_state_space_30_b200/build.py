@@ -3,7 +3,9 @@
     python -m selective_state_space_30_b200.build [--force] [--debug]
 
 The library is the product: kernels plus the C ABI declared in
-include/ssm_scan.h.  Each translation unit compiles in parallel.  --debug builds
+include/ssm_scan.h.  Each translation unit compiles in parallel, and beside them
+_front.so, the compiled torch front ends of the slot and convolution operators
+(csrc/front.cpp), which call the library's entry points.  --debug builds
 libssmscan_debug.so from the same sources with SSM_DEBUG defined: the scan
 kernels then check their indices against the buffers they touch and record
 SSM_ERR_BOUNDS in the device status word instead of making a bad access.
@@ -21,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libssmscan.so")
 LIB_DEBUG = os.path.join(HERE, "libssmscan_debug.so")
+FRONT = os.path.join(HERE, "_front.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 BUILD_DIR_DEBUG = os.path.join(HERE, "_build_debug")
 
@@ -45,6 +48,22 @@ def _compile(src: str, extra, build_dir=BUILD_DIR) -> str:
     return obj
 
 
+def _compile_front() -> str:
+    """The compiled front ends: host C++ against torch's headers; torch's libraries are loaded before it."""
+    import sysconfig
+    from torch.utils.cpp_extension import include_paths, library_paths
+    tmp = FRONT + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", f"-I{INCLUDE}",
+           *(f"-I{p}" for p in include_paths("cuda")), f"-I{sysconfig.get_paths()['include']}",
+           os.path.join(CSRC, "front.cpp"), "-o", tmp, *(f"-L{p}" for p in library_paths("cuda")),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on front.cpp:\n{res.stderr[-4000:]}")
+    os.replace(tmp, FRONT)
+    return FRONT
+
+
 def _stale(lib, outputs_newer_than):
     if not os.path.exists(lib):
         return True
@@ -58,12 +77,18 @@ def build(force: bool = False, extra=(), debug: bool = False) -> str:
     extra = list(extra) + (["-DSSM_DEBUG"] if debug else [])
     deps = sources() + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + \
         [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
+    front = force or _stale(FRONT, [os.path.join(CSRC, "front.cpp"), os.path.join(INCLUDE, "ssm_scan.h")])
     if not force and not _stale(lib, deps):
+        if front:
+            _compile_front()
         return lib
     os.makedirs(build_dir, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        host = ex.submit(_compile_front) if front else None
         objs = list(ex.map(lambda s: _compile(s, extra, build_dir), srcs))
+        if host:
+            host.result()
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [NVCC, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)

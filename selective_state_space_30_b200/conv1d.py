@@ -2,58 +2,24 @@
 (ssm_causal_conv1d_fwd and ssm_causal_conv1d_bwd of include/ssm_scan.h)."""
 from __future__ import annotations
 
-from . import _abi
-from ._tensors import io_code, launch, need, need_cuda, ptr
-
-
-def _checked(x, w, bias):
-    import torch
-    dev = need_cuda("x", x, 3)
-    if w.dim() != 2:
-        raise ValueError("w must have shape (dim, width)")
-    need("w", w, torch.float32, (x.shape[1], w.shape[1]), dev)
-    need("bias", bias, torch.float32, (x.shape[1],), dev)
-    return (*x.shape, w.shape[1], io_code(x))
+from ._frontend import load, on_stream
 
 
 def causal_conv1d_fwd(x, w, bias=None, silu: bool = True, out=None, stream=None):
     """out[b,d,t] = act(bias[d] + sum_k w[d,k] x[b,d,t-width+1+k]) on CUDA tensors: x (batch, dim, seqlen)
     bf16 or fp32, w (dim, width) and bias fp32."""
-    import torch
-    batch, dim, seqlen, width, io = _checked(x, w, bias)
-    need("out", out, x.dtype, x.shape, x.get_device())
-
-    def call(raw):
-        o = torch.empty_like(x) if out is None else out
-        _abi.ssm_causal_conv1d_fwd(batch, dim, seqlen, width, io, x, w, bias, silu, o, raw)
-        return o
-    return launch(call, x.get_device(), stream)
+    f = load().conv_fwd
+    return f(x, w, bias, silu, out) if stream is None else on_stream(f, stream, x, x, w, bias, silu, out)
 
 
 def causal_conv1d_bwd(x, w, dout, bias=None, silu: bool = True, workspace=None, stream=None) -> dict:
     """Gradients of causal_conv1d_fwd: {"dx": x's dtype, "dw": fp32, "dbias": fp32} (dbias is the gradient
     at zero where bias is None).  The workspace (uint8, at least ssm_causal_conv1d_bwd_workspace_size bytes)
     is allocated with torch unless given."""
-    import torch
-    batch, dim, seqlen, width, io = _checked(x, w, bias)
-    dev = x.get_device()
-    need("dout", dout, x.dtype, x.shape, dev)
-    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
-
-    def call(raw):
-        ws = workspace
-        if ws is None:
-            nbytes = _abi.ssm_causal_conv1d_bwd_workspace_size(batch, dim, seqlen, width, io)
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-        dx, dw, dbias = torch.empty_like(x), torch.empty_like(w), w.new_empty(dim)
-        lib = _abi._lib or _abi.load_library()
-        _abi._check(lib.ssm_causal_conv1d_bwd(
-            batch, dim, seqlen, width, io, x.data_ptr(), w.data_ptr(), ptr(bias), 1 if silu else 0, dout.data_ptr(),
-            dx.data_ptr(), dw.data_ptr(), dbias.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), raw),
-            "ssm_causal_conv1d_bwd")
-        return {"dx": dx, "dw": dw, "dbias": dbias}
-    return launch(call, dev, stream)
+    f = load().conv_bwd
+    args = (x, w, dout, bias, silu, workspace)
+    dx, dw, dbias = f(*args) if stream is None else on_stream(f, stream, x, *args)
+    return {"dx": dx, "dw": dw, "dbias": dbias}
 
 
 _fn_cls = None

@@ -139,52 +139,42 @@ def test_conv_bwd_refusals(ssm):
 
 
 def test_front_end_refusals(ssm):
-    """Tensors that are no CUDA tensors, of other shapes or types: refused before the library is called."""
+    """What is no tensor, no CUDA tensor or of another rank is refused before the library is called."""
     import torch
-    z = torch.zeros
+    z, i32 = torch.zeros, torch.int32
     with pytest.raises(ValueError, match="CUDA"):
-        ssm.causal_conv1d_packed(z(4, 8), z(4, 4), z(2, dtype=torch.int32), z(1, 4, 3))
+        ssm.causal_conv1d_packed(z(4, 8), z(4, 4), z(2, dtype=i32), z(1, 4, 3))
     with pytest.raises(ValueError, match="CUDA"):
         ssm.causal_conv1d_update(z(2, 4), z(4, 4), z(2, 4, 3))
-    with pytest.raises(ValueError, match="dimensions"):
+    with pytest.raises(ValueError, match="2 dimensions"):
         ssm.causal_conv1d_update(z(2, 4, 1), z(4, 4), z(2, 4, 3))
+    with pytest.raises(TypeError, match="x must be a tensor"):
+        ssm.causal_conv1d_update([1.0], z(4, 4), z(2, 4, 3))
+    with pytest.raises(ValueError, match="x must be a tensor"):
+        ssm.causal_conv1d_update(None, z(4, 4), z(2, 4, 3))
     with pytest.raises(ValueError, match="CUDA"):
-        ssm.selective_scan_packed(z(4, 8), z(4, 8), z(4, 16), z(1, 16, 8), z(1, 16, 8), z(2, dtype=torch.int32), z(1, 4, 16))
+        ssm.selective_scan_packed(z(4, 8), z(4, 8), z(4, 16), z(1, 16, 8), z(1, 16, 8), z(2, dtype=i32), z(1, 4, 16))
     with pytest.raises(ValueError, match="CUDA"):
         ssm.selective_state_update_slots(z(1, 4, 16), z(1, 4), z(1, 4), z(4, 16), z(1, 1, 16), z(1, 1, 16))
     with pytest.raises(ValueError, match="CUDA"):
-        ssm.state_slots_copy(z(2, 4), z(1, dtype=torch.int32), z(1, dtype=torch.int32))
+        ssm.state_slots_copy(z(2, 4), z(1, dtype=i32), z(1, dtype=i32))
     with pytest.raises(ValueError, match="CUDA"):
         ssm.causal_conv1d_bwd(z(1, 4, 8), z(4, 4), z(1, 4, 8))
     with pytest.raises(ValueError, match="CUDA"):
         ssm.causal_conv1d_fn(z(1, 4, 8), z(4, 4))
+    with pytest.raises(ValueError, match="CUDA"):
+        ssm.causal_conv1d_fwd(z(1, 4, 8), z(4, 4))
 
 
-def test_tensor_checks():
-    import torch
-    from selective_state_space_30_b200._tensors import inner_contiguous, io_code, need, pool_stride
-    t, f32 = torch.zeros(4, 6), torch.float32
-    here = t.get_device()          # -1: the checks of a device go by its number
-    need("t", None, f32, (1,), here)
-    need("t", t, f32, (4, 6), here)
-    for dtype, shape, word in ((torch.float64, (4, 6), "float64"), (f32, (6, 4), "shape")):
-        with pytest.raises(ValueError, match=word):
-            need("t", t, dtype, shape, here)
-    with pytest.raises(ValueError, match="contiguous"):
-        need("t", t.t(), f32, (6, 4), here)
-    with pytest.raises(ValueError, match="cuda:1"):
-        need("t", t, f32, (4, 6), 1)
-    with pytest.raises(ValueError):
-        io_code(t.double())
-    assert pool_stride("p", torch.zeros(5, 4, 6), f32, 4, 6, here) == 24
-    assert pool_stride("p", torch.zeros(5, 40)[:, :24].view(5, 4, 6), f32, 4, 6, here) == 40
-    assert pool_stride("p", torch.zeros(1, 40)[:, :24].view(1, 4, 6), f32, 4, 6, here) == 24
-    cut = torch.zeros(5, 4, 10)[:, :, :6]
-    for pool, dtype, word in ((cut, f32, "slot of p"), (torch.zeros(5, 4, 7), f32, "shape"), (torch.zeros(5, 24), f32, "shape"),
-                              (torch.zeros(5, 4, 6), torch.bfloat16, "bfloat16")):
-        with pytest.raises(ValueError, match=word):
-            pool_stride("p", pool, dtype, 4, 6, here)
-    assert inner_contiguous(torch.zeros(3, 5, 4).transpose(0, 1), 2) and not inner_contiguous(cut, 1)
+def test_front_ends_are_bound_to_the_loaded_library(ssm):
+    """The compiled front ends take exactly the arguments that they document, and need the build."""
+    from selective_state_space_30_b200 import _abi, _frontend
+    front = _frontend.load()
+    assert set(_frontend._ENTRIES) <= set(_abi.EXPORTS)
+    with pytest.raises(TypeError, match="7 arguments wanted"):
+        front.conv_update(1, 2)
+    with pytest.raises(KeyError):
+        front.bind({}, ssm.SsmError)
 
 
 # ------------------------------------------------- the fp64 forms against the oracle

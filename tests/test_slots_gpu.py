@@ -663,3 +663,60 @@ def test_bounds_out_of_order_stay_inside(ssm):
         ssm.causal_conv1d_packed(p["u"], w, i32(cu), conv_pool, out=guard[1])
         torch.cuda.synchronize()
         assert (guard[0] == 7).all() and (guard[2] == 7).all()
+
+
+def test_front_end_refusals(ssm):
+    """Tensors of another shape, type, device or layout than an operator takes."""
+    def t(*s, dt=torch.float32):
+        return torch.zeros(*s, dtype=dt, device="cuda")
+
+    bf = torch.bfloat16
+    x, w, pool, cu = t(2, 8), t(8, 4), t(3, 8, 3), i32([0, 2])
+    ok = dict(x=x, w=w, conv_states=pool)
+    for bad, word in ((dict(x=t(2, 8).double()), "bfloat16 or float32"), (dict(x=t(8, 2).t()), "contiguous"),
+                      (dict(w=t(7, 4)), "w must have shape"), (dict(w=t(8, 5)), "width of 1 to 4"),
+                      (dict(w=t(8, 4, dt=bf)), "w must be"), (dict(w=t(4, 8).t()), "w must be contiguous"),
+                      (dict(conv_states=t(3, 8, 2)), "conv_states must have shape"),
+                      (dict(conv_states=t(3, 8, 3, dt=bf)), "conv_states must be"),
+                      (dict(conv_states=t(3, 8, 6)[:, :, ::2]), "every slot"),
+                      (dict(conv_states=torch.zeros(3, 8, 3)), "on the device"),
+                      (dict(slots=t(2)), "slots must be"), (dict(slots=i32([0])), "slots must have shape"),
+                      (dict(bias=t(7)), "bias must have shape"), (dict(out=t(2, 7)), "out must have shape"),
+                      (dict(w=None), "w must be a tensor")):
+        with pytest.raises(ValueError, match=word):
+            ssm.causal_conv1d_update(**{**ok, **bad})
+    with pytest.raises(ValueError, match="n_seq"):
+        ssm.causal_conv1d_packed(t(8, 2), w, i32([]), pool)
+    with pytest.raises(ValueError, match="cu_seqlens must be"):
+        ssm.causal_conv1d_packed(t(8, 2), w, cu.long(), pool)
+    with pytest.raises(ValueError, match="has_state must be"):
+        ssm.causal_conv1d_packed(t(8, 2), w, cu, pool, has_state=i32([1]))
+    good = dict(u=t(8, 2), delta=t(8, 2), A=t(8, 16), B=t(1, 16, 2), C=t(1, 16, 2), cu_seqlens=cu, states=t(3, 8, 16))
+    for bad, word in ((dict(A=t(8)), "A must have shape"), (dict(A=None), "A must be a tensor"), (dict(C=t(1, 16, 3)), "C must"),
+                      (dict(delta=t(8, 2, dt=bf)), "delta must be"), (dict(states=t(3, 8, 16, dt=bf)), "states must be"),
+                      (dict(z=t(8, 3)), "z must"), (dict(workspace=torch.zeros(4, dtype=torch.uint8)), "workspace must")):
+        with pytest.raises(ValueError, match=word):
+            ssm.selective_scan_packed(**{**good, **bad})
+    with pytest.raises(ssm.SsmError):                    # the library's own refusals: 24 states, heads that do not divide
+        ssm.selective_scan_packed(**{**good, "A": t(8, 24), "B": t(1, 24, 2), "C": t(1, 24, 2), "states": t(3, 8, 24)})
+    with pytest.raises(ssm.SsmError):
+        ssm.selective_scan_packed(**{**good, "delta": t(3, 2), "A": t(3)})
+    with pytest.raises(ssm.SsmError):                    # a workspace that is too small
+        ssm.selective_scan_packed(**{**good, "u": t(8, 4096), "delta": t(8, 4096), "B": t(1, 16, 4096), "C": t(1, 16, 4096)},
+                                  workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+    step = dict(states=t(3, 8, 16), u=x, delta=t(2, 8), A=t(8, 16), B=t(2, 1, 16), C=t(2, 1, 16))
+    for bad, word in ((dict(B=t(1, 1, 16)), "B must"), (dict(delta=t(2, 8, 1)), "dimensions"), (dict(D=t(7)), "D must")):
+        with pytest.raises(ValueError, match=word):
+            ssm.selective_state_update_slots(**{**step, **bad})
+    with pytest.raises(ssm.SsmError):                    # slots off the 16-byte grid
+        ssm.selective_state_update_slots(**{**step, "states": torch.as_strided(t(3 * 130), (3, 8, 16), (130, 16, 1))})
+    for args, word in (((pool, i32([0]), i32([0, 1])), "dst must"), ((pool, t(1), i32([0])), "src must be"),
+                       ((pool, i32([0]), i32([0]), 2), "slot_dim"), ((t(3, 8, 6)[:, :, ::2], i32([0]), i32([0])), "every slot")):
+        with pytest.raises(ValueError, match=word):
+            ssm.state_slots_copy(*args)
+    with pytest.raises(ssm.SsmError):                    # layers that overlap
+        ssm.state_slots_copy(torch.as_strided(t(100), (2, 3, 8), (4, 8, 1)), i32([0]), i32([1]), slot_dim=1)
+    with pytest.raises(ssm.SsmError):                    # more pairs than a call takes
+        ssm.state_slots_copy(pool, i32([-1] * 5000), i32([0] * 5000))
+    with pytest.raises(ValueError, match="dout must"):
+        ssm.causal_conv1d_bwd(t(1, 8, 4), w, t(1, 8, 5))
