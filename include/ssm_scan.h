@@ -426,8 +426,9 @@ int ssm_selective_scan_bwd_test_hooks(int stall, int64_t wait_budget_us);
  *               the pool's slots and the elements from one slot to the next (at least a slot's
  *               own), so a pool may hold several layers' states side by side.
  *
- * All four calls launch on `stream` without a plan, allocate nothing, and may be captured into
- * a graph; their slots, lengths and flags are read when the kernels run.
+ * The calls launch on `stream` without a plan, allocate nothing, and may be captured into a
+ * graph (after a first call, which loads the kernels); slots, lengths and flags are read when the
+ * kernels run.  Two calls at once must not touch the same slots.
  */
 
 /*
@@ -436,9 +437,9 @@ int ssm_selective_scan_bwd_test_hooks(int stall, int64_t wait_budget_us);
  * history, and the sequence's last width - 1 inputs replace that history (inputs of a sequence
  * shorter than that join what the slot held).  states: the pool, slot s at s * slot_stride, a
  * slot being (dim, width - 1) in io_dtype, the oldest input first; not used for width 1.
- * width is 1 to 4, else SSM_ERR_UNSUPPORTED.  out must not alias x.  One kernel.
+ * width is 1 to 4, else SSM_ERR_UNSUPPORTED.  out must not overlap x.  One kernel.
  * SSM_ERR_INVALID_ARG for a bad size, stride or dtype, a pointer off its element's alignment,
- * or a NULL w, cu_seqlens, states (width > 1), x or out (total > 0).
+ * a NULL w, cu_seqlens, states (width > 1), x or out (total > 0), or out == x.
  */
 int ssm_causal_conv1d_packed_fwd(int64_t dim, int64_t total, int64_t n_seq, int32_t width, int32_t io_dtype,
                                  const void* x, const float* w, const float* bias, int silu,
@@ -470,7 +471,12 @@ int ssm_causal_conv1d_update(int64_t batch, int64_t dim, int32_t width, int32_t 
  * for the same dims and max_seqlen (0 bytes: it may be NULL); it is scratch after the call, and
  * one workspace must not serve two calls at once, nor two graphs that may run at once.
  *
- * out must not alias an input.  SSM_ERR_INVALID_ARG for a bad shape or stride, a pointer off its
+ * bf16 I/O with nheads < dim, dim / nheads == 64 and dstate 128 runs on the tensor cores once the
+ * sequences are 64 tokens or more in the mean, in blocks of 128 tokens: there a NaN or infinity in
+ * a token of u reaches every token of its block and sequence, the earlier ones too, and a wait for
+ * the tensor cores that runs out (half a second) leaves NaN in the rest of that head's outputs.
+ *
+ * out must not overlap an input.  SSM_ERR_INVALID_ARG for a bad shape or stride, a pointer off its
  * element's alignment, a workspace that is too small, or a NULL A, cu_seqlens, states, or u,
  * delta, B, C, out (seqlen > 0).
  */
@@ -527,7 +533,7 @@ int ssm_state_slots_copy(void* pool, int64_t n_layers, int64_t n_slots, int64_t 
  * are fp32, summed in a fixed order.  bias is the forward's (NULL: zero).  `workspace` (device,
  * 4-byte aligned, caller-owned) has at least ssm_causal_conv1d_bwd_workspace_size bytes; one
  * workspace must not serve two calls at once.  Two kernels on `stream`; the call allocates
- * nothing.  dx must not alias x or dout.  width is 1 to 4, else SSM_ERR_UNSUPPORTED;
+ * nothing.  dx must not overlap x or dout.  width is 1 to 4, else SSM_ERR_UNSUPPORTED;
  * SSM_ERR_INVALID_ARG for a bad shape or dtype, a pointer off its element's alignment, a
  * workspace that is too small, or a NULL w, dw, x, dout or dx.
  */

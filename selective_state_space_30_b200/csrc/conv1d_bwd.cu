@@ -21,7 +21,7 @@
 namespace {
 
 constexpr int kMaxWidth = 4;
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 
 struct ConvBwd {
     const void *x, *dout;
@@ -144,7 +144,7 @@ __device__ __forceinline__ Piece<T> load_piece(const T* x, const T* go, int64_t 
 // the 16-byte grid have their pieces at different tokens; the arithmetic is the same.)
 // ALIGNED: every row of x, dout and dx starts on the 16-byte grid.
 template <typename T, int W, bool ALIGNED, bool SILU>
-__global__ void __launch_bounds__(32 * kWarps, 2) conv1d_bwd_kernel(const ConvBwd p) {
+__global__ void __launch_bounds__(32 * kWarps, 4) conv1d_bwd_kernel(const ConvBwd p) {
     constexpr int V = 16 / sizeof(T), H = W - 1, PW = Piece<T>::PW;
     const int lane = threadIdx.x & 31;
     const int64_t id = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -182,8 +182,10 @@ __global__ void __launch_bounds__(32 * kWarps, 2) conv1d_bwd_kernel(const ConvBw
     const float2 bias = p.bias ? make_float2(__ldg(p.bias + d[0]), __ldg(p.bias + d[1])) : ssm::dup2(0.f);
     auto load = [&](int r, int64_t tile) {
         if constexpr (ALIGNED) {
-            const int64_t t = (tile * 32 + lane) * V;
-            return load_aligned<T>(x[r] + t, go[r] + t, t < L, lane == 0 && t > 0);
+            // both rows alike: only the row's last tile has lanes behind its end
+            const int64_t o = (tile * 32 + lane) * V;
+            const bool in = tile + 1 < tile1 || o < L;
+            return load_aligned<T>(x[r] + o, go[r] + o, in, lane == 0 && tile > 0);
         }
         const int64_t t = tile * 32 * V - m[r];
         if (tile >= tiles[r]) return Piece<T>{};      // this row ends a tile before the other
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) conv1d_bwd_kernel(const ConvBw
         for (int r = 0; r < 2; ++r) {
             const int64_t t = (tile * 32 + lane) * V - m[r];
             if (r && !both) break;
-            if (ALIGNED ? t < L : t >= 0 && t + V <= L) {
+            if (ALIGNED ? tile + 1 < tile1 || t < L : t >= 0 && t + V <= L) {
                 uint32_t u[4];
                 if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -408,7 +410,8 @@ extern "C" int ssm_causal_conv1d_bwd(int64_t batch, int64_t dim, int64_t seqlen,
     const int rc = ssm_causal_conv1d_bwd_workspace_size(batch, dim, seqlen, width, io_dtype, &need);
     if (rc != SSM_OK) return rc;
     if (!w || !dw) return SSM_ERR_INVALID_ARG;
-    if (need > 0 && (!x || !dout || !dx || !workspace || workspace_bytes < need)) return SSM_ERR_INVALID_ARG;
+    if (need > 0 && (!x || !dout || !dx || dx == x || dx == dout || !workspace || workspace_bytes < need))
+        return SSM_ERR_INVALID_ARG;
     const uintptr_t esz = io_dtype == SSM_BF16 ? 2 : 4;
     if (!aligned_to(x, esz) || !aligned_to(dout, esz) || !aligned_to(dx, esz) || !aligned_to(workspace, 4))
         return SSM_ERR_INVALID_ARG;

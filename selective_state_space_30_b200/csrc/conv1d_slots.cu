@@ -626,7 +626,7 @@ extern "C" int ssm_causal_conv1d_packed_fwd(int64_t dim, int64_t total, int64_t 
     if (width < 1 || width > kMaxWidth) return SSM_ERR_UNSUPPORTED;
     if (n_seq == 0) return SSM_OK;
     if (!w || !cu_seqlens || (width > 1 && !states)) return SSM_ERR_INVALID_ARG;
-    if (total > 0 && (!x || !out)) return SSM_ERR_INVALID_ARG;
+    if (total > 0 && (!x || !out || x == out)) return SSM_ERR_INVALID_ARG;
     if (width > 1 && slot_stride < dim * (width - 1)) return SSM_ERR_INVALID_ARG;
     const uintptr_t esz = io_dtype == SSM_BF16 ? 2 : 4;
     if (!aligned_to(x, esz) || !aligned_to(out, esz) || !aligned_to(states, esz)) return SSM_ERR_INVALID_ARG;

@@ -47,7 +47,9 @@ bool on_tensor_cores(const ssm_dims_t& d) { return ssm::packed::ssd_packed_cover
 // products.  Sequences are cut, into chunks of one share, where the longest is over four shares
 // and so would still run when everything else is done: one prompt of 8191 tokens x 1536 channels
 // takes 203 us cut at 352 tokens, 231 at 448, 292 at 672; 24 ragged prompts (16384 tokens x 4096
-// channels, the longest under two shares) 523 us uncut and 666 cut at 1184.
+// channels, the longest under two shares) 523 us uncut and 666 cut at 1184.  On the tensor cores a
+// middle chunk's first pass costs less than half of its second, so two and a half shares do: two
+// prompts of 4096 tokens, 32 heads, 195 us uncut and 138 cut at 768; six (two shares) 114 and 154.
 int64_t choose_chunk(const ssm_dims_t& d, int64_t max_seqlen) {
     const bool ssd = on_tensor_cores(d);
     const int64_t ct = tile_channels(d.dstate), gd = d.dim / d.ngroups;
@@ -62,7 +64,7 @@ int64_t choose_chunk(const ssm_dims_t& d, int64_t max_seqlen) {
     if (q < least) q = least;
     const int64_t step = ssd ? 128 : 32;
     q = (q + step - 1) / step * step;
-    return longest > 4 * q ? q : kNoChunk;
+    return longest > (ssd ? 5 * q / 2 : 4 * q) ? q : kNoChunk;
 }
 
 bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

@@ -27,7 +27,7 @@ def _raises(ssm, status, fn, *args):
 
 def test_conv_packed_refusals(ssm):
     ok = dict(dim=8, total=20, n_seq=2, width=4, io=ssm.SSM_BF16, x=A16, w=A16, bias=None, silu=True, cu=A16, slots=None,
-              has=None, states=A16, n_slots=3, stride=24, out=A16)
+              has=None, states=A16, n_slots=3, stride=24, out=2 * A16)
 
     def rc(**kw):
         a = dict(ok, **kw)
@@ -35,7 +35,7 @@ def test_conv_packed_refusals(ssm):
 
     inv, uns = ssm.SSM_ERR_INVALID_ARG, ssm.SSM_ERR_UNSUPPORTED
     for bad in (dict(dim=0), dict(total=-1), dict(n_seq=-1), dict(io=7), dict(x=None), dict(w=None), dict(cu=None),
-                dict(states=None), dict(out=None), dict(n_slots=-1), dict(stride=23), dict(x=OFF1), dict(out=OFF1),
+                dict(states=None), dict(out=None), dict(out=A16), dict(n_slots=-1), dict(stride=23), dict(x=OFF1), dict(out=OFF1),
                 dict(states=OFF1), dict(total=2 ** 31), dict(n_seq=2 ** 31), dict(n_slots=2 ** 31)):
         assert rc(**bad) == inv, bad
     assert rc(width=0) == uns and rc(width=5) == uns
@@ -124,13 +124,13 @@ def test_conv_bwd_refusals(ssm):
     size = ssm.ssm_causal_conv1d_bwd_workspace_size
     need = size(2, 8, 30, 4, ssm.SSM_BF16)
     assert need >= 2 * 8 * 5 * 4 and size(2, 8, 0, 4, ssm.SSM_BF16) == 0
-    ok = dict(batch=2, dim=8, L=30, width=4, io=ssm.SSM_BF16, x=A16, w=A16, bias=None, silu=True, dout=A16, dx=A16, dw=A16,
+    ok = dict(batch=2, dim=8, L=30, width=4, io=ssm.SSM_BF16, x=A16, w=A16, bias=None, silu=True, dout=A16, dx=2 * A16, dw=A16,
               db=None, ws=A16, nws=need)
 
     def rc(**kw):
         return ssm.ssm_causal_conv1d_bwd(*dict(ok, **kw).values(), check=False)
 
-    for bad in (dict(x=None), dict(w=None), dict(dout=None), dict(dx=None), dict(dw=None), dict(ws=None), dict(nws=need - 1),
+    for bad in (dict(x=None), dict(w=None), dict(dout=None), dict(dx=None), dict(dx=A16), dict(x=2 * A16), dict(dw=None), dict(ws=None), dict(nws=need - 1),
                 dict(batch=-1), dict(dim=0), dict(L=-1), dict(io=3), dict(x=OFF1), dict(dout=OFF1), dict(dx=OFF1)):
         assert rc(**bad) == ssm.SSM_ERR_INVALID_ARG, bad
     assert rc(width=5) == ssm.SSM_ERR_UNSUPPORTED and rc(width=0) == ssm.SSM_ERR_UNSUPPORTED

@@ -67,6 +67,10 @@ CONV = [
     ([40, 55], 12, 4, "bf16", True, True, 1, 0, 0, True),
     ([40, 56], 12, 1, "bf16", True, True, 0, 0, 0, False),                 # no history at all
     ([3, 4, 5] * 40, 300, 4, "bf16", True, True, 0, 0, 0, False),          # many short prompts
+    ([1, 2, 0, 5] * 300, 3, 4, "bf16", True, True, 0, 0, 0, False),        # more than a CTA looks at one by one
+    ([900, 1, 700], 1, 4, "f32", True, True, 0, 3, 0, False),              # one channel
+    ([4096, 4096], 130, 4, "bf16", True, True, 0, 8, 0, False),            # aligned rows, whole pieces, an odd last pair
+    ([2048, 2048], 67, 3, "f32", True, False, 0, 0, 0, False),
 ]
 
 
@@ -225,6 +229,9 @@ SCAN = [
     ([25, 39], 64, 4, 2, 8, "bf16", 0, 0, 0, False, {}),
     ([20, 12], 32, 32, 1, 16, "bf16", 0, 0, 0, False, dict(softplus=False, bias=False)),
     ([2, 3, 1] * 30, 50, 50, 1, 16, "bf16", 0, 0, 0, False, {}),                     # many short prompts
+    ([1, 0, 3] * 130, 4, 4, 1, 16, "f32", 0, 0, 0, False, {}),                       # more than a CTA's threads
+    ([70, 1], 1, 1, 1, 8, "bf16", 0, 0, 0, False, {}),                               # one channel
+    ([70, 9], 2, 1, 1, 16, "f32", 0, 0, 0, False, {}),                               # one head of two channels
 ]
 
 
