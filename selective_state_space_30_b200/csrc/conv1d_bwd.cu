@@ -8,8 +8,14 @@
 // HBM-bound: x and dout are read once and dx is written once.  A warp walks a stretch of two
 // rows from its end to its start, 32 16-byte pieces at a time: the inputs before a piece come
 // from the lane below, the dv behind it from the lane above, and lane 31's from the tile before.
-// dw and dbias stay in registers for the stretch; each warp writes one partial and a second
-// kernel adds the partials in a fixed order, so the gradients repeat bit for bit.
+// dw and dbias stay in registers over a warp's stretches and are added over the CTA's warps in
+// order; where a channel is split over CTAs a second kernel adds their partials, in order too, so
+// the gradients repeat bit for bit.
+//
+// Measured on one B200: 8 x 1536 x 2048 bf16, width 4, 43 us (3.5 TB/s; 23 us of HBM time), issue
+// 59 % busy with 14 of 64 warps an SM (128 registers hold two rows and the loads ahead); three CTAs an
+// SM with 84 registers 61 us.  2 x 768 x 1021 fp32 8.5 us in a graph, 9.6 with partials and a second
+// kernel (10.2 and 13.5 us a call).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -21,15 +27,16 @@
 namespace {
 
 constexpr int kMaxWidth = 4;
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
 
 struct ConvBwd {
     const void *x, *dout;
     const float *w, *bias;
     void* dx;
-    float* part;            // [batch * n_seg][dim][W + 1]
-    int64_t rows, dim, seqlen;
-    int64_t tiles, tiles_per_seg, n_seg;
+    float *dw, *dbias;
+    float* part;            // [n_split][dim][W + 1] where a channel's sums are split over CTAs
+    int64_t batch, dim, seqlen;
+    int64_t tiles_per_seg, n_seg, n_split;
     int silu;
 };
 
@@ -144,35 +151,13 @@ __device__ __forceinline__ Piece<T> load_piece(const T* x, const T* go, int64_t 
 // the 16-byte grid have their pieces at different tokens; the arithmetic is the same.)
 // ALIGNED: every row of x, dout and dx starts on the 16-byte grid.
 template <typename T, int W, bool ALIGNED, bool SILU>
-__global__ void __launch_bounds__(32 * kWarps, 4) conv1d_bwd_kernel(const ConvBwd p) {
+__global__ void __launch_bounds__(32 * kWarps, 2) conv1d_bwd_kernel(const ConvBwd p) {
     constexpr int V = 16 / sizeof(T), H = W - 1, PW = Piece<T>::PW;
-    const int lane = threadIdx.x & 31;
-    const int64_t id = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int64_t pairs = (p.dim + 1) / 2, batch = p.rows / p.dim;
-    if (id >= batch * pairs * p.n_seg) return;
-    const int64_t seg = id % p.n_seg, b = id / p.n_seg / pairs, d0 = id / p.n_seg % pairs * 2, L = p.seqlen;
+    __shared__ float sums[kWarps][2 * (W + 1)];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t d0 = blockIdx.x / p.n_split * 2, split = blockIdx.x % p.n_split, L = p.seqlen;
     const bool both = d0 + 1 < p.dim;                 // an odd last channel pairs with itself and writes once
     const int64_t d[2] = {d0, both ? d0 + 1 : d0};
-    const T *x[2], *go[2];
-    T* dx[2];
-    int m[2];
-    bool grid[2];
-    int64_t tiles[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int64_t row = (b * p.dim + d[r]) * L;
-        x[r] = static_cast<const T*>(p.x) + row;
-        go[r] = static_cast<const T*>(p.dout) + row;
-        dx[r] = static_cast<T*>(p.dx) + row;
-        // pieces sit on dx's 16-byte grid: the row's first one may start up to V-1 tokens early
-        m[r] = ALIGNED ? 0 : (int)((reinterpret_cast<uintptr_t>(dx[r]) & 15u) / sizeof(T));
-        grid[r] = ((reinterpret_cast<uintptr_t>(x[r]) ^ reinterpret_cast<uintptr_t>(dx[r])) & 15u) == 0 &&
-                  ((reinterpret_cast<uintptr_t>(go[r]) ^ reinterpret_cast<uintptr_t>(dx[r])) & 15u) == 0;
-        // the row's own tiles end where its tokens do, which may be one tile earlier than another row's
-        tiles[r] = (L + m[r] + 32 * V - 1) / (32 * V);
-    }
-    const int64_t all = tiles[0] > tiles[1] ? tiles[0] : tiles[1];
-    const int64_t tile0 = seg * p.tiles_per_seg, tile1 = tile0 + p.tiles_per_seg < all ? tile0 + p.tiles_per_seg : all;
     float2 w[W], dw[W], db = ssm::dup2(0.f);
 #pragma unroll
     for (int k = 0; k < W; ++k) {
@@ -180,119 +165,143 @@ __global__ void __launch_bounds__(32 * kWarps, 4) conv1d_bwd_kernel(const ConvBw
         dw[k] = ssm::dup2(0.f);
     }
     const float2 bias = p.bias ? make_float2(__ldg(p.bias + d[0]), __ldg(p.bias + d[1])) : ssm::dup2(0.f);
-    auto load = [&](int r, int64_t tile) {
-        if constexpr (ALIGNED) {
-            // both rows alike: only the row's last tile has lanes behind its end
-            const int64_t o = (tile * 32 + lane) * V;
-            const bool in = tile + 1 < tile1 || o < L;
-            return load_aligned<T>(x[r] + o, go[r] + o, in, lane == 0 && tile > 0);
-        }
-        const int64_t t = tile * 32 * V - m[r];
-        if (tile >= tiles[r]) return Piece<T>{};      // this row ends a tile before the other
-        return load_piece<T>(x[r], go[r], t + lane * V, L, grid[r] && t >= 0 && t + 32 * V <= L, lane);
-    };
-    Piece<T> next[2] = {};
-    if (tile1 > tile0) {
-        next[0] = load(0, tile1 - 1);
-        next[1] = load(1, tile1 - 1);
-    }
-    // dv of the W-1 tokens behind the stretch, on lanes 0 .. W-2, then on every lane
-    float2 behind[H > 0 ? H : 1];
-    {
-        float g[2] = {0.f, 0.f};
+    // the pair's stretches, one after the other over the warps of its CTAs
+    for (int64_t item = split * kWarps + warp; item < p.batch * p.n_seg; item += p.n_split * kWarps) {
+        const int64_t seg = item % p.n_seg, b = item / p.n_seg;
+        const T *x[2], *go[2];
+        T* dx[2];
+        int m[2];
+        bool grid[2];
+        int64_t tiles[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const int64_t t = tile1 * 32 * V - m[r] + lane;
-            if (lane < H && t < L) {
-                float v = r ? bias.y : bias.x;
+            const int64_t row = (b * p.dim + d[r]) * L;
+            x[r] = static_cast<const T*>(p.x) + row;
+            go[r] = static_cast<const T*>(p.dout) + row;
+            dx[r] = static_cast<T*>(p.dx) + row;
+            // pieces sit on dx's 16-byte grid: the row's first one may start up to V-1 tokens early
+            m[r] = ALIGNED ? 0 : (int)((reinterpret_cast<uintptr_t>(dx[r]) & 15u) / sizeof(T));
+            grid[r] = ((reinterpret_cast<uintptr_t>(x[r]) ^ reinterpret_cast<uintptr_t>(dx[r])) & 15u) == 0 &&
+                      ((reinterpret_cast<uintptr_t>(go[r]) ^ reinterpret_cast<uintptr_t>(dx[r])) & 15u) == 0;
+            // the row's own tiles end where its tokens do, which may be one tile earlier than another row's
+            tiles[r] = (L + m[r] + 32 * V - 1) / (32 * V);
+        }
+        const int64_t all = tiles[0] > tiles[1] ? tiles[0] : tiles[1];
+        const int64_t tile0 = seg * p.tiles_per_seg, tile1 = tile0 + p.tiles_per_seg < all ? tile0 + p.tiles_per_seg : all;
+        auto load = [&](int r, int64_t tile) {
+            if constexpr (ALIGNED) {
+                // both rows alike: only the row's last tile has lanes behind its end
+                const int64_t o = (tile * 32 + lane) * V;
+                const bool in = tile + 1 < tile1 || o < L;
+                return load_aligned<T>(x[r] + o, go[r] + o, in, lane == 0 && tile > 0);
+            }
+            const int64_t t = tile * 32 * V - m[r];
+            if (tile >= tiles[r]) return Piece<T>{};      // this row ends a tile before the other
+            return load_piece<T>(x[r], go[r], t + lane * V, L, grid[r] && t >= 0 && t + 32 * V <= L, lane);
+        };
+        Piece<T> next[2] = {};
+        if (tile1 > tile0) {
+            next[0] = load(0, tile1 - 1);
+            next[1] = load(1, tile1 - 1);
+        }
+        // dv of the W-1 tokens behind the stretch, on lanes 0 .. W-2, then on every lane
+        float2 behind[H > 0 ? H : 1];
+        {
+            float g[2] = {0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < W; ++k) {
-                    const int64_t s = t - H + k;
-                    if (s >= 0) v = fmaf(r ? w[k].y : w[k].x, to_f<T>(x[r][s]), v);
+            for (int r = 0; r < 2; ++r) {
+                const int64_t t = tile1 * 32 * V - m[r] + lane;
+                if (lane < H && t < L) {
+                    float v = r ? bias.y : bias.x;
+#pragma unroll
+                    for (int k = 0; k < W; ++k) {
+                        const int64_t s = t - H + k;
+                        if (s >= 0) v = fmaf(r ? w[k].y : w[k].x, to_f<T>(x[r][s]), v);
+                    }
+                    g[r] = dact2<SILU>(ssm::dup2(v), ssm::dup2(to_f<T>(go[r][t]))).x;
                 }
-                g[r] = dact2<SILU>(ssm::dup2(v), ssm::dup2(to_f<T>(go[r][t]))).x;
             }
+#pragma unroll
+            for (int k = 0; k < H; ++k)
+                behind[k] = make_float2(__shfl_sync(0xffffffffu, g[0], k), __shfl_sync(0xffffffffu, g[1], k));
         }
-#pragma unroll
-        for (int k = 0; k < H; ++k)
-            behind[k] = make_float2(__shfl_sync(0xffffffffu, g[0], k), __shfl_sync(0xffffffffu, g[1], k));
-    }
-    for (int64_t tile = tile1 - 1; tile >= tile0; --tile) {
-        const Piece<T> cur[2] = {next[0], next[1]};
-        if (tile > tile0) {
-            next[0] = load(0, tile - 1);
-            next[1] = load(1, tile - 1);
-        }
-        // tokens t - 4 .. t + V - 1 of x; t .. t + V + H - 1 of dv
-        float2 xv[4 + V], dv[V + H];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const uint32_t xw[4] = {cur[r].x.x, cur[r].x.y, cur[r].x.z, cur[r].x.w};
-            const uint32_t gw[4] = {cur[r].g.x, cur[r].g.y, cur[r].g.z, cur[r].g.w};
-            uint32_t bw[PW];
-#pragma unroll
-            for (int i = 0; i < PW; ++i) {
-                bw[i] = __shfl_up_sync(0xffffffffu, xw[4 - PW + i], 1);
-                if (lane == 0) bw[i] = cur[r].before[i];
+        for (int64_t tile = tile1 - 1; tile >= tile0; --tile) {
+            const Piece<T> cur[2] = {next[0], next[1]};
+            if (tile > tile0) {
+                next[0] = load(0, tile - 1);
+                next[1] = load(1, tile - 1);
             }
-            float xb[4], xc[V], gc[V];
-            unpack<T, 4>(bw, xb);
-            unpack<T, V>(xw, xc);
-            unpack<T, V>(gw, gc);
+            // tokens t - 4 .. t + V - 1 of x; t .. t + V + H - 1 of dv
+            float2 xv[4 + V], dv[V + H];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) (r ? xv[e].y : xv[e].x) = xb[e];
+            for (int r = 0; r < 2; ++r) {
+                const uint32_t xw[4] = {cur[r].x.x, cur[r].x.y, cur[r].x.z, cur[r].x.w};
+                const uint32_t gw[4] = {cur[r].g.x, cur[r].g.y, cur[r].g.z, cur[r].g.w};
+                uint32_t bw[PW];
+#pragma unroll
+                for (int i = 0; i < PW; ++i) {
+                    bw[i] = __shfl_up_sync(0xffffffffu, xw[4 - PW + i], 1);
+                    if (lane == 0) bw[i] = cur[r].before[i];
+                }
+                float xb[4], xc[V], gc[V];
+                unpack<T, 4>(bw, xb);
+                unpack<T, V>(xw, xc);
+                unpack<T, V>(gw, gc);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) (r ? xv[e].y : xv[e].x) = xb[e];
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    (r ? xv[4 + e].y : xv[4 + e].x) = xc[e];
+                    (r ? dv[e].y : dv[e].x) = gc[e];
+                }
+            }
+            const float2* xh = xv + 4 - H;                // xh[e + k] meets w[k] at token e
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                (r ? xv[4 + e].y : xv[4 + e].x) = xc[e];
-                (r ? dv[e].y : dv[e].x) = gc[e];
+                float2 v = bias;
+#pragma unroll
+                for (int k = 0; k < W; ++k) v = ssm::fma2(w[k], xh[e + k], v);
+                dv[e] = dact2<SILU>(v, dv[e]);
+                db = ssm::add2(db, dv[e]);
+#pragma unroll
+                for (int k = 0; k < W; ++k) dw[k] = ssm::fma2(dv[e], xh[e + k], dw[k]);
             }
-        }
-        const float2* xh = xv + 4 - H;                // xh[e + k] meets w[k] at token e
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            float2 v = bias;
+            for (int k = 0; k < H; ++k) {
+                dv[V + k] = make_float2(__shfl_down_sync(0xffffffffu, dv[k].x, 1), __shfl_down_sync(0xffffffffu, dv[k].y, 1));
+                if (lane == 31) dv[V + k] = behind[k];
+                behind[k] = make_float2(__shfl_sync(0xffffffffu, dv[k].x, 0), __shfl_sync(0xffffffffu, dv[k].y, 0));
+            }
+            float2 o[V];
 #pragma unroll
-            for (int k = 0; k < W; ++k) v = ssm::fma2(w[k], xh[e + k], v);
-            dv[e] = dact2<SILU>(v, dv[e]);
-            db = ssm::add2(db, dv[e]);
+            for (int e = 0; e < V; ++e) {
+                o[e] = ssm::mul2(w[H], dv[e]);
 #pragma unroll
-            for (int k = 0; k < W; ++k) dw[k] = ssm::fma2(dv[e], xh[e + k], dw[k]);
-        }
+                for (int k = 0; k < H; ++k) o[e] = ssm::fma2(w[k], dv[e + H - k], o[e]);
+            }
 #pragma unroll
-        for (int k = 0; k < H; ++k) {
-            dv[V + k] = make_float2(__shfl_down_sync(0xffffffffu, dv[k].x, 1), __shfl_down_sync(0xffffffffu, dv[k].y, 1));
-            if (lane == 31) dv[V + k] = behind[k];
-            behind[k] = make_float2(__shfl_sync(0xffffffffu, dv[k].x, 0), __shfl_sync(0xffffffffu, dv[k].y, 0));
-        }
-        float2 o[V];
+            for (int r = 0; r < 2; ++r) {
+                const int64_t t = (tile * 32 + lane) * V - m[r];
+                if (r && !both) break;
+                if (ALIGNED ? tile + 1 < tile1 || t < L : t >= 0 && t + V <= L) {
+                    uint32_t u[4];
+                    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            o[e] = ssm::mul2(w[H], dv[e]);
+                        for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(r ? o[i].y : o[i].x);
+                    } else {
 #pragma unroll
-            for (int k = 0; k < H; ++k) o[e] = ssm::fma2(w[k], dv[e + H - k], o[e]);
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int64_t t = (tile * 32 + lane) * V - m[r];
-            if (r && !both) break;
-            if (ALIGNED ? tile + 1 < tile1 || t < L : t >= 0 && t + V <= L) {
-                uint32_t u[4];
-                if constexpr (sizeof(T) == 4) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(r ? o[i].y : o[i].x);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const __nv_bfloat162 b2 = r ? __floats2bfloat162_rn(o[2 * i].y, o[2 * i + 1].y)
-                                                    : __floats2bfloat162_rn(o[2 * i].x, o[2 * i + 1].x);
-                        u[i] = *reinterpret_cast<const uint32_t*>(&b2);
+                        for (int i = 0; i < 4; ++i) {
+                            const __nv_bfloat162 b2 = r ? __floats2bfloat162_rn(o[2 * i].y, o[2 * i + 1].y)
+                                                        : __floats2bfloat162_rn(o[2 * i].x, o[2 * i + 1].x);
+                            u[i] = *reinterpret_cast<const uint32_t*>(&b2);
+                        }
                     }
-                }
-                *reinterpret_cast<uint4*>(dx[r] + t) = make_uint4(u[0], u[1], u[2], u[3]);
-            } else if (!ALIGNED) {
+                    *reinterpret_cast<uint4*>(dx[r] + t) = make_uint4(u[0], u[1], u[2], u[3]);
+                } else if (!ALIGNED) {
 #pragma unroll
-                for (int e = 0; e < V; ++e)
-                    if (t + e >= 0 && t + e < L) dx[r][t + e] = from_f<T>(r ? o[e].y : o[e].x);
+                    for (int e = 0; e < V; ++e)
+                        if (t + e >= 0 && t + e < L) dx[r][t + e] = from_f<T>(r ? o[e].y : o[e].x);
+                }
             }
         }
     }
@@ -305,15 +314,23 @@ __global__ void __launch_bounds__(32 * kWarps, 4) conv1d_bwd_kernel(const ConvBw
                                                  __shfl_xor_sync(0xffffffffu, dw[k].y, s)));
     }
     if (lane == 0) {
-        float* o = p.part + ((b * p.n_seg + seg) * p.dim + d0) * (W + 1);
 #pragma unroll
-        for (int k = 0; k < W; ++k) o[k] = dw[k].x;
-        o[W] = db.x;
-        if (both) {
-#pragma unroll
-            for (int k = 0; k < W; ++k) o[W + 1 + k] = dw[k].y;
-            o[2 * W + 1] = db.y;
+        for (int k = 0; k < W; ++k) {
+            sums[warp][k] = dw[k].x;
+            sums[warp][W + 1 + k] = dw[k].y;
         }
+        sums[warp][W] = db.x;
+        sums[warp][2 * W + 1] = db.y;
+    }
+    __syncthreads();
+    if (threadIdx.x < (both ? 2 : 1) * (W + 1)) {
+        float a = sums[0][threadIdx.x];
+#pragma unroll
+        for (int q = 1; q < kWarps; ++q) a += sums[q][threadIdx.x];
+        const int r = threadIdx.x / (W + 1), k = threadIdx.x % (W + 1);
+        if (p.n_split > 1) p.part[(split * p.dim + d0 + r) * (W + 1) + k] = a;
+        else if (k < W) p.dw[(d0 + r) * W + k] = a;
+        else if (p.dbias) p.dbias[d0 + r] = a;
     }
 }
 
@@ -338,21 +355,24 @@ __global__ void __launch_bounds__(256) conv1d_bwd_sum_kernel(const float* part, 
 }
 
 struct Plan {
-    int64_t tiles, tiles_per_seg, n_seg;
+    int64_t tiles_per_seg, n_seg, n_split;
 };
 
-// Rows are cut into stretches where there are too few pairs of them to fill the machine (32 warps
-// on each of 148 SMs); the shape alone decides, so the sums' order is the shape's.
+// A pair of channels is one CTA's where there are enough pairs for two CTAs on each of 148 SMs: its
+// sums then need no second kernel.  Fewer pairs are split over several CTAs, and rows into stretches
+// as far as the CTAs' warps need them.  The shape alone decides, so the sums' order is the shape's.
 Plan plan_of(int64_t batch, int64_t dim, int64_t seqlen, int io_dtype) {
-    const int64_t V = io_dtype == SSM_BF16 ? 8 : 4;
-    Plan q;
-    q.tiles = (seqlen + V - 1 + 32 * V - 1) / (32 * V);
-    const int64_t rows = batch * ((dim + 1) / 2), want = 148 * 32;
-    int64_t n = rows > 0 ? (want + rows - 1) / rows : 1;
-    if (n > q.tiles) n = q.tiles;
-    if (n < 1) n = 1;
-    q.tiles_per_seg = (q.tiles + n - 1) / n;
-    q.n_seg = q.tiles_per_seg > 0 ? (q.tiles + q.tiles_per_seg - 1) / q.tiles_per_seg : 1;
+    const int64_t V = io_dtype == SSM_BF16 ? 8 : 4, pairs = (dim + 1) / 2;
+    const int64_t tiles = (seqlen + V - 1 + 32 * V - 1) / (32 * V);
+    Plan q{1, 1, 1};
+    if (batch <= 0 || seqlen <= 0) return q;
+    const int64_t ctas = (148 * 2 + pairs - 1) / pairs;
+    int64_t seg = (ctas * kWarps + batch - 1) / batch;
+    if (seg > tiles) seg = tiles;
+    q.tiles_per_seg = (tiles + seg - 1) / seg;
+    q.n_seg = (tiles + q.tiles_per_seg - 1) / q.tiles_per_seg;
+    const int64_t most = (batch * q.n_seg + kWarps - 1) / kWarps;
+    q.n_split = ctas < most ? ctas : most;
     return q;
 }
 
@@ -370,7 +390,7 @@ int check_shape(int64_t batch, int64_t dim, int64_t seqlen, int32_t width, int32
 
 template <typename T, int W>
 int launch(const ConvBwd& p, bool aligned, cudaStream_t s) {
-    const int64_t ctas = (p.rows / p.dim * ((p.dim + 1) / 2) * p.n_seg + kWarps - 1) / kWarps;
+    const int64_t ctas = (p.dim + 1) / 2 * p.n_split;
     if (ctas > 0x7FFFFFFF) return SSM_ERR_UNSUPPORTED;
     const unsigned g = (unsigned)ctas;
     if (aligned && p.silu) conv1d_bwd_kernel<T, W, true, true><<<g, 32 * kWarps, 0, s>>>(p);
@@ -398,7 +418,8 @@ extern "C" int ssm_causal_conv1d_bwd_workspace_size(int64_t batch, int64_t dim, 
     if (!bytes) return SSM_ERR_INVALID_ARG;
     const int rc = check_shape(batch, dim, seqlen, width, io_dtype);
     if (rc != SSM_OK) return rc;
-    *bytes = seqlen == 0 ? 0 : (size_t)(batch * plan_of(batch, dim, seqlen, io_dtype).n_seg * dim * (width + 1)) * 4;
+    const Plan q = plan_of(batch, dim, seqlen, io_dtype);
+    *bytes = q.n_split > 1 ? (size_t)(q.n_split * dim * (width + 1)) * 4 : 0;
     return SSM_OK;
 }
 
@@ -410,29 +431,25 @@ extern "C" int ssm_causal_conv1d_bwd(int64_t batch, int64_t dim, int64_t seqlen,
     const int rc = ssm_causal_conv1d_bwd_workspace_size(batch, dim, seqlen, width, io_dtype, &need);
     if (rc != SSM_OK) return rc;
     if (!w || !dw) return SSM_ERR_INVALID_ARG;
-    if (need > 0 && (!x || !dout || !dx || dx == x || dx == dout || !workspace || workspace_bytes < need))
-        return SSM_ERR_INVALID_ARG;
+    const bool tokens = batch > 0 && seqlen > 0;
+    if (tokens && (!x || !dout || !dx || dx == x || dx == dout)) return SSM_ERR_INVALID_ARG;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return SSM_ERR_INVALID_ARG;
     const uintptr_t esz = io_dtype == SSM_BF16 ? 2 : 4;
     if (!aligned_to(x, esz) || !aligned_to(dout, esz) || !aligned_to(dx, esz) || !aligned_to(workspace, 4))
         return SSM_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    int64_t n_part = 0;
-    if (need > 0) {
-        const Plan q = plan_of(batch, dim, seqlen, io_dtype);
-        ConvBwd p{};
-        p.x = x; p.dout = dout; p.w = w; p.bias = bias; p.dx = dx; p.part = static_cast<float*>(workspace);
-        p.rows = batch * dim; p.dim = dim; p.seqlen = seqlen;
-        p.tiles = q.tiles; p.tiles_per_seg = q.tiles_per_seg; p.n_seg = q.n_seg;
-        p.silu = silu ? 1 : 0;
-        const bool aligned = seqlen * (int64_t)esz % 16 == 0 && aligned_to(x, 16) && aligned_to(dout, 16) && aligned_to(dx, 16);
-        const int r = io_dtype == SSM_BF16 ? launch_t<__nv_bfloat16>(p, width, aligned, s)
-                                            : launch_t<float>(p, width, aligned, s);
-        if (r != SSM_OK) return r;
-        n_part = batch * q.n_seg;
-    }
-    // with no tokens every gradient is an empty sum
+    // without tokens every gradient is an empty sum: the kernel finds no stretch and writes zeros
+    const Plan q = plan_of(batch, dim, seqlen, io_dtype);
+    ConvBwd p{};
+    p.x = x; p.dout = dout; p.w = w; p.bias = bias; p.dx = dx; p.dw = dw; p.dbias = dbias;
+    p.part = static_cast<float*>(workspace);
+    p.batch = tokens ? batch : 0; p.dim = dim; p.seqlen = seqlen;
+    p.tiles_per_seg = q.tiles_per_seg; p.n_seg = q.n_seg; p.n_split = q.n_split;
+    p.silu = silu ? 1 : 0;
+    const bool aligned = seqlen * (int64_t)esz % 16 == 0 && aligned_to(x, 16) && aligned_to(dout, 16) && aligned_to(dx, 16);
+    const int r = io_dtype == SSM_BF16 ? launch_t<__nv_bfloat16>(p, width, aligned, s) : launch_t<float>(p, width, aligned, s);
+    if (r != SSM_OK || q.n_split == 1) return r;
     const int64_t n = dim * (width + 1);
-    conv1d_bwd_sum_kernel<<<(unsigned)((n + 31) / 32), dim3(32, 8), 0, s>>>(static_cast<const float*>(workspace), n_part,
-                                                                           dim, width, dw, dbias);
+    conv1d_bwd_sum_kernel<<<(unsigned)((n + 31) / 32), dim3(32, 8), 0, s>>>(p.part, q.n_split, dim, width, dw, dbias);
     return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }

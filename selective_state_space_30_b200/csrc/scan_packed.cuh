@@ -16,11 +16,21 @@
 // fp32 pipe (three operations per (t, channel, state)) in the per-head layout, whose decay is
 // one ex2 per (t, channel).
 //
-// Layout.  A lane holds 8 states of CPL channels, N/8 lanes a channel group: the B and C of a
-// step, fp32 in shared memory, then serve CPL channels per load, and the sum over states
-// crosses lanes only log2(N/8) times.  The tokens of a block (64 bytes of a row) are staged by
-// 16-byte asynchronous copies one block ahead; rows whose starts are not 16-byte aligned are
-// copied as the aligned pieces that hold them and read at their offset.
+// Layout.  A lane holds S states (4, from dstate 64 on 8) of CPL channels, N/S lanes a channel
+// group: the B and C of a step, fp32 in shared memory, then serve CPL channels per load, and the
+// sum over states crosses lanes only log2(N/S) times.  The tokens of a block (64 bytes of a row)
+// are staged by 16-byte asynchronous copies one block ahead; rows whose starts are not 16-byte
+// aligned are copied as the aligned pieces that hold them and read at their offset.  The warps of a
+// CTA meet twice per block, around the conversion of B and C.
+//
+// Measured on one B200, bf16, dstate 16: 16384 tokens in 24 ragged prompts x 4096 channels 525 us
+// in the mean of three draws (the longest of them 3305 to 3913 tokens, whose chain of blocks is most
+// of it; 453 us where the tokens lie more evenly), one prompt of 8191 tokens x 1536 channels 200 us
+// in 24 chunks.  MUFU 66 % busy while SMs have work, issue 57 %, 15 of 64 warps an SM.  Against it:
+// eight states of two channels per lane (half the warps, longer chains) 721 and 260 us; blocks of 32
+// bytes 636 and 226; eight warps a CTA 611 and 221; a quarter of the exponentials as polynomials on
+// the fp32 pipe 4 to 9 % more (the issue slots they need are as scarce); three CTAs an SM with more
+// registers 510 and 213; outputs stored without their pass through shared memory 3 % more.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -64,12 +74,12 @@ struct PackedCfg {
     static constexpr int V = 16 / ESZ;                  // elements per 16-byte piece
     static constexpr int RB = 64;                       // bytes of a row's block
     static constexpr int TB = RB / ESZ;                 // steps per block
-    static constexpr int S = N <= 32 ? 4 : 8;                   // states per lane
+    static constexpr int S = N <= 32 ? 4 : 8;           // states per lane
     static constexpr int TPC = N / S;                   // lanes per channel
     static constexpr int CPL = N == 128 ? 4 : 2;        // channels per lane
     static constexpr int LG = 32 / TPC;                 // lane groups of a warp
     static constexpr int CW = LG * CPL;                 // channels per warp
-    static constexpr int W = N == 8 ? 2 : 4;  // warps
+    static constexpr int W = N == 8 ? 2 : 4;            // warps
     static constexpr int CT = W * CW;                   // channels per tile
     static constexpr int NT = 32 * W;
     static constexpr int CTAS = N <= 32 ? 4 : 2;        // per SM, at least
@@ -400,8 +410,10 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
         }
         __syncthreads();   // bc is complete; the warp's own q rows too
 
-        // the recurrence
-        for (int w = lo / WT; w * WT < hi; ++w) {
+        // the recurrence (two windows at a time: the second one's loads pass under the first one's sums)
+        const int w_end = (hi + WT - 1) / WT;
+#pragma unroll 2
+        for (int w = lo / WT; w < w_end; ++w) {
             float yw[CPL * WT];
 #pragma unroll
             for (int tt = 0; tt < WT; ++tt) {

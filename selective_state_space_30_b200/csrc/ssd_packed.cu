@@ -20,8 +20,12 @@
 // in j's 32-step stretch, whole stretches between, and the steps of i's stretch; within one
 // stretch it is a difference of two sums of at most 32 terms.
 //
-// Bound: the phases between the products, which threads compute (M, X', the outputs), one CTA of
-// 16 warps per SM; the products of a block take about 1.2 of its microseconds.  Tiles arrive by
+// Bound: the phases between the products, which threads compute one after the other, one CTA of 16
+// warps per SM.  Of a block's 6.6 us about 1.2 go into M, 0.9 into the outputs, 0.6 into X', 0.7 into
+// addresses of copies and 2.3 into the products and the barriers around them (tensor pipe 11 % busy).
+// Measured on one B200: 6 prompts of 4096 tokens, 32 heads 115 us (the scan kernel 400), one of 8192
+// tokens, 16 heads 121 (441).  Values in f32x2 pairs with log2 dt folded into the exponent, and whole
+// words of x, z and the outputs in the epilogue, brought a block from 9.2 to 6.6 us.  Tiles arrive by
 // 16-byte asynchronous copies into the 128-byte swizzle that the tensor cores read, each as soon as
 // its place is free: X a block ahead in a second buffer, B once G and S are done, C once C H is.
 // Rows off the 16-byte grid are shifted into place through registers.

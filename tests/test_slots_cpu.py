@@ -122,9 +122,10 @@ def test_slots_copy_refusals(ssm):
 
 def test_conv_bwd_refusals(ssm):
     size = ssm.ssm_causal_conv1d_bwd_workspace_size
-    need = size(2, 8, 30, 4, ssm.SSM_BF16)
-    assert need >= 2 * 8 * 5 * 4 and size(2, 8, 0, 4, ssm.SSM_BF16) == 0
-    ok = dict(batch=2, dim=8, L=30, width=4, io=ssm.SSM_BF16, x=A16, w=A16, bias=None, silu=True, dout=A16, dx=2 * A16, dw=A16,
+    # a workspace where a channel's sums are split over CTAs: few channels and many rows
+    need = size(40, 8, 30, 4, ssm.SSM_BF16)
+    assert need >= 2 * 8 * 5 * 4 and size(40, 8, 0, 4, ssm.SSM_BF16) == 0 and size(8, 1536, 2048, 4, ssm.SSM_BF16) == 0
+    ok = dict(batch=40, dim=8, L=30, width=4, io=ssm.SSM_BF16, x=A16, w=A16, bias=None, silu=True, dout=A16, dx=2 * A16, dw=A16,
               db=None, ws=A16, nws=need)
 
     def rc(**kw):
