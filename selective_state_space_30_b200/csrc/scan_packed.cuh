@@ -82,7 +82,9 @@ struct PackedCfg {
     static constexpr int W = N == 8 ? 2 : 4;            // warps
     static constexpr int CT = W * CW;                   // channels per tile
     static constexpr int NT = 32 * W;
-    static constexpr int CTAS = N <= 32 ? 4 : 2;        // per SM, at least
+    // CTAs per SM, at least.  Uncut calls end with the longest sequences' CTAs, which more registers
+    // make faster; cut ones want as many chunks at a time as fit.
+    static constexpr int CTAS_UNCUT = N <= 32 ? 3 : 2, CTAS_CUT = N <= 32 ? 4 : 2;
     static constexpr int WT = CPL * 4 >= TPC ? 4 : 8;   // steps per window
     static constexpr int PA = RB / 16;                  // 16-byte pieces of a row's block
     static constexpr int PIECES = ALIGNED ? PA : PA + 1;    // that hold it
@@ -206,8 +208,8 @@ struct Task {
     bool has;                // starts from the slot's state
 };
 
-// One chunk.  LOCAL: only its decay and its end state from zero.
-template <typename T, int N, bool HEAD, bool ALIGNED, bool LOCAL>
+// One chunk (all of a sequence unless CUT).  LOCAL: only its decay and its end state from zero.
+template <typename T, int N, bool HEAD, bool ALIGNED, bool LOCAL, bool CUT>
 __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk, unsigned char* smem) {
     using Cf = PackedCfg<T, N, HEAD, ALIGNED>;
     constexpr int S = Cf::S, TPC = Cf::TPC, CPL = Cf::CPL, CW = Cf::CW, CT = Cf::CT, TB = Cf::TB, V = Cf::V;
@@ -315,7 +317,7 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
             for (int s = 0; s < S / 2; ++s) a2[c][s] = make_float2(__ldg(ar + 2 * s) * kLog2e, __ldg(ar + 2 * s + 1) * kLog2e);
         }
         // the state that enters the chunk
-        if (!LOCAL && tk.k > 0) {
+        if (CUT && !LOCAL && tk.k > 0) {
             // join the chunks before: the first holds a state, the later ones (decay, state from zero)
             const int64_t c0 = tk.chunk_id - tk.k;
             const float* hr = p.ws_h + (c0 * p.dim + d) * N + j * S;
@@ -535,7 +537,7 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
 #pragma unroll
                 for (int s = 0; s < S / 2; ++s) { hr[2 * s] = h[c][s].x; hr[2 * s + 1] = h[c][s].y; }
             }
-        } else if (LOCAL || tk.k == 0) {
+        } else if (CUT && (LOCAL || tk.k == 0)) {
             float* hr = p.ws_h + ((int64_t)tk.chunk_id * p.dim + d) * N + j * S;
 #pragma unroll
             for (int s = 0; s < S / 2; ++s) __stcg(reinterpret_cast<float2*>(hr) + s, h[c][s]);
@@ -672,8 +674,10 @@ __device__ __forceinline__ Run find_run(const PackedParams& p, int64_t x, int64_
     return tk.k > 0 ? kRunFull : kRunNone;
 }
 
-template <typename T, int N, bool HEAD, bool ALIGNED>
-__global__ void __launch_bounds__(PackedCfg<T, N, HEAD, ALIGNED>::NT, PackedCfg<T, N, HEAD, ALIGNED>::CTAS)
+// CUT: sequences may be cut into chunks.
+template <typename T, int N, bool HEAD, bool ALIGNED, bool CUT>
+__global__ void __launch_bounds__(PackedCfg<T, N, HEAD, ALIGNED>::NT, CUT ? PackedCfg<T, N, HEAD, ALIGNED>::CTAS_CUT
+                                                                          : PackedCfg<T, N, HEAD, ALIGNED>::CTAS_UNCUT)
 scan_packed_kernel(const PackedParams p) {
     using Cf = PackedCfg<T, N, HEAD, ALIGNED>;
     extern __shared__ __align__(16) unsigned char packed_smem[];
@@ -685,8 +689,9 @@ scan_packed_kernel(const PackedParams p) {
     tk.d0 = tk.g * (int)p.group_dim + tk.ci0;
     tk.nch = (int)p.group_dim - tk.ci0 < Cf::CT ? (int)p.group_dim - tk.ci0 : Cf::CT;
     const Run run = find_run<T>(p, blockIdx.x / p.n_tiles, reinterpret_cast<int64_t*>(smem), Cf::NT, tk);
-    if (run == kRunFull) run_chunk<T, N, HEAD, ALIGNED, false>(p, tk, smem);
-    else if (run == kRunLocal) run_chunk<T, N, HEAD, ALIGNED, true>(p, tk, smem);
+    if (run == kRunFull) run_chunk<T, N, HEAD, ALIGNED, false, CUT>(p, tk, smem);
+    if constexpr (CUT)
+        if (run == kRunLocal) run_chunk<T, N, HEAD, ALIGNED, true, true>(p, tk, smem);
 }
 
 template <typename T, int N, bool HEAD, bool ALIGNED>
@@ -697,7 +702,7 @@ int launch(PackedParams& p, cudaStream_t s) {
     const int64_t ctas = tiles * (p.chunk > 0 ? p.n_chunks : p.n_seq);
     if (tiles > 0x7FFFFFFF || ctas > 0x7FFFFFFF) return SSM_ERR_UNSUPPORTED;
     p.n_tiles = (unsigned)tiles;
-    auto* k = scan_packed_kernel<T, N, HEAD, ALIGNED>;
+    auto* k = p.chunk > 0 ? scan_packed_kernel<T, N, HEAD, ALIGNED, true> : scan_packed_kernel<T, N, HEAD, ALIGNED, false>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM) != cudaSuccess) return SSM_ERR_CUDA;
     for (p.phase = 1; p.phase <= (p.chunk > 0 ? 2 : 1); ++p.phase) {
         k<<<(unsigned)ctas, Cf::NT, Cf::SMEM, s>>>(p);
