@@ -67,7 +67,7 @@ struct PackedParams {
     int grid16;              // every row starts on the 16-byte grid
 };
 
-template <typename T, int N, bool HEAD, bool ALIGNED>
+template <typename T, int N, bool HEAD, bool ALIGNED, bool CUT = true>
 struct PackedCfg {
     static constexpr bool kAligned = ALIGNED;
     static constexpr int ESZ = sizeof(T);
@@ -84,7 +84,7 @@ struct PackedCfg {
     static constexpr int NT = 32 * W;
     // CTAs per SM, at least.  Uncut calls end with the longest sequences' CTAs, which more registers
     // make faster; cut ones want as many chunks at a time as fit.
-    static constexpr int CTAS_UNCUT = N <= 32 ? 3 : 2, CTAS_CUT = N <= 32 ? 4 : 2;
+    static constexpr int CTAS = N > 32 ? 2 : CUT ? 4 : 3;
     static constexpr int WT = CPL * 4 >= TPC ? 4 : 8;   // steps per window
     static constexpr int PA = RB / 16;                  // 16-byte pieces of a row's block
     static constexpr int PIECES = ALIGNED ? PA : PA + 1;    // that hold it
@@ -101,7 +101,18 @@ struct PackedCfg {
     static constexpr int ITEMS = CW * TB / PS / 32;     // per lane
     static constexpr int OFF_BC = 2 * STAGE;            // fp32 [step][B of all states | C of all states]
     static constexpr int OFF_Q = OFF_BC + TB * 2 * N * 4;   // per warp: [step][channel] (dt or decay, dt u), then y
-    static constexpr int Q_WARP = TB * CW * 8;
+    // Uncut calls have the shared memory for a row of partial sums of y per lane and step, which the
+    // epilogue adds; the others add them by shuffles, into q's place.  The rows run over q, which
+    // ends where they end and whose steps are no longer: a step's row covers no later step of q.
+    static constexpr bool YROWS = !CUT && N <= 32;
+    static constexpr int Q_BYTES = TB * CW * 8;
+    static constexpr int Q_WARP = YROWS ? TB * 32 * CPL * 4 : Q_BYTES;
+    static_assert(!YROWS || (CPL == 2 && Q_WARP >= Q_BYTES), "q ends where the rows end");
+    // where lane (lg, j) puts its sum for channel ch of step t (floats): a step's sums of a channel lie
+    // side by side, and those of eight neighbouring channels in different banks
+    __device__ static constexpr int y_off(int t, int lg, int ch, int j) {
+        return t * 32 * CPL + ch * 32 + (lg ^ (ch * (LG / 2))) * TPC + j;
+    }
     static constexpr int OFF_PAR = OFF_Q + W * Q_WARP;  // bias, D, and the head's A (log2 e folded in), per channel
     static constexpr int OFF_MISC = OFF_PAR + 3 * CT * 4;
     static constexpr int SMEM = OFF_MISC + 64;
@@ -211,7 +222,7 @@ struct Task {
 // One chunk (all of a sequence unless CUT).  LOCAL: only its decay and its end state from zero.
 template <typename T, int N, bool HEAD, bool ALIGNED, bool LOCAL, bool CUT>
 __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk, unsigned char* smem) {
-    using Cf = PackedCfg<T, N, HEAD, ALIGNED>;
+    using Cf = PackedCfg<T, N, HEAD, ALIGNED, CUT>;
     constexpr int S = Cf::S, TPC = Cf::TPC, CPL = Cf::CPL, CW = Cf::CW, CT = Cf::CT, TB = Cf::TB, V = Cf::V;
     constexpr int ESZ = Cf::ESZ, NT = Cf::NT, WT = Cf::WT, PS = Cf::PS;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -221,7 +232,8 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
     const int h_lo = HEAD ? tk.d0 / head_dim : tk.d0;                 // first delta row of the tile
     const int n_dt = HEAD ? (tk.d0 + tk.nch - 1) / head_dim - h_lo + 1 : tk.nch;
     float* bc = reinterpret_cast<float*>(smem + Cf::OFF_BC);
-    float2* q = reinterpret_cast<float2*>(smem + Cf::OFF_Q + warp * Cf::Q_WARP);
+    float* yrows = reinterpret_cast<float*>(smem + Cf::OFF_Q + warp * Cf::Q_WARP);
+    float2* q = reinterpret_cast<float2*>(smem + Cf::OFF_Q + (warp + 1) * Cf::Q_WARP - Cf::Q_BYTES);
     float* s_bias = reinterpret_cast<float*>(smem + Cf::OFF_PAR);
     float* s_D = s_bias + CT;
     float* s_a = s_D + CT;
@@ -464,7 +476,14 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
                     }
                 }
             }
-            if constexpr (!LOCAL) {
+            if constexpr (!LOCAL && Cf::YROWS) {
+                __syncwarp();                           // every lane has read the window's q
+#pragma unroll
+                for (int tt = 0; tt < WT; ++tt)
+#pragma unroll
+                    for (int c = 0; c < CPL; ++c) yrows[Cf::y_off(w * WT + tt, lg, c, j)] = yw[c * WT + tt];
+            }
+            if constexpr (!LOCAL && !Cf::YROWS) {
                 // sum over the lanes of a channel; y takes the place of dt in q, which every lane
                 // of the channel has read before the shuffles
                 int off = 0;
@@ -492,10 +511,29 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
                 read_row<Cf, PS>(sb, Cf::R_U + lc, (ALIGNED ? 0 : skew<T>(ub + ro)) + e0, uv);
                 if (zb) read_row<Cf, PS>(sb, Cf::R_Z + lc, (ALIGNED ? 0 : skew<T>(zb + ro)) + e0, zv);
                 const float2 D2 = dup2(s_D[lc]);
+                auto y_of = [&](int t) {
+                    if constexpr (Cf::YROWS) {
+                        // the lanes' sums, in the order of the shuffles
+                        const float* r = yrows + Cf::y_off(t, c / CPL, c % CPL, 0);
+                        float part[TPC];
+#pragma unroll
+                        for (int k = 0; k < TPC; k += 2) {
+                            const float2 f = *reinterpret_cast<const float2*>(r + k);
+                            part[k] = f.x;
+                            part[k + 1] = f.y;
+                        }
+#pragma unroll
+                        for (int m = TPC / 2; m >= 1; m >>= 1)
+#pragma unroll
+                            for (int k = 0; k < m; ++k) part[k] += part[k + m];
+                        return part[0];
+                    } else {
+                        return q[t * CW + c].x;
+                    }
+                };
 #pragma unroll
                 for (int e = 0; e < PS; e += 2) {
-                    float2 y = fma2(D2, make_float2(uv[e], uv[e + 1]),
-                                    make_float2(q[(e0 + e) * CW + c].x, q[(e0 + e + 1) * CW + c].x));
+                    float2 y = fma2(D2, make_float2(uv[e], uv[e + 1]), make_float2(y_of(e0 + e), y_of(e0 + e + 1)));
                     if (zb) y = mul2(y, ssm::silu2(make_float2(zv[e], zv[e + 1])));
                     o[e] = y.x;
                     o[e + 1] = y.y;
@@ -676,10 +714,9 @@ __device__ __forceinline__ Run find_run(const PackedParams& p, int64_t x, int64_
 
 // CUT: sequences may be cut into chunks.
 template <typename T, int N, bool HEAD, bool ALIGNED, bool CUT>
-__global__ void __launch_bounds__(PackedCfg<T, N, HEAD, ALIGNED>::NT, CUT ? PackedCfg<T, N, HEAD, ALIGNED>::CTAS_CUT
-                                                                          : PackedCfg<T, N, HEAD, ALIGNED>::CTAS_UNCUT)
+__global__ void __launch_bounds__(PackedCfg<T, N, HEAD, ALIGNED, CUT>::NT, PackedCfg<T, N, HEAD, ALIGNED, CUT>::CTAS)
 scan_packed_kernel(const PackedParams p) {
-    using Cf = PackedCfg<T, N, HEAD, ALIGNED>;
+    using Cf = PackedCfg<T, N, HEAD, ALIGNED, CUT>;
     extern __shared__ __align__(16) unsigned char packed_smem[];
     unsigned char* smem = packed_smem;
     const unsigned tile = blockIdx.x % p.n_tiles;
@@ -694,21 +731,26 @@ scan_packed_kernel(const PackedParams p) {
         if (run == kRunLocal) run_chunk<T, N, HEAD, ALIGNED, true, true>(p, tk, smem);
 }
 
-template <typename T, int N, bool HEAD, bool ALIGNED>
+template <typename T, int N, bool HEAD, bool ALIGNED, bool CUT>
 int launch(PackedParams& p, cudaStream_t s) {
-    using Cf = PackedCfg<T, N, HEAD, ALIGNED>;
+    using Cf = PackedCfg<T, N, HEAD, ALIGNED, CUT>;
     p.tiles_per_group = (unsigned)((p.group_dim + Cf::CT - 1) / Cf::CT);
     const int64_t tiles = p.ngroups * p.tiles_per_group;
-    const int64_t ctas = tiles * (p.chunk > 0 ? p.n_chunks : p.n_seq);
+    const int64_t ctas = tiles * (CUT ? p.n_chunks : p.n_seq);
     if (tiles > 0x7FFFFFFF || ctas > 0x7FFFFFFF) return SSM_ERR_UNSUPPORTED;
     p.n_tiles = (unsigned)tiles;
-    auto* k = p.chunk > 0 ? scan_packed_kernel<T, N, HEAD, ALIGNED, true> : scan_packed_kernel<T, N, HEAD, ALIGNED, false>;
+    auto* k = scan_packed_kernel<T, N, HEAD, ALIGNED, CUT>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM) != cudaSuccess) return SSM_ERR_CUDA;
-    for (p.phase = 1; p.phase <= (p.chunk > 0 ? 2 : 1); ++p.phase) {
+    for (p.phase = 1; p.phase <= (CUT ? 2 : 1); ++p.phase) {
         k<<<(unsigned)ctas, Cf::NT, Cf::SMEM, s>>>(p);
         if (cudaGetLastError() != cudaSuccess) return SSM_ERR_CUDA;
     }
     return SSM_OK;
+}
+
+template <typename T, int N, bool HEAD, bool ALIGNED>
+int launch(PackedParams& p, cudaStream_t s) {
+    return p.chunk > 0 ? launch<T, N, HEAD, ALIGNED, true>(p, s) : launch<T, N, HEAD, ALIGNED, false>(p, s);
 }
 
 // One (dtype, dstate), in a translation unit of its own.
