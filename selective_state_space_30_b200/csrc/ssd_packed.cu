@@ -65,12 +65,15 @@ constexpr int OFF_DEC = 208 * 1024;            // two blocks' Decay
 constexpr int OFF_BAR = OFF_DEC + 2 * 4096;
 constexpr int kSmem = OFF_BAR + 256 + 1024;    // and room to align the base
 
-// A block's decay, in log2 units: over the 32-step stretches of its 128 steps
+// A block's decay, in log2 units: over the 32-step stretches of its 128 steps.  dt_j is a factor of
+// j's weights: as its logarithm, one sum less per element of M, where softplus makes it positive,
+// and by itself (`dt`) where it may have any sign.
 struct Decay {
     float head[kQ];       // from the stretch's start through the step
     float near[kQ];       // log2 dt_j less that: with head_i, the weight of j for i of the same stretch
     float far[kQ];        // log2 dt_j and the steps from behind j to the stretch's end: for later stretches
     float w[kQ];          // 2^s(end, j) dt_j
+    float dt[kQ];
     float stretch[4];     // whole stretches
 };
 static_assert(sizeof(Decay) <= 4096, "fits its place");
@@ -174,6 +177,7 @@ __device__ __forceinline__ void store_out(const unsigned char* tile, unsigned sh
 }
 
 // A block's decay, by one warp: four steps per lane, so eight lanes hold a stretch.
+template <bool SOFTPLUS>
 __device__ __forceinline__ void block_decay(const PackedParams& p, const unsigned short* delta, const Block& k, float Ah,
                                             float bias, int lane, Decay& o) {
     float dt[4], pre[4], run = 0.f;
@@ -183,7 +187,7 @@ __device__ __forceinline__ void block_decay(const PackedParams& p, const unsigne
         dt[e] = 0.f;
         if (t >= k.t0 && t < k.t1) {
             const float x = __uint_as_float((uint32_t)__ldg(delta + t) << 16) + bias;
-            dt[e] = p.softplus ? softplus1(x) : x;
+            dt[e] = SOFTPLUS ? softplus1(x) : x;
         }
         run += dt[e] * Ah;
         pre[e] = run;
@@ -210,11 +214,12 @@ __device__ __forceinline__ void block_decay(const PackedParams& p, const unsigne
 #pragma unroll
     for (int e = 3; e >= 0; --e) {
         const int j = 4 * lane + e;
-        const float l = __log2f(dt[e]);                  // -inf where dt = 0: a weight of zero
+        const float l = SOFTPLUS ? __log2f(dt[e]) : 0.f;     // -inf where dt = 0: a weight of zero
         o.head[j] = up + pre[e];
         o.near[j] = l - (up + pre[e]);
         o.far[j] = l + (suf + down);
         o.w[j] = ex2_approx((suf + down) + later) * dt[e];
+        if (!SOFTPLUS) o.dt[j] = dt[e];
         suf += dt[e] * Ah;
     }
     if ((lane & 7) == 0) o.stretch[lane >> 3] = whole;
@@ -224,7 +229,7 @@ template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.as
 
 // Thread: TMEM lane and tile row `row`, and a quarter of that row's columns (32 of the 128 steps,
 // 16 of the 64 channels).  LOCAL: only the end state from zero and the product of the decays.
-template <bool LOCAL>
+template <bool LOCAL, bool SOFTPLUS>
 __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, unsigned char* smem) {
     uint64_t* mb_s = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
     uint64_t* mb_y = mb_s + 1;
@@ -277,7 +282,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
     stage_b(0);
     stage_c(0);
     stage_z(0);
-    if (warp == 1 && nblk > 0) block_decay(p, delta, block(0), Ah, bias, lane, dec[0]);
+    if (warp == 1 && nblk > 0) block_decay<SOFTPLUS>(p, delta, block(0), Ah, bias, lane, dec[0]);
 
     // the state: n = row, channels p0 .. p0 + 15
     float H[16], Dv[LOCAL ? 1 : 8];                     // the skip weights of the channels it writes
@@ -374,7 +379,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
             last_bar = mb_s;
             last_ph = ph;
         }
-        if (warp == 1 && c + 1 < nblk) block_decay(p, delta, block(c + 1), Ah, bias, lane, dec[(c + 1) & 1]);
+        if (warp == 1 && c + 1 < nblk) block_decay<SOFTPLUS>(p, delta, block(c + 1), Ah, bias, lane, dec[(c + 1) & 1]);
         bool ok = mbar_wait(mb_s, ph, kWaitNs, status);
         tc::fence_after();
         // (a wait that ran out is voted on before anything overwrites what the products may still read)
@@ -410,6 +415,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
                     for (int q = 0; q < 4; ++q) {
                         v[q] = pmul(pk(__uint_as_float(gv[k + 2 * q]), __uint_as_float(gv[k + 2 * q + 1])),
                                     pex2(padd(ci2, c2[q])));
+                        if constexpr (!SOFTPLUS) v[q] = pmul(v[q], *reinterpret_cast<const pair_t*>(dc.dt + j0 + k + 2 * q));
                         if (same) {                     // of the stretch's own steps, those up to the row's
                             const float2 f = halves(v[q]);
                             const int j = k + 2 * q;
@@ -540,6 +546,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
     if (warp == 0) tc::dealloc(tbase, kTmemCols);
 }
 
+template <bool SOFTPLUS>
 __global__ void __launch_bounds__(kThreads, 1) ssd_packed_kernel(const PackedParams p) {
     extern __shared__ __align__(1024) unsigned char ssd_smem[];
     unsigned char* smem = ssd_smem + ((1024u - (smem_u32(ssd_smem) & 1023u)) & 1023u);
@@ -550,8 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_packed_kernel(const PackedPar
     tk.ci0 = tk.d0 - tk.g * (int)p.group_dim;
     tk.nch = kP;
     const Run run = find_run<bf16>(p, blockIdx.x / p.n_tiles, reinterpret_cast<int64_t*>(smem), kThreads, tk);
-    if (run == kRunFull) run_head<false>(p, tk, smem);
-    else if (run == kRunLocal) run_head<true>(p, tk, smem);
+    if (run == kRunFull) run_head<false, SOFTPLUS>(p, tk, smem);
+    else if (run == kRunLocal) run_head<true, SOFTPLUS>(p, tk, smem);
 }
 
 }  // namespace
@@ -564,10 +571,11 @@ int ssd_packed_launch(PackedParams& p, cudaStream_t s) {
     const int64_t ctas = p.nheads * (p.chunk > 0 ? p.n_chunks : p.n_seq);
     if (ctas > 0x7FFFFFFF) return SSM_ERR_UNSUPPORTED;
     p.n_tiles = (unsigned)p.nheads;
-    if (cudaFuncSetAttribute(ssd_packed_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+    auto* kernel = p.softplus ? ssd_packed_kernel<true> : ssd_packed_kernel<false>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
         return SSM_ERR_CUDA;
     for (p.phase = 1; p.phase <= (p.chunk > 0 ? 2 : 1); ++p.phase) {
-        ssd_packed_kernel<<<(unsigned)ctas, kThreads, kSmem, s>>>(p);
+        kernel<<<(unsigned)ctas, kThreads, kSmem, s>>>(p);
         if (cudaGetLastError() != cudaSuccess) return SSM_ERR_CUDA;
     }
     return SSM_OK;

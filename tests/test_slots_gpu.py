@@ -303,6 +303,23 @@ def test_scan_packed_cut_sequences(ssm, case):
     assert torch.equal(again, states) and torch.equal(out2, out)
 
 
+@pytest.mark.parametrize("dim,heads,N,head", [(32, 32, 16, 0), (64, 1, 128, 0), (128, 2, 128, 5)])
+def test_scan_packed_steps_of_either_sign(ssm, dim, heads, N, head):
+    """Without softplus a step is what delta and the bias add up to: negative ones let the state grow."""
+    gen = torch.Generator().manual_seed(27)
+    lens = [150, 40, 302]
+    cu, total, bounds = packing(lens, head)
+    p = _scan_inputs(gen, total, dim, heads, 1, N, "bf16", softplus=False)
+    p["delta"] = rnd(gen, heads, total, dtype="bf16", scale=0.02)
+    p["delta_bias"] = rnd(gen, heads, scale=0.005)
+    states, out = rnd(gen, 3, dim, N), rnd(gen, dim, total, dtype="bf16")
+    ref, err, ref_pool, pool_err = sp.scan_packed(_plain(p), bounds, [0, 1, 2], [1, 0, 1], f64(states), f64(out),
+                                                  tensor=_tensor(dim, heads, N, "bf16", total, 3))
+    got = _call(ssm, p, i32(cu), states, out, has_state=torch.tensor([1, 0, 1], dtype=torch.uint8).cuda(), max_seqlen=302)
+    sp.check(f64(got), ref, err, "bf16", "out")
+    sp.check(f64(states), ref_pool, pool_err, "f32", "states")
+
+
 def test_scan_packed_hint_is_only_a_hint(ssm):
     """A max_seqlen that is too small, zero or too large: right results all the same."""
     gen = torch.Generator().manual_seed(23)
@@ -670,6 +687,21 @@ def test_bounds_out_of_order_stay_inside(ssm):
         ssm.causal_conv1d_packed(p["u"], w, i32(cu), conv_pool, out=guard[1])
         torch.cuda.synchronize()
         assert (guard[0] == 7).all() and (guard[2] == 7).all()
+
+
+def test_overlapping_outputs_are_refused(ssm):
+    gen = torch.Generator().manual_seed(5)
+    x, w, pool, cu = rnd(gen, 8, 40), rnd(gen, 8, 4), rnd(gen, 2, 8, 3), i32([0, 15, 40])
+    buf = torch.zeros(8 * 40 + 40, device="cuda")
+    for out in (x, buf[40:].view(8, 40)):
+        with pytest.raises(ValueError, match="out must not overlap x"):
+            ssm.causal_conv1d_packed(x if out is x else buf[:320].view(8, 40), w, cu, pool, out=out)
+    ssm.causal_conv1d_packed(buf[:160].view(4, 40), w[:4], cu, pool[:, :4].contiguous(), out=buf[160:320].view(4, 40))
+    p = _scan_inputs(gen, 40, 8, 8, 1, 8, "f32")
+    states = rnd(gen, 2, 8, 8)
+    for k in ("u", "delta", "z", "B", "C"):
+        with pytest.raises(ValueError, match=f"out must not overlap {k}"):
+            _call(ssm, p, cu, states, p[k].view(8, 40))
 
 
 def test_front_end_refusals(ssm):
