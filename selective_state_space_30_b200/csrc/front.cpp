@@ -146,6 +146,13 @@ void need_workspace(const Arg& ws, int device) {
     if (ws && (!ws->is_cuda() || ws->get_device() != device || !ws->is_contiguous()))
         refuse("%s must be contiguous and on the device of the other tensors%s", ws.name);
 }
+// Two contiguous tensors, or one and nothing, that share no byte.
+void need_apart(const Arg& out, const Arg& in) {
+    if (!out || !in) return;
+    const char *a = static_cast<const char*>(out.ptr()), *b = static_cast<const char*>(in.ptr());
+    if (a < b + in->numel() * in->element_size() && b < a + out->numel() * out->element_size())
+        refuse("%s must not overlap %s", out.name, in.name);
+}
 size_t bytes_of(const Tensor& t) { return (size_t)t.numel() * t.element_size(); }
 
 // The device's current stream, with the device current for as long as this lives.
@@ -229,6 +236,7 @@ PyObject* conv_packed(PyObject* const* v) {
     need(out, x->scalar_type(), x->sizes(), dev);
     const int64_t stride = pool_stride(states, x->scalar_type(), dim, width - 1, dev);
     need_indices(n, dev, cu, slots, has);
+    need_apart(out, x);
     const Launch on(dev);
     Tensor o = out_or(out, *x, true);
     check(entry.conv_packed(dim, total, n, (int32_t)width, io, x.ptr(), f32(w), f32(bias), silu, i32(cu), i32(slots), u8(has),
@@ -281,6 +289,7 @@ PyObject* scan_packed(PyObject* const* v) {
     const int64_t stride = pool_stride(states, at::kFloat, dim, N, dev);
     need_indices(n, dev, cu, slots, has);
     need_workspace(ws, dev);
+    for (const Arg* in : {&u, &delta, &B, &C, &z}) need_apart(out, *in);
     const ssm_dims_t d = {n, dim, total, N, heads, groups, io, 0};
     const Launch on(dev);
     size_t bytes = 0;

@@ -590,7 +590,7 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
 // sequences have ceil(length / chunk) items each, at least one, and keep their own order, which
 // their chunks' places in the workspace follow.
 __device__ __forceinline__ bool find_item(const PackedParams& p, int64_t x, int64_t* sh, int nt, int64_t& seq, int64_t& k) {
-    // sh: [0] sequence, [1] item of it, [2 ..] warp sums, [8 ..] counts of the buckets
+    // sh: [0] sequence, [1] item of it, [2 ..] warp sums, [34 ..] counts of the buckets
     constexpr int kBuckets = 64;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt / 32;
     const bool cut = p.chunk > 0;
@@ -634,7 +634,7 @@ __device__ __forceinline__ bool find_item(const PackedParams& p, int64_t x, int6
         return kBuckets - 2 - 2 * e - half;             // the longest come first
     };
     int want = 0;
-    if (!cut && p.n_seq > 1) {
+    if (!cut) {
         for (int i = tid; i < kBuckets; i += nt) count[i] = 0u;
         __syncthreads();
         for (int64_t i = tid; i < p.n_seq; i += nt) {
@@ -652,7 +652,7 @@ __device__ __forceinline__ bool find_item(const PackedParams& p, int64_t x, int6
         if (i < p.n_seq) {
             const TokenRange r = token_range(p.cu, i, p.total);
             const int64_t len = r.hi - r.lo;
-            n = cut ? (len > 0 ? (len + p.chunk - 1) / p.chunk : 1) : p.n_seq == 1 || bucket(len) == want;
+            n = cut ? (len > 0 ? (len + p.chunk - 1) / p.chunk : 1) : bucket(len) == want;
         }
         int64_t inc = n;
 #pragma unroll

@@ -23,8 +23,8 @@ constexpr int kThreads = 256;
 // Bytes a CTA stages at most where its pairs' 16-byte pieces fit in as many: with 32 KB seven CTAs
 // fit an SM, whose reads and writes overlap
 constexpr int kStage = 32 * 1024;
-constexpr int kStageMost = 192 * 1024;
 constexpr int kMaxPairs = 4096;
+constexpr int kStageMost = 32 * kMaxPairs;   // the shortest slice, and 16 bytes more where it is off the grid
 constexpr int kMaxSlice = 4096;
 
 struct CopyParams {
@@ -156,7 +156,7 @@ extern "C" int ssm_state_slots_copy(void* pool, int64_t n_layers, int64_t n_slot
     const int extra = vec ? 0 : 16;
     int slice = kMaxSlice;
     while (slice > 16 && (slice + extra) * n_pairs > kStage) slice /= 2;
-    if ((slice + extra) * n_pairs > kStageMost) return SSM_ERR_UNSUPPORTED;
+    static_assert((16 + 16) * kMaxPairs <= kStageMost && kStageMost <= 227 * 1024, "the shortest slices fit");
     while (slice > 512 && n_layers * ((slot_bytes + slice - 1) / slice) < 148 * 4) slice /= 2;
     p.slice = slice;
     p.slices = (slot_bytes + slice - 1) / slice;
