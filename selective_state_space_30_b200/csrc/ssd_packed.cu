@@ -50,18 +50,19 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kQ = 128, kP = 64, kN = 128;
 constexpr int kThreads = 512;
+constexpr int kDecayWarp = 12;                 // steps 96 .. 127 of rows 0 .. 31: nothing of M
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColG = 0, kColY = 128, kColCH = 192, kColS = 256;
+constexpr uint32_t kColG = 0, kColY = 128, kColCH = 192, kColS = 256, kColM = 320;   // M: two terms of 64 columns
 constexpr uint64_t kWaitNs = 500000000ull;
 
 // shared memory (bytes from a 1024-aligned base); a tile is two 64-step halves of rows of 128 bytes
 constexpr int OFF_C = 0;                       // 128 states
 constexpr int OFF_B = 32 * 1024;
 constexpr int OFF_X = 64 * 1024;               // two buffers of 64 channels
-constexpr int OFF_M = 96 * 1024;               // X' (three terms), then M (two terms of 32 KB)
-constexpr int OFF_H = 160 * 1024;              // two terms of 128 x 64
-constexpr int OFF_Z = 192 * 1024;              // z, then the outputs
-constexpr int OFF_DEC = 208 * 1024;            // two blocks' Decay
+constexpr int OFF_XW = 96 * 1024;              // X', three terms
+constexpr int OFF_H = 144 * 1024;              // two terms of 128 x 64
+constexpr int OFF_Z = 176 * 1024;              // z, then the outputs
+constexpr int OFF_DEC = 192 * 1024;            // two blocks' Decay
 constexpr int OFF_BAR = OFF_DEC + 2 * 4096;
 constexpr int kSmem = OFF_BAR + 256 + 1024;    // and room to align the base
 
@@ -78,11 +79,9 @@ struct Decay {
 };
 static_assert(sizeof(Decay) <= 4096, "fits its place");
 
-// Four pairs of values (columns c0 .. c0 + 7 of row r) as sums of K bf16 terms, into K tiles `step`
-// bytes apart.
-template <int K>
-__device__ __forceinline__ void store_split8(unsigned char* tile, int step, uint32_t r, uint32_t c0, pair_t (&v)[4]) {
-    const uint32_t off = tc::sw128_off(r, c0);
+// Four pairs of values as sums of K bf16 terms: `put(k, words)` takes term k's.
+template <int K, class Put>
+__device__ __forceinline__ void split8(pair_t (&v)[4], const Put& put) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         uint32_t w[4];
@@ -93,8 +92,16 @@ __device__ __forceinline__ void store_split8(unsigned char* tile, int step, uint
             w[q] = *reinterpret_cast<const uint32_t*>(&t);
             if (k + 1 < K) v[q] = pfma(pk(__uint_as_float(w[q] << 16), __uint_as_float(w[q] & 0xFFFF0000u)), pk(-1.f), v[q]);
         }
-        *reinterpret_cast<uint4*>(tile + k * step + off) = make_uint4(w[0], w[1], w[2], w[3]);
+        put(k, w);
     }
+}
+// Into K tiles `step` bytes apart, columns c0 .. c0 + 7 of row r.
+template <int K>
+__device__ __forceinline__ void store_split8(unsigned char* tile, int step, uint32_t r, uint32_t c0, pair_t (&v)[4]) {
+    unsigned char* to = tile + tc::sw128_off(r, c0);
+    split8<K>(v, [&](int k, const uint32_t (&w)[4]) {
+        *reinterpret_cast<uint4*>(to + k * step) = make_uint4(w[0], w[1], w[2], w[3]);
+    });
 }
 
 struct Block {
@@ -231,13 +238,13 @@ template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.as
 // 16 of the 64 channels).  LOCAL: only the end state from zero and the product of the decays.
 template <bool LOCAL, bool SOFTPLUS>
 __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, unsigned char* smem) {
-    uint64_t* mb_s = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
-    uint64_t* mb_y = mb_s + 1;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(mb_s + 2);
-    int* status = reinterpret_cast<int*>(mb_s + 3);
+    uint64_t* mb_g = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+    uint64_t *mb_s = mb_g + 1, *mb_y = mb_g + 2;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(mb_g + 3);
+    int* status = reinterpret_cast<int*>(mb_g + 4);
     Decay* dec = reinterpret_cast<Decay*>(smem + OFF_DEC);
     static_assert(OFF_DEC % 16 == 0, "vector reads of the decay");
-    unsigned char *sC = smem + OFF_C, *sB = smem + OFF_B, *sM = smem + OFF_M, *sH = smem + OFF_H, *sZ = smem + OFF_Z;
+    unsigned char *sC = smem + OFF_C, *sB = smem + OFF_B, *sXw = smem + OFF_XW, *sH = smem + OFF_H, *sZ = smem + OFF_Z;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int quarter = warp & 3, part = warp >> 2;
@@ -271,18 +278,17 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
 
     __syncthreads();
     if (tid == 0) {
+        mbar_init(mb_g, 1);
         mbar_init(mb_s, 1);
         mbar_init(mb_y, 1);
         *status = SSM_OK;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) tc::alloc(tslot, kTmemCols);
-    // the order of these groups is the order of the waits below
     stage_x(0);
     stage_b(0);
     stage_c(0);
-    stage_z(0);
-    if (warp == 1 && nblk > 0) block_decay<SOFTPLUS>(p, delta, block(0), Ah, bias, lane, dec[0]);
+    if (warp == kDecayWarp && nblk > 0) block_decay<SOFTPLUS>(p, delta, block(0), Ah, bias, lane, dec[0]);
 
     // the state: n = row, channels p0 .. p0 + 15
     float H[16], Dv[LOCAL ? 1 : 8];                     // the skip weights of the channels it writes
@@ -317,26 +323,47 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
         }
     };
     if (start_state) store_state();
+    cp_wait<0>();
     tc::fence_async_smem();
     tc::fence_before();
-    __syncthreads();
+    __syncthreads();                                    // X, B, C, the decay and the state are staged
     tc::fence_after();
     const uint32_t tbase = *tslot, trow = tbase + ((uint32_t)(32 * quarter) << 16);
 
-    float total = 0.f;                                  // LOCAL: the sum of a over the task
-    int done = 0;                                       // blocks whose outputs are written
     uint64_t* last_bar = nullptr;                       // thread 0: its latest commit
     unsigned last_ph = 0;
+    auto commit = [&](uint64_t* bar, unsigned ph) {
+        tc::commit(bar);
+        last_bar = bar;
+        last_ph = ph;
+    };
+    auto issue_g = [&](unsigned ph) {
+        constexpr uint32_t id = tc::idesc_bf16(128, 128, true, true);
+#pragma unroll
+        for (int kk = 0; kk < kN / 16; ++kk)
+            tc::mma_bf16(tbase + kColG, tc::desc(sC + kk * 2048, 16384, 1024, tc::kSwizzle128),
+                         tc::desc(sB + kk * 2048, 16384, 1024, tc::kSwizzle128), id, kk > 0 ? 1u : 0u);
+        commit(mb_g, ph);
+    };
+    if constexpr (!LOCAL) {
+        if (tid == 0 && nblk > 0) issue_g(0u);
+        if (part > quarter) {                           // M's steps behind all of the warp's rows stay zero
+            const uint32_t none[16] = {};
+            tc::st16(trow + kColM + j0 / 2, none);
+            tc::st16(trow + kColM + 64 + j0 / 2, none);
+            tc::wait_st();
+        }
+    }
+    stage_x(1);
+
+    float total = 0.f;                                  // LOCAL: the sum of a over the task
+    int done = 0;                                       // blocks whose outputs are written
     for (int c = 0; c < nblk; ++c) {
         const unsigned ph = (unsigned)c & 1u;
         const Decay& dc = dec[c & 1];
         const unsigned char* sX = smem + OFF_X + (c & 1) * 16384;
         const bool with_state = c > 0 || start_state;
-        // copies in flight, the oldest first: X, B, C, z of this block, X of the next
-        stage_x(c + 1);
-        cp_wait<4>();
-        __syncthreads();                                // X is staged, and this block's decay
-        // ---- X', in three terms: two 8-step pieces of a channel per thread
+        // ---- X', in three terms: two 8-step pieces of a channel per thread (G runs)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const uint32_t e = (uint32_t)tid + (uint32_t)r * kThreads, pp = e >> 4, s8 = (e & 15u) * 8u;
@@ -350,52 +377,45 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 v[k] = pmul(pk(__uint_as_float(w4[k] << 16), __uint_as_float(w4[k] & 0xFFFF0000u)), w2[k]);
-            store_split8<3>(sM + half, 16384, pp, s8 & 63u, v);
+            store_split8<3>(sXw + half, 16384, pp, s8 & 63u, v);
         }
-        cp_wait<2>();                                   // B and C
         tc::fence_async_smem();
         tc::fence_before();
         __syncthreads();
         if (tid == 0) {
             tc::fence_after();
-            if constexpr (!LOCAL) {
-                constexpr uint32_t id = tc::idesc_bf16(128, 128, true, true);
-#pragma unroll
-                for (int kk = 0; kk < kN / 16; ++kk)
-                    tc::mma_bf16(tbase + kColG, tc::desc(sC + kk * 2048, 16384, 1024, tc::kSwizzle128),
-                                 tc::desc(sB + kk * 2048, 16384, 1024, tc::kSwizzle128), id, kk > 0 ? 1u : 0u);
-            }
-            constexpr uint32_t ids = tc::idesc_bf16(128, kP, false, false);
+            constexpr uint32_t ids = tc::idesc_bf16(128, kP, false, false), idh = tc::idesc_bf16(128, kP, true, true);
 #pragma unroll
             for (int kk = 0; kk < kQ / 16; ++kk) {
                 const uint64_t ab = tc::desc(sB + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024, tc::kSwizzle128);
 #pragma unroll
                 for (int s = 0; s < 3; ++s)
                     tc::mma_bf16(tbase + kColS, ab,
-                                 tc::desc(sM + s * 16384 + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024, tc::kSwizzle128), ids,
+                                 tc::desc(sXw + s * 16384 + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024, tc::kSwizzle128), ids,
                                  kk > 0 || s > 0 ? 1u : 0u);
             }
-            tc::commit(mb_s);
-            last_bar = mb_s;
-            last_ph = ph;
-        }
-        if (warp == 1 && c + 1 < nblk) block_decay<SOFTPLUS>(p, delta, block(c + 1), Ah, bias, lane, dec[(c + 1) & 1]);
-        bool ok = mbar_wait(mb_s, ph, kWaitNs, status);
-        tc::fence_after();
-        // (a wait that ran out is voted on before anything overwrites what the products may still read)
-        if (__syncthreads_or(!ok)) break;
-        stage_b(c + 1);
-        if constexpr (!LOCAL) {
-            // ---- M: row i = row, steps j0 ..; a warp whose steps all come after its rows writes zeros
-            unsigned char* mt = sM + (j0 >> 6) * 16384;
-            if (part > quarter) {
+            if (!LOCAL && with_state) {
 #pragma unroll
-                for (int k = 0; k < 32; k += 8) {
-                    const uint32_t off = tc::sw128_off(row, (j0 & 63u) + k);
-                    *reinterpret_cast<uint4*>(mt + off) = make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4*>(mt + 32768 + off) = make_uint4(0u, 0u, 0u, 0u);
+                for (int kk = 0; kk < kN / 16; ++kk) {
+                    const uint64_t a = tc::desc(sC + kk * 2048, 16384, 1024, tc::kSwizzle128);
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+                        tc::mma_bf16(tbase + kColCH, a, tc::desc(sH + s * 16384 + kk * 2048, 16384, 1024, tc::kSwizzle128),
+                                     idh, kk > 0 || s > 0 ? 1u : 0u);
                 }
-            } else {
+            }
+            commit(mb_s, ph);
+        }
+        stage_z(c);
+        // (by a warp that has no part in M)
+        if (warp == kDecayWarp && c + 1 < nblk) block_decay<SOFTPLUS>(p, delta, block(c + 1), Ah, bias, lane, dec[(c + 1) & 1]);
+        bool ok = true;
+        if constexpr (!LOCAL) {
+            // ---- M, in two terms in TMEM: row i = row, steps j0 ..
+            ok = mbar_wait(mb_g, ph, kWaitNs, status);
+            __syncwarp();
+            tc::fence_after();
+            if (part <= quarter) {
                 uint32_t gv[32];
                 tc::ld32(trow + kColG + j0, gv);
                 const bool same = part == quarter;
@@ -403,6 +423,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
                 for (int s = part + 1; s < quarter; ++s) ci += dc.stretch[s];
                 const pair_t ci2 = pk(ci);
                 const float* cj = (same ? dc.near : dc.far) + j0;
+                uint32_t m0[16], m1[16];
                 tc::wait_ld();
                 tc::after_wait(gv);
 #pragma unroll
@@ -422,103 +443,106 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
                             v[q] = pk(j <= lane ? f.x : 0.f, j + 1 <= lane ? f.y : 0.f);
                         }
                     }
-                    store_split8<2>(mt, 32768, row, (j0 & 63u) + k, v);
+                    split8<2>(v, [&](int t, const uint32_t (&w)[4]) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) (t ? m1 : m0)[k / 2 + q] = w[q];
+                    });
                 }
+                tc::st16(trow + kColM + j0 / 2, m0);
+                tc::st16(trow + kColM + 64 + j0 / 2, m1);
+                tc::wait_st();
             }
-            cp_wait<2>();                               // z (X and B of the next block may be on their way)
-            tc::fence_async_smem();
-            tc::fence_before();
-            __syncthreads();
+        }
+        ok = mbar_wait(mb_s, ph, kWaitNs, status) && ok;
+        tc::fence_after();
+        tc::fence_before();
+        // (a wait that ran out is voted on before anything overwrites what the products may still read)
+        if (__syncthreads_or(!ok)) break;
+        if constexpr (!LOCAL) {
             if (tid == 0) {
                 tc::fence_after();
-                constexpr uint32_t idy = tc::idesc_bf16(128, kP, false, false), idh = tc::idesc_bf16(128, kP, true, true);
+                constexpr uint32_t idy = tc::idesc_bf16(128, kP, false, false);
 #pragma unroll
                 for (int kk = 0; kk < kQ / 16; ++kk) {
                     const uint64_t bx = tc::desc(sX + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024, tc::kSwizzle128);
 #pragma unroll
                     for (int s = 0; s < 2; ++s)
-                        tc::mma_bf16(tbase + kColY,
-                                     tc::desc(sM + s * 32768 + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024, tc::kSwizzle128), bx,
-                                     idy, kk > 0 || s > 0 ? 1u : 0u);
+                        tc::mma_bf16_ta(tbase + kColY, tbase + kColM + s * 64 + kk * 8, bx, idy, kk > 0 || s > 0 ? 1u : 0u);
                 }
-                if (with_state) {
-#pragma unroll
-                    for (int kk = 0; kk < kN / 16; ++kk) {
-                        const uint64_t a = tc::desc(sC + kk * 2048, 16384, 1024, tc::kSwizzle128);
-#pragma unroll
-                        for (int s = 0; s < 2; ++s)
-                            tc::mma_bf16(tbase + kColCH, a, tc::desc(sH + s * 16384 + kk * 2048, 16384, 1024, tc::kSwizzle128),
-                                         idh, kk > 0 || s > 0 ? 1u : 0u);
-                    }
-                }
-                tc::commit(mb_y);
-                last_bar = mb_y;
-                last_ph = ph;
+                commit(mb_y, ph);
             }
-            ok = mbar_wait(mb_y, ph, kWaitNs, status);
-            tc::fence_after();
-            if (__syncthreads_or(!ok)) break;
-            stage_c(c + 1);
-            // ---- outputs of step row, channels p0 ..
-            {
-                uint32_t yv[16], cv[16];
-                tc::ld16(trow + kColY + p0, yv);
-                if (with_state) tc::ld16(trow + kColCH + p0, cv);
-                float e = dc.head[row];
-                for (int s = 0; s < quarter; ++s) e += dc.stretch[s];
-                e = ex2_approx(e);
-                tc::wait_ld();
-                tc::after_wait(yv);
-                if (with_state) tc::after_wait(cv);
-                const unsigned char* xt = sX + (row >> 6) * 8192;
-                unsigned char* zt = sZ + (row >> 6) * 8192;
-                // neighbouring lanes trade a channel, so that each has two steps of one: whole words of
-                // x, z and the outputs
-                const bool odd = lane & 1;
-#pragma unroll
-                for (int k = 0; k < 16; k += 2) {
-                    float v0 = __uint_as_float(yv[k]), v1 = __uint_as_float(yv[k + 1]);
-                    if (with_state) {
-                        v0 = fmaf(e, __uint_as_float(cv[k]), v0);
-                        v1 = fmaf(e, __uint_as_float(cv[k + 1]), v1);
-                    }
-                    const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-                    const uint32_t at = tc::sw128_off(p0 + k + (odd ? 1u : 0u), row & 62u);
-                    const uint32_t xw = *reinterpret_cast<const uint32_t*>(xt + at);
-                    pair_t v = pfma(pk(Dv[k / 2]), pk(__uint_as_float(xw << 16), __uint_as_float(xw & 0xFFFF0000u)),
-                                    odd ? pk(got, v1) : pk(v0, got));
-                    uint32_t* zo = reinterpret_cast<uint32_t*>(zt + at);
-                    if (gate) {
-                        const uint32_t zw = *zo;
-                        v = pmul(v, psilu(pk(__uint_as_float(zw << 16), __uint_as_float(zw & 0xFFFF0000u))));
-                    }
-                    const float2 f = halves(v);
-                    const __nv_bfloat162 t = __floats2bfloat162_rn(f.x, f.y);
-                    *zo = *reinterpret_cast<const uint32_t*>(&t);
-                }
-            }
-        } else {
-            stage_c(c + 1);
         }
-        // ---- the state
+        stage_b(c + 1);
+        stage_c(c + 1);
+        // ---- the state (Y runs)
+        uint32_t cv[LOCAL ? 8 : 16];
         {
             uint32_t sv[16];
             tc::ld16(trow + kColS + p0, sv);
+            if constexpr (!LOCAL)
+                if (with_state) tc::ld16(trow + kColCH + p0, cv);
             const float a = (dc.stretch[0] + dc.stretch[1]) + (dc.stretch[2] + dc.stretch[3]);
             const float d = ex2_approx(a);
             total += a;
             tc::wait_ld();
             tc::after_wait(sv);
+            if (!LOCAL && with_state) tc::after_wait(cv);
 #pragma unroll
             for (int k = 0; k < 16; ++k) H[k] = fmaf(d, H[k], __uint_as_float(sv[k]));
             if constexpr (!LOCAL) store_state();
         }
+        if constexpr (!LOCAL) {
+            ok = mbar_wait(mb_y, ph, kWaitNs, status);
+            tc::fence_after();
+            cp_wait<2>();                               // z; B and C of the next block may be on their way
+            if (__syncthreads_or(!ok)) break;
+            // ---- outputs of step row, channels p0 ..
+            uint32_t yv[16];
+            tc::ld16(trow + kColY + p0, yv);
+            float e = dc.head[row];
+            for (int s = 0; s < quarter; ++s) e += dc.stretch[s];
+            e = ex2_approx(e);
+            tc::wait_ld();
+            tc::after_wait(yv);
+            const unsigned char* xt = sX + (row >> 6) * 8192;
+            unsigned char* zt = sZ + (row >> 6) * 8192;
+            // neighbouring lanes trade a channel, so that each has two steps of one: whole words of
+            // x, z and the outputs
+            const bool odd = lane & 1;
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+                float v0 = __uint_as_float(yv[k]), v1 = __uint_as_float(yv[k + 1]);
+                if (with_state) {
+                    v0 = fmaf(e, __uint_as_float(cv[k]), v0);
+                    v1 = fmaf(e, __uint_as_float(cv[k + 1]), v1);
+                }
+                const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+                const uint32_t at = tc::sw128_off(p0 + k + (odd ? 1u : 0u), row & 62u);
+                const uint32_t xw = *reinterpret_cast<const uint32_t*>(xt + at);
+                pair_t v = pfma(pk(Dv[k / 2]), pk(__uint_as_float(xw << 16), __uint_as_float(xw & 0xFFFF0000u)),
+                                odd ? pk(got, v1) : pk(v0, got));
+                uint32_t* zo = reinterpret_cast<uint32_t*>(zt + at);
+                if (gate) {
+                    const uint32_t zw = *zo;
+                    v = pmul(v, psilu(pk(__uint_as_float(zw << 16), __uint_as_float(zw & 0xFFFF0000u))));
+                }
+                const float2 f = halves(v);
+                const __nv_bfloat162 t = __floats2bfloat162_rn(f.x, f.y);
+                *zo = *reinterpret_cast<const uint32_t*>(&t);
+            }
+        }
+        cp_wait<0>();                                   // X, B and C of the next block
         tc::fence_async_smem();
         tc::fence_before();
         __syncthreads();
-        if constexpr (!LOCAL) store_out(sZ, out, L, block(c), grid);
-        if (!LOCAL && !grid) __syncthreads();           // others' outputs are still in the tile
-        stage_z(c + 1);
+        if constexpr (!LOCAL) {
+            if (tid == 0 && c + 1 < nblk) {
+                tc::fence_after();
+                issue_g(ph ^ 1u);
+            }
+            store_out(sZ, out, L, block(c), grid);
+        }
+        stage_x(c + 2);
         done = c + 1;
     }
     // a wait ran out: the products may still be under way, so wait (bounded) for the last batch
