@@ -50,16 +50,19 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kQ = 128, kP = 64, kN = 128;
 constexpr int kThreads = 512;
-constexpr int kDecayWarp = 12;                 // steps 96 .. 127 of rows 0 .. 31: nothing of M
+// warps with nothing of M to compute (steps 64 .. 95 and 96 .. 127 of rows 0 .. 31)
+constexpr int kIssueWarp = 8, kDecayWarp = 12;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColG = 0, kColY = 128, kColCH = 192, kColS = 256, kColM = 320;   // M: two terms of 64 columns
+// TMEM columns.  M's two terms lie where G was, 16 columns each for a stretch's 32 steps: each thread
+// writes what it has read.  C H and S keep the products of H's and X' terms apart.
+constexpr uint32_t kColG = 0, kColY = 128, kColCH = 192, kColS = 320;
 constexpr uint64_t kWaitNs = 500000000ull;
 
 // shared memory (bytes from a 1024-aligned base); a tile is two 64-step halves of rows of 128 bytes
 constexpr int OFF_C = 0;                       // 128 states
 constexpr int OFF_B = 32 * 1024;
 constexpr int OFF_X = 64 * 1024;               // two buffers of 64 channels
-constexpr int OFF_XW = 96 * 1024;              // X', three terms
+constexpr int OFF_XW = 96 * 1024;              // X': [half][term]
 constexpr int OFF_H = 144 * 1024;              // two terms of 128 x 64
 constexpr int OFF_Z = 176 * 1024;              // z, then the outputs
 constexpr int OFF_DEC = 192 * 1024;            // two blocks' Decay
@@ -246,7 +249,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
     static_assert(OFF_DEC % 16 == 0, "vector reads of the decay");
     unsigned char *sC = smem + OFF_C, *sB = smem + OFF_B, *sXw = smem + OFF_XW, *sH = smem + OFF_H, *sZ = smem + OFF_Z;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int quarter = warp & 3, part = warp >> 2;
     const uint32_t row = (uint32_t)(32 * quarter + lane), j0 = (uint32_t)(32 * part), p0 = (uint32_t)(16 * part);
     const int64_t L = p.total, h = tk.d0 / kP, d_first = tk.d0, g_first = tk.g;
@@ -330,30 +333,65 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
     tc::fence_after();
     const uint32_t tbase = *tslot, trow = tbase + ((uint32_t)(32 * quarter) << 16);
 
-    uint64_t* last_bar = nullptr;                       // thread 0: its latest commit
+    uint64_t* last_bar = nullptr;                       // the issuing thread's: its latest commit
     unsigned last_ph = 0;
     auto commit = [&](uint64_t* bar, unsigned ph) {
         tc::commit(bar);
         last_bar = bar;
         last_ph = ph;
     };
-    auto issue_g = [&](unsigned ph) {
-        constexpr uint32_t id = tc::idesc_bf16(128, 128, true, true);
+    // X' of a block, in three terms: two 8-step pieces of a channel per thread
+    auto make_xw = [&](int c) {
+        const Decay& dc = dec[c & 1];
+        const unsigned char* sX = smem + OFF_X + (c & 1) * 16384;
 #pragma unroll
-        for (int kk = 0; kk < kN / 16; ++kk)
-            tc::mma_bf16(tbase + kColG, tc::desc(sC + kk * 2048, 16384, 1024, tc::kSwizzle128),
-                         tc::desc(sB + kk * 2048, 16384, 1024, tc::kSwizzle128), id, kk > 0 ? 1u : 0u);
-        commit(mb_g, ph);
-    };
-    if constexpr (!LOCAL) {
-        if (tid == 0 && nblk > 0) issue_g(0u);
-        if (part > quarter) {                           // M's steps behind all of the warp's rows stay zero
-            const uint32_t none[16] = {};
-            tc::st16(trow + kColM + j0 / 2, none);
-            tc::st16(trow + kColM + 64 + j0 / 2, none);
-            tc::wait_st();
+        for (int r = 0; r < 2; ++r) {
+            const uint32_t e = (uint32_t)tid + (uint32_t)r * kThreads, pp = e >> 4, s8 = (e & 15u) * 8u;
+            const uint4 raw = *reinterpret_cast<const uint4*>(sX + (s8 >> 6) * 8192 + tc::sw128_off(pp, s8 & 63u));
+            const uint32_t w4[4] = {raw.x, raw.y, raw.z, raw.w};
+            const ulonglong2* wj = reinterpret_cast<const ulonglong2*>(dc.w + s8);
+            const ulonglong2 wa = wj[0], wb = wj[1];
+            const pair_t w2[4] = {wa.x, wa.y, wb.x, wb.y};
+            pair_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[k] = pmul(pk(__uint_as_float(w4[k] << 16), __uint_as_float(w4[k] & 0xFFFF0000u)), w2[k]);
+            store_split8<3>(sXw + (s8 >> 6) * 24576, 8192, pp, s8 & 63u, v);
         }
-    }
+    };
+    // G, S and C H of a block, by one thread
+    auto issue_products = [&](unsigned ph, bool with_state) {
+        tc::fence_after();
+        if constexpr (!LOCAL) {
+            constexpr uint32_t id = tc::idesc_bf16(128, 128, true, true);
+            const uint64_t a = tc::desc(sC, 16384, 1024, tc::kSwizzle128), b = tc::desc(sB, 16384, 1024, tc::kSwizzle128);
+#pragma unroll
+            for (int kk = 0; kk < kN / 16; ++kk)
+                tc::mma_bf16(tbase + kColG, a + kk * (2048 >> 4), b + kk * (2048 >> 4), id, kk > 0 ? 1u : 0u);
+            commit(mb_g, ph);
+        }
+        {
+            constexpr uint32_t id = tc::idesc_bf16(128, 3 * kP, false, false);
+            const uint64_t a = tc::desc(sB, 16, 1024, tc::kSwizzle128), b = tc::desc(sXw, 16, 1024, tc::kSwizzle128);
+#pragma unroll
+            for (int kk = 0; kk < kQ / 16; ++kk)
+                tc::mma_bf16(tbase + kColS, a + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2, b + (kk >> 2) * (24576 >> 4) + (kk & 3) * 2,
+                             id, kk > 0 ? 1u : 0u);
+        }
+        if (!LOCAL && with_state) {
+            constexpr uint32_t id = tc::idesc_bf16(128, 2 * kP, true, true);
+            const uint64_t a = tc::desc(sC, 16384, 1024, tc::kSwizzle128), b = tc::desc(sH, 16384, 1024, tc::kSwizzle128);
+#pragma unroll
+            for (int kk = 0; kk < kN / 16; ++kk)
+                tc::mma_bf16(tbase + kColCH, a + kk * (2048 >> 4), b + kk * (2048 >> 4), id, kk > 0 ? 1u : 0u);
+        }
+        commit(mb_s, ph);
+    };
+    if (nblk > 0) make_xw(0);
+    tc::fence_async_smem();
+    __syncthreads();
+    if (warp == kIssueWarp && nblk > 0 && tc::elect_one()) issue_products(0u, start_state);
+    __syncwarp();
     stage_x(1);
 
     float total = 0.f;                                  // LOCAL: the sum of a over the task
@@ -363,59 +401,18 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
         const Decay& dc = dec[c & 1];
         const unsigned char* sX = smem + OFF_X + (c & 1) * 16384;
         const bool with_state = c > 0 || start_state;
-        // ---- X', in three terms: two 8-step pieces of a channel per thread (G runs)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const uint32_t e = (uint32_t)tid + (uint32_t)r * kThreads, pp = e >> 4, s8 = (e & 15u) * 8u;
-            const uint32_t half = (s8 >> 6) * 8192;
-            const uint4 raw = *reinterpret_cast<const uint4*>(sX + half + tc::sw128_off(pp, s8 & 63u));
-            const uint32_t w4[4] = {raw.x, raw.y, raw.z, raw.w};
-            const ulonglong2* wj = reinterpret_cast<const ulonglong2*>(dc.w + s8);
-            const ulonglong2 wa = wj[0], wb = wj[1];
-            const pair_t w2[4] = {wa.x, wa.y, wb.x, wb.y};
-            pair_t v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                v[k] = pmul(pk(__uint_as_float(w4[k] << 16), __uint_as_float(w4[k] & 0xFFFF0000u)), w2[k]);
-            store_split8<3>(sXw + half, 16384, pp, s8 & 63u, v);
-        }
-        tc::fence_async_smem();
-        tc::fence_before();
-        __syncthreads();
-        if (tid == 0) {
-            tc::fence_after();
-            constexpr uint32_t ids = tc::idesc_bf16(128, kP, false, false), idh = tc::idesc_bf16(128, kP, true, true);
-#pragma unroll
-            for (int kk = 0; kk < kQ / 16; ++kk) {
-                const uint64_t ab = tc::desc(sB + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024, tc::kSwizzle128);
-#pragma unroll
-                for (int s = 0; s < 3; ++s)
-                    tc::mma_bf16(tbase + kColS, ab,
-                                 tc::desc(sXw + s * 16384 + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024, tc::kSwizzle128), ids,
-                                 kk > 0 || s > 0 ? 1u : 0u);
-            }
-            if (!LOCAL && with_state) {
-#pragma unroll
-                for (int kk = 0; kk < kN / 16; ++kk) {
-                    const uint64_t a = tc::desc(sC + kk * 2048, 16384, 1024, tc::kSwizzle128);
-#pragma unroll
-                    for (int s = 0; s < 2; ++s)
-                        tc::mma_bf16(tbase + kColCH, a, tc::desc(sH + s * 16384 + kk * 2048, 16384, 1024, tc::kSwizzle128),
-                                     idh, kk > 0 || s > 0 ? 1u : 0u);
-                }
-            }
-            commit(mb_s, ph);
-        }
-        stage_z(c);
-        // (by a warp that has no part in M)
         if (warp == kDecayWarp && c + 1 < nblk) block_decay<SOFTPLUS>(p, delta, block(c + 1), Ah, bias, lane, dec[(c + 1) & 1]);
         bool ok = true;
         if constexpr (!LOCAL) {
-            // ---- M, in two terms in TMEM: row i = row, steps j0 ..
+            // ---- M, in two terms over G: row i = row, steps j0 .. (S and C H run)
             ok = mbar_wait(mb_g, ph, kWaitNs, status);
             __syncwarp();
             tc::fence_after();
-            if (part <= quarter) {
+            uint32_t m0[16], m1[16];
+            if (part > quarter) {                       // all steps behind the warp's rows
+#pragma unroll
+                for (int k = 0; k < 16; ++k) m0[k] = m1[k] = 0u;
+            } else {
                 uint32_t gv[32];
                 tc::ld32(trow + kColG + j0, gv);
                 const bool same = part == quarter;
@@ -423,7 +420,6 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
                 for (int s = part + 1; s < quarter; ++s) ci += dc.stretch[s];
                 const pair_t ci2 = pk(ci);
                 const float* cj = (same ? dc.near : dc.far) + j0;
-                uint32_t m0[16], m1[16];
                 tc::wait_ld();
                 tc::after_wait(gv);
 #pragma unroll
@@ -448,49 +444,68 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
                         for (int q = 0; q < 4; ++q) (t ? m1 : m0)[k / 2 + q] = w[q];
                     });
                 }
-                tc::st16(trow + kColM + j0 / 2, m0);
-                tc::st16(trow + kColM + 64 + j0 / 2, m1);
-                tc::wait_st();
             }
+            tc::st16(trow + kColG + j0, m0);
+            tc::st16(trow + kColG + j0 + 16, m1);
+            tc::wait_st();
         }
         ok = mbar_wait(mb_s, ph, kWaitNs, status) && ok;
         tc::fence_after();
+        cp_wait<0>();                                   // X of the next block
         tc::fence_before();
         // (a wait that ran out is voted on before anything overwrites what the products may still read)
         if (__syncthreads_or(!ok)) break;
         if constexpr (!LOCAL) {
-            if (tid == 0) {
+            if (warp == kIssueWarp && tc::elect_one()) {
                 tc::fence_after();
-                constexpr uint32_t idy = tc::idesc_bf16(128, kP, false, false);
+                constexpr uint32_t id = tc::idesc_bf16(128, kP, false, false);
+                const uint64_t b = tc::desc(sX, 16, 1024, tc::kSwizzle128);
 #pragma unroll
-                for (int kk = 0; kk < kQ / 16; ++kk) {
-                    const uint64_t bx = tc::desc(sX + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024, tc::kSwizzle128);
+                for (int kk = 0; kk < kQ / 16; ++kk)
 #pragma unroll
                     for (int s = 0; s < 2; ++s)
-                        tc::mma_bf16_ta(tbase + kColY, tbase + kColM + s * 64 + kk * 8, bx, idy, kk > 0 || s > 0 ? 1u : 0u);
-                }
+                        tc::mma_bf16_ta(tbase + kColY, tbase + kColG + (kk >> 1) * 32 + s * 16 + (kk & 1) * 8,
+                                        b + (kk >> 2) * (8192 >> 4) + (kk & 3) * 2, id, kk > 0 || s > 0 ? 1u : 0u);
                 commit(mb_y, ph);
             }
+            __syncwarp();
         }
+        stage_z(c);
         stage_b(c + 1);
         stage_c(c + 1);
         // ---- the state (Y runs)
-        uint32_t cv[LOCAL ? 8 : 16];
+        uint32_t cv[LOCAL ? 8 : 16];                    // C H
         {
-            uint32_t sv[16];
-            tc::ld16(trow + kColS + p0, sv);
-            if constexpr (!LOCAL)
-                if (with_state) tc::ld16(trow + kColCH + p0, cv);
+            uint32_t s0[16], s1[16], s2[16];
+            tc::ld16(trow + kColS + p0, s0);
+            tc::ld16(trow + kColS + kP + p0, s1);
+            tc::ld16(trow + kColS + 2 * kP + p0, s2);
             const float a = (dc.stretch[0] + dc.stretch[1]) + (dc.stretch[2] + dc.stretch[3]);
             const float d = ex2_approx(a);
             total += a;
             tc::wait_ld();
-            tc::after_wait(sv);
-            if (!LOCAL && with_state) tc::after_wait(cv);
+            tc::after_wait(s0);
+            tc::after_wait(s1);
+            tc::after_wait(s2);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) H[k] = fmaf(d, H[k], __uint_as_float(sv[k]));
-            if constexpr (!LOCAL) store_state();
+            for (int k = 0; k < 16; ++k)
+                H[k] = fmaf(d, H[k], __uint_as_float(s0[k]) + (__uint_as_float(s1[k]) + __uint_as_float(s2[k])));
+            if constexpr (!LOCAL) {
+                store_state();
+                if (with_state) {
+                    uint32_t c1[16];
+                    tc::ld16(trow + kColCH + p0, cv);
+                    tc::ld16(trow + kColCH + kP + p0, c1);
+                    tc::wait_ld();
+                    tc::after_wait(cv);
+                    tc::after_wait(c1);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) cv[k] = __float_as_uint(__uint_as_float(cv[k]) + __uint_as_float(c1[k]));
+                }
+            }
         }
+        // ---- X' of the next block
+        if (c + 1 < nblk) make_xw(c + 1);
         if constexpr (!LOCAL) {
             ok = mbar_wait(mb_y, ph, kWaitNs, status);
             tc::fence_after();
@@ -531,24 +546,20 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
                 *zo = *reinterpret_cast<const uint32_t*>(&t);
             }
         }
-        cp_wait<0>();                                   // X, B and C of the next block
+        cp_wait<0>();                                   // B and C of the next block
         tc::fence_async_smem();
         tc::fence_before();
         __syncthreads();
-        if constexpr (!LOCAL) {
-            if (tid == 0 && c + 1 < nblk) {
-                tc::fence_after();
-                issue_g(ph ^ 1u);
-            }
-            store_out(sZ, out, L, block(c), grid);
-        }
+        if (warp == kIssueWarp && c + 1 < nblk && tc::elect_one()) issue_products(ph ^ 1u, true);
+        __syncwarp();
+        if constexpr (!LOCAL) store_out(sZ, out, L, block(c), grid);
         stage_x(c + 2);
         done = c + 1;
     }
     // a wait ran out: the products may still be under way, so wait (bounded) for the last batch
     // before TMEM and shared memory go; the outputs that are missing become NaN
     if (done < nblk) {
-        if (tid == 0 && last_bar) mbar_wait(last_bar, last_ph, kWaitNs, status);
+        if (last_bar) mbar_wait(last_bar, last_ph, kWaitNs, status);
         if constexpr (!LOCAL) {
             const int64_t a = tb0 + (int64_t)done * kQ > tk.t0 ? tb0 + (int64_t)done * kQ : tk.t0, n = tk.t1 - a;
             for (int64_t i = tid; i < n * kP; i += kThreads) out[i / n * L + a + i % n] = 0x7FC0;
