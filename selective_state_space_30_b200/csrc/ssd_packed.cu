@@ -32,11 +32,13 @@
 //
 // Every wait for the tensor cores is bounded; one that ran out ends the CTA's work with NaN in the
 // rest of its outputs.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
+#include "layout.h"            // encode_rows
 #include "pair.cuh"
 #include "scan_packed.cuh"
 #include "ssd_packed.h"
@@ -51,7 +53,7 @@ using bf16 = __nv_bfloat16;
 constexpr int kQ = 128, kP = 64, kN = 128;
 constexpr int kThreads = 512;
 // warps with nothing of M to compute (steps 64 .. 95 and 96 .. 127 of rows 0 .. 31)
-constexpr int kIssueWarp = 8, kDecayWarp = 12;
+constexpr int kIssueWarp = 8, kCopyWarp = 9, kDecayWarp = 12;
 constexpr uint32_t kTmemCols = 512;
 // TMEM columns.  M's two terms lie where G was, 16 columns each for a stretch's 32 steps: each thread
 // writes what it has read.  C H and S keep the products of H's and X' terms apart.
@@ -112,52 +114,81 @@ struct Block {
     int64_t t0, t1;         // the task's tokens
 };
 
-// Stages ROWS rows (the first at `base`) of a block into a tile; steps outside the task are zero.
-// [lo, hi): the tensor.  `grid`: every row starts on the 16-byte grid, and so does step 0.
+// The tensors as boxes of 64 steps, where their rows lie on the 16-byte grid.
+struct SsdMaps {
+    CUtensorMap u, z, B, C, out;
+};
+
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, const void* src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y),
+                 "r"(tc::smem_addr(src))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// Stages ROWS rows (the first at `base`) of a block into a tile, from rows off the 16-byte grid; steps
+// outside the task are zero.  [lo, hi): the tensor.  (Out of line, as is store_out: the block's loop is
+// long, and what seldom runs in it costs instruction fetches: 5.40 -> 4.84 us a block.)
 template <int ROWS>
-__device__ __forceinline__ void stage_tile(unsigned char* tile, const unsigned short* base, int64_t L, const Block& k,
-                                           const unsigned short* lo, const unsigned short* hi, bool grid) {
+__device__ __noinline__ void stage_tile(unsigned char* tile, const unsigned short* base, int64_t L, const Block& k,
+                                        const unsigned short* lo, const unsigned short* hi) {
     // a thread's pieces: the same eight steps of every 32nd row, which the swizzle treats alike
     const int r0 = threadIdx.x >> 4, q = threadIdx.x & 15;
     unsigned char* dst = tile + (q >> 3) * (ROWS * 128) + tc::sw128_off(r0, (q & 7) * 8);
     const int64_t t = k.tb + 8 * q, step = 32 * L;
     const unsigned short* src = base + (int64_t)r0 * L + t;
-    if (t >= k.t0 && t + 8 <= k.t1 && grid) {
-#pragma unroll
-        for (int i = 0; i < ROWS / 32; ++i, src += step) cp16(smem_u32(dst + i * 4096), src, 16);
-    } else if (t >= k.t1 || t + 8 <= k.t0) {
+    if (t >= k.t1 || t + 8 <= k.t0) {
 #pragma unroll
         for (int i = 0; i < ROWS / 32; ++i) *reinterpret_cast<uint4*>(dst + i * 4096) = make_uint4(0u, 0u, 0u, 0u);
-    } else {
-        const bool whole = t >= k.t0 && t + 8 <= k.t1;
+        return;
+    }
+    const bool whole = t >= k.t0 && t + 8 <= k.t1;
 #pragma unroll
-        for (int i = 0; i < ROWS / 32; ++i, src += step) {
-            const uintptr_t m = reinterpret_cast<uintptr_t>(src) & 15u;
-            const unsigned short* a = src - m / 2;
-            uint32_t o[4] = {0u, 0u, 0u, 0u};
-            if (whole && a >= lo && a + 16 <= hi) {
-                const uint4 x = __ldg(reinterpret_cast<const uint4*>(a)), y = __ldg(reinterpret_cast<const uint4*>(a) + 1);
-                const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-                // by whole words, then by half of one
-                uint32_t s[6];
+    for (int i = 0; i < ROWS / 32; ++i, src += step) {
+        const uintptr_t m = reinterpret_cast<uintptr_t>(src) & 15u;
+        const unsigned short* a = src - m / 2;
+        uint32_t o[4] = {0u, 0u, 0u, 0u};
+        if (whole && a >= lo && a + 16 <= hi) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(a)), y = __ldg(reinterpret_cast<const uint4*>(a) + 1);
+            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            // by whole words, then by half of one
+            uint32_t s[6];
 #pragma unroll
-                for (int e = 0; e < 6; ++e) s[e] = (m & 8) ? w[e + 2] : w[e];
+            for (int e = 0; e < 6; ++e) s[e] = (m & 8) ? w[e + 2] : w[e];
 #pragma unroll
-                for (int e = 0; e < 5; ++e) s[e] = (m & 4) ? s[e + 1] : s[e];
+            for (int e = 0; e < 5; ++e) s[e] = (m & 4) ? s[e + 1] : s[e];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] = __funnelshift_r(s[e], s[e + 1], (unsigned)(m & 2) * 8);
-            } else {
+            for (int e = 0; e < 4; ++e) o[e] = __funnelshift_r(s[e], s[e + 1], (unsigned)(m & 2) * 8);
+        } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (t + e >= k.t0 && t + e < k.t1) o[e / 2] |= (uint32_t)src[e] << (16 * (e & 1));
-            }
-            *reinterpret_cast<uint4*>(dst + i * 4096) = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int e = 0; e < 8; ++e)
+                if (t + e >= k.t0 && t + e < k.t1) o[e / 2] |= (uint32_t)src[e] << (16 * (e & 1));
         }
+        *reinterpret_cast<uint4*>(dst + i * 4096) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+// Zeroes the steps of a staged tile that lie outside the task.
+template <int ROWS>
+__device__ __forceinline__ void clear_outside(unsigned char* tile, const Block& k) {
+    const int r0 = threadIdx.x >> 4, q = threadIdx.x & 15;
+    const int64_t t = k.tb + 8 * q;
+    if (t >= k.t0 && t + 8 <= k.t1) return;
+    unsigned char* dst = tile + (q >> 3) * (ROWS * 128) + tc::sw128_off(r0, (q & 7) * 8);
+    uint32_t keep[4];
+#pragma unroll
+    for (int e = 0; e < 8; e += 2)
+        keep[e / 2] = (t + e >= k.t0 && t + e < k.t1 ? 0xFFFFu : 0u) | (t + e + 1 >= k.t0 && t + e + 1 < k.t1 ? 0xFFFF0000u : 0u);
+#pragma unroll
+    for (int i = 0; i < ROWS / 32; ++i) {
+        uint4* w = reinterpret_cast<uint4*>(dst + i * 4096);
+        const uint4 v = *w;
+        *w = make_uint4(v.x & keep[0], v.y & keep[1], v.z & keep[2], v.w & keep[3]);
     }
 }
 
 // The outputs, staged in the z tile, to global memory: each thread the pieces that it staged.
-__device__ __forceinline__ void store_out(const unsigned char* tile, unsigned short* base, int64_t L, const Block& k, bool grid) {
+__device__ __noinline__ void store_out(const unsigned char* tile, unsigned short* base, int64_t L, const Block& k, bool grid) {
     if (grid) {
 #pragma unroll
         for (int i0 = 0; i0 < kP * 16; i0 += kThreads) {
@@ -235,16 +266,14 @@ __device__ __forceinline__ void block_decay(const PackedParams& p, const unsigne
     if ((lane & 7) == 0) o.stretch[lane >> 3] = whole;
 }
 
-template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // Thread: TMEM lane and tile row `row`, and a quarter of that row's columns (32 of the 128 steps,
 // 16 of the 64 channels).  LOCAL: only the end state from zero and the product of the decays.
 template <bool LOCAL, bool SOFTPLUS>
-__device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, unsigned char* smem) {
+__device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& maps, const Task& tk, unsigned char* smem) {
     uint64_t* mb_g = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
-    uint64_t *mb_s = mb_g + 1, *mb_y = mb_g + 2;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(mb_g + 3);
-    int* status = reinterpret_cast<int*>(mb_g + 4);
+    uint64_t *mb_s = mb_g + 1, *mb_y = mb_g + 2, *mb_x = mb_g + 3, *mb_bc = mb_g + 4, *mb_z = mb_g + 5;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(mb_g + 6);
+    int* status = reinterpret_cast<int*>(mb_g + 7);
     Decay* dec = reinterpret_cast<Decay*>(smem + OFF_DEC);
     static_assert(OFF_DEC % 16 == 0, "vector reads of the decay");
     unsigned char *sC = smem + OFF_C, *sB = smem + OFF_B, *sXw = smem + OFF_XW, *sH = smem + OFF_H, *sZ = smem + OFF_Z;
@@ -262,35 +291,81 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
     const int64_t tb0 = grid ? tk.t0 & ~7 : tk.t0;
     const int nblk = (int)((tk.t1 - tb0 + kQ - 1) / kQ);
     auto block = [&](int c) { return Block{tb0 + (int64_t)c * kQ, tk.t0, tk.t1}; };
+    // Copies of a block's tiles: boxes that one thread asks for on the 16-byte grid, else by all threads.
+    auto inside = [&](int c) { return block(c).tb >= tk.t0 && block(c).tb + kQ <= tk.t1; };
+    auto boxes = [&](unsigned char* tile, int half, const CUtensorMap* map, int c, int64_t row0, uint64_t* bar) {
+        const int t = (int)block(c).tb;
+        tma_2d(tile, map, t, (int)row0, bar);
+        tma_2d(tile + half, map, t + 64, (int)row0, bar);
+    };
+    unsigned ph_x = 0u, ph_bc = 0u, ph_z = 0u;
+    bool due_x = false, due_bc = false, due_z = false;   // boxes are on their way
+    auto wait_box = [&](bool& due, uint64_t* bar, unsigned& phase) {
+        if (!due) return true;
+        if (!mbar_wait(bar, phase, kWaitNs, status)) return false;
+        phase ^= 1u;
+        due = false;
+        return true;
+    };
     auto stage_x = [&](int c) {
-        if (c < nblk) stage_tile<kP>(smem + OFF_X + (c & 1) * 16384, u + d_first * L, L, block(c), u, u + p.dim * L, grid);
-        cp_commit();
+        if (c >= nblk) return;
+        unsigned char* tile = smem + OFF_X + (c & 1) * 16384;
+        due_x = grid;
+        if (!grid) {
+            stage_tile<kP>(tile, u + d_first * L, L, block(c), u, u + p.dim * L);
+        } else if (warp == kCopyWarp && tc::elect_one()) {
+            mbar_arrive_tx(mb_x, 16384);
+            boxes(tile, 8192, &maps.u, c, d_first, mb_x);
+        }
     };
-    auto stage_b = [&](int c) {
-        if (c < nblk) stage_tile<kN>(sB, Bt + g_first * kN * L, L, block(c), Bt, Bt + p.ngroups * kN * L, grid);
-        cp_commit();
-    };
-    auto stage_c = [&](int c) {
-        if (!LOCAL && c < nblk) stage_tile<kN>(sC, Ct + g_first * kN * L, L, block(c), Ct, Ct + p.ngroups * kN * L, grid);
-        cp_commit();
+    auto stage_bc = [&](int c) {
+        if (c >= nblk) return;
+        due_bc = grid;
+        if (!grid) {
+            stage_tile<kN>(sB, Bt + g_first * kN * L, L, block(c), Bt, Bt + p.ngroups * kN * L);
+            if (!LOCAL) stage_tile<kN>(sC, Ct + g_first * kN * L, L, block(c), Ct, Ct + p.ngroups * kN * L);
+        } else if (warp == kCopyWarp && tc::elect_one()) {
+            mbar_arrive_tx(mb_bc, LOCAL ? 32768u : 65536u);
+            boxes(sB, 16384, &maps.B, c, g_first * kN, mb_bc);
+            if (!LOCAL) boxes(sC, 16384, &maps.C, c, g_first * kN, mb_bc);
+        }
     };
     auto stage_z = [&](int c) {
-        if (gate && c < nblk) stage_tile<kP>(sZ, z + d_first * L, L, block(c), z, z + p.dim * L, grid);
-        cp_commit();
+        // the outputs before are out of the tile
+        if (grid && warp == kCopyWarp && tc::elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        if (!gate) return;
+        due_z = grid;
+        if (!grid) {
+            stage_tile<kP>(sZ, z + d_first * L, L, block(c), z, z + p.dim * L);
+        } else if (warp == kCopyWarp && tc::elect_one()) {
+            mbar_arrive_tx(mb_z, 16384);
+            boxes(sZ, 8192, &maps.z, c, d_first, mb_z);
+        }
+    };
+    // Where boxes brought tokens of others: of X and B those have to be zero; of C and z they reach
+    // outputs alone that are not written.
+    auto wait_x = [&](int c) {
+        const bool was = due_x, ok = wait_box(due_x, mb_x, ph_x);
+        if (was && !inside(c)) clear_outside<kP>(smem + OFF_X + (c & 1) * 16384, block(c));
+        return ok;
+    };
+    auto wait_bc = [&](int c) {
+        const bool was = due_bc, ok = wait_box(due_bc, mb_bc, ph_bc);
+        if (was && !inside(c)) clear_outside<kN>(sB, block(c));
+        return ok;
     };
 
+    tc::fence_async_smem();                             // (the item search wrote where boxes will)
     __syncthreads();
     if (tid == 0) {
-        mbar_init(mb_g, 1);
-        mbar_init(mb_s, 1);
-        mbar_init(mb_y, 1);
+        for (uint64_t* b = mb_g; b <= mb_z; ++b) mbar_init(b, 1);
         *status = SSM_OK;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) tc::alloc(tslot, kTmemCols);
+    __syncthreads();
     stage_x(0);
-    stage_b(0);
-    stage_c(0);
+    stage_bc(0);
     if (warp == kDecayWarp && nblk > 0) block_decay<SOFTPLUS>(p, delta, block(0), Ah, bias, lane, dec[0]);
 
     // the state: n = row, channels p0 .. p0 + 15
@@ -326,10 +401,11 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
         }
     };
     if (start_state) store_state();
-    cp_wait<0>();
+    bool ok = wait_x(0);
+    ok = wait_bc(0) && ok;
     tc::fence_async_smem();
     tc::fence_before();
-    __syncthreads();                                    // X, B, C, the decay and the state are staged
+    const bool staged = !__syncthreads_or(!ok);         // X, B, C, the decay and the state
     tc::fence_after();
     const uint32_t tbase = *tslot, trow = tbase + ((uint32_t)(32 * quarter) << 16);
 
@@ -390,19 +466,21 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
     if (nblk > 0) make_xw(0);
     tc::fence_async_smem();
     __syncthreads();
-    if (warp == kIssueWarp && nblk > 0 && tc::elect_one()) issue_products(0u, start_state);
-    __syncwarp();
-    stage_x(1);
+    if (staged) {
+        stage_x(1);
+        if (warp == kIssueWarp && nblk > 0 && tc::elect_one()) issue_products(0u, start_state);
+        __syncwarp();
+    }
 
     float total = 0.f;                                  // LOCAL: the sum of a over the task
     int done = 0;                                       // blocks whose outputs are written
-    for (int c = 0; c < nblk; ++c) {
+    for (int c = 0; staged && c < nblk; ++c) {
         const unsigned ph = (unsigned)c & 1u;
         const Decay& dc = dec[c & 1];
         const unsigned char* sX = smem + OFF_X + (c & 1) * 16384;
         const bool with_state = c > 0 || start_state;
         if (warp == kDecayWarp && c + 1 < nblk) block_decay<SOFTPLUS>(p, delta, block(c + 1), Ah, bias, lane, dec[(c + 1) & 1]);
-        bool ok = true;
+        ok = true;
         if constexpr (!LOCAL) {
             // ---- M, in two terms over G: row i = row, steps j0 .. (S and C H run)
             ok = mbar_wait(mb_g, ph, kWaitNs, status);
@@ -451,7 +529,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
         }
         ok = mbar_wait(mb_s, ph, kWaitNs, status) && ok;
         tc::fence_after();
-        cp_wait<0>();                                   // X of the next block
+        ok = wait_x(c + 1) && ok;
         tc::fence_before();
         // (a wait that ran out is voted on before anything overwrites what the products may still read)
         if (__syncthreads_or(!ok)) break;
@@ -470,9 +548,8 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
             }
             __syncwarp();
         }
-        stage_z(c);
-        stage_b(c + 1);
-        stage_c(c + 1);
+        if constexpr (!LOCAL) stage_z(c);
+        stage_bc(c + 1);
         // ---- the state (Y runs)
         uint32_t cv[LOCAL ? 8 : 16];                    // C H
         {
@@ -509,7 +586,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
         if constexpr (!LOCAL) {
             ok = mbar_wait(mb_y, ph, kWaitNs, status);
             tc::fence_after();
-            cp_wait<2>();                               // z; B and C of the next block may be on their way
+            ok = wait_box(due_z, mb_z, ph_z) && ok;
             if (__syncthreads_or(!ok)) break;
             // ---- outputs of step row, channels p0 ..
             uint32_t yv[16];
@@ -546,20 +623,33 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
                 *zo = *reinterpret_cast<const uint32_t*>(&t);
             }
         }
-        cp_wait<0>();                                   // B and C of the next block
+        ok = wait_bc(c + 1);
         tc::fence_async_smem();
         tc::fence_before();
-        __syncthreads();
+        if (__syncthreads_or(!ok)) break;
+        if constexpr (!LOCAL) {
+            if (!grid || !inside(c)) {
+                store_out(sZ, out, L, block(c), grid);
+            } else if (warp == kCopyWarp && tc::elect_one()) {
+                const int t = (int)block(c).tb;
+                tma_store(&maps.out, t, (int)d_first, sZ);
+                tma_store(&maps.out, t + 64, (int)d_first, sZ + 8192);
+            }
+        }
+        stage_x(c + 2);
         if (warp == kIssueWarp && c + 1 < nblk && tc::elect_one()) issue_products(ph ^ 1u, true);
         __syncwarp();
-        if constexpr (!LOCAL) store_out(sZ, out, L, block(c), grid);
-        stage_x(c + 2);
         done = c + 1;
     }
+    if (warp == kCopyWarp && tc::elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
     // a wait ran out: the products may still be under way, so wait (bounded) for the last batch
     // before TMEM and shared memory go; the outputs that are missing become NaN
     if (done < nblk) {
         if (last_bar) mbar_wait(last_bar, last_ph, kWaitNs, status);
+        wait_box(due_x, mb_x, ph_x);
+        wait_box(due_bc, mb_bc, ph_bc);
+        wait_box(due_z, mb_z, ph_z);
         if constexpr (!LOCAL) {
             const int64_t a = tb0 + (int64_t)done * kQ > tk.t0 ? tb0 + (int64_t)done * kQ : tk.t0, n = tk.t1 - a;
             for (int64_t i = tid; i < n * kP; i += kThreads) out[i / n * L + a + i % n] = 0x7FC0;
@@ -567,7 +657,6 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
 #pragma unroll
         for (int k = 0; k < 16; ++k) H[k] = __int_as_float(0x7FC00000);
     }
-    cp_wait_all();
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
         const int64_t d = d_first + p0 + k;
@@ -582,7 +671,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const Task& tk, 
 }
 
 template <bool SOFTPLUS>
-__global__ void __launch_bounds__(kThreads, 1) ssd_packed_kernel(const PackedParams p) {
+__global__ void __launch_bounds__(kThreads, 1) ssd_packed_kernel(const PackedParams p, const __grid_constant__ SsdMaps maps) {
     extern __shared__ __align__(1024) unsigned char ssd_smem[];
     unsigned char* smem = ssd_smem + ((1024u - (smem_u32(ssd_smem) & 1023u)) & 1023u);
     const unsigned h = blockIdx.x % p.n_tiles;
@@ -592,8 +681,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_packed_kernel(const PackedPar
     tk.ci0 = tk.d0 - tk.g * (int)p.group_dim;
     tk.nch = kP;
     const Run run = find_run<bf16>(p, blockIdx.x / p.n_tiles, reinterpret_cast<int64_t*>(smem), kThreads, tk);
-    if (run == kRunFull) run_head<false, SOFTPLUS>(p, tk, smem);
-    else if (run == kRunLocal) run_head<true, SOFTPLUS>(p, tk, smem);
+    if (run == kRunFull) run_head<false, SOFTPLUS>(p, maps, tk, smem);
+    else if (run == kRunLocal) run_head<true, SOFTPLUS>(p, maps, tk, smem);
 }
 
 }  // namespace
@@ -606,11 +695,21 @@ int ssd_packed_launch(PackedParams& p, cudaStream_t s) {
     const int64_t ctas = p.nheads * (p.chunk > 0 ? p.n_chunks : p.n_seq);
     if (ctas > 0x7FFFFFFF) return SSM_ERR_UNSUPPORTED;
     p.n_tiles = (unsigned)p.nheads;
+    SsdMaps maps{};
+    if (p.grid16) {
+        auto rows = [&](CUtensorMap* m, const void* t, int64_t n, uint32_t box) {
+            return encode_rows(m, t, 2, (uint64_t)p.total, (uint64_t)n, box, CU_TENSOR_MAP_SWIZZLE_128B, 64);
+        };
+        const int64_t bc = p.ngroups * kN;
+        if (!rows(&maps.u, p.u, p.dim, kP) || !rows(&maps.B, p.B, bc, kN) || !rows(&maps.C, p.C, bc, kN) ||
+            !rows(&maps.out, p.out, p.dim, kP) || (p.z && !rows(&maps.z, p.z, p.dim, kP)))
+            return SSM_ERR_CUDA;
+    }
     auto* kernel = p.softplus ? ssd_packed_kernel<true> : ssd_packed_kernel<false>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
         return SSM_ERR_CUDA;
     for (p.phase = 1; p.phase <= (p.chunk > 0 ? 2 : 1); ++p.phase) {
-        kernel<<<(unsigned)ctas, kThreads, kSmem, s>>>(p);
+        kernel<<<(unsigned)ctas, kThreads, kSmem, s>>>(p, maps);
         if (cudaGetLastError() != cudaSuccess) return SSM_ERR_CUDA;
     }
     return SSM_OK;
