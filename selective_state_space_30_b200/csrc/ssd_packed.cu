@@ -71,13 +71,13 @@ constexpr int OFF_DEC = 192 * 1024;            // two blocks' Decay
 constexpr int OFF_BAR = OFF_DEC + 2 * 4096;
 constexpr int kSmem = OFF_BAR + 256 + 1024;    // and room to align the base
 
-// A block's decay, in log2 units: over the 32-step stretches of its 128 steps.  dt_j is a factor of
-// j's weights: as its logarithm, one sum less per element of M, where softplus makes it positive,
-// and by itself (`dt`) where it may have any sign.
+// A block's decay over the 32-step stretches of its 128 steps, in log2 units but for far and w.
+// Within a stretch dt_j is a factor of j's weights: as its logarithm, one product less per element of
+// M, where softplus makes it positive, and by itself (`dt`) where it may have any sign.
 struct Decay {
     float head[kQ];       // from the stretch's start through the step
     float near[kQ];       // log2 dt_j less that: with head_i, the weight of j for i of the same stretch
-    float far[kQ];        // log2 dt_j and the steps from behind j to the stretch's end: for later stretches
+    float far[kQ];        // dt_j times the decay from behind j to the stretch's end: for later stretches
     float w[kQ];          // 2^s(end, j) dt_j
     float dt[kQ];
     float stretch[4];     // whole stretches
@@ -251,6 +251,7 @@ __device__ __forceinline__ void block_decay(const PackedParams& p, const unsigne
         const float v = __shfl_sync(0xffffffffu, whole, 8 * s);
         if (s > (lane >> 3)) later += v;
     }
+    const float rest = ex2_approx(later);
     float suf = 0.f;
 #pragma unroll
     for (int e = 3; e >= 0; --e) {
@@ -258,8 +259,9 @@ __device__ __forceinline__ void block_decay(const PackedParams& p, const unsigne
         const float l = SOFTPLUS ? __log2f(dt[e]) : 0.f;     // -inf where dt = 0: a weight of zero
         o.head[j] = up + pre[e];
         o.near[j] = l - (up + pre[e]);
-        o.far[j] = l + (suf + down);
-        o.w[j] = ex2_approx((suf + down) + later) * dt[e];
+        const float far = ex2_approx(suf + down) * dt[e];
+        o.far[j] = far;
+        o.w[j] = far * rest;
         if (!SOFTPLUS) o.dt[j] = dt[e];
         suf += dt[e] * Ah;
     }
@@ -496,7 +498,8 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
                 const bool same = part == quarter;
                 float ci = dc.head[row];
                 for (int s = part + 1; s < quarter; ++s) ci += dc.stretch[s];
-                const pair_t ci2 = pk(ci);
+                // over whole stretches the weight is a product of the row's and the step's
+                const pair_t ci2 = pk(same ? ci : ex2_approx(ci));
                 const float* cj = (same ? dc.near : dc.far) + j0;
                 tc::wait_ld();
                 tc::after_wait(gv);
@@ -508,13 +511,15 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
                     pair_t v[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        v[q] = pmul(pk(__uint_as_float(gv[k + 2 * q]), __uint_as_float(gv[k + 2 * q + 1])),
-                                    pex2(padd(ci2, c2[q])));
-                        if constexpr (!SOFTPLUS) v[q] = pmul(v[q], *reinterpret_cast<const pair_t*>(dc.dt + j0 + k + 2 * q));
+                        v[q] = pk(__uint_as_float(gv[k + 2 * q]), __uint_as_float(gv[k + 2 * q + 1]));
                         if (same) {                     // of the stretch's own steps, those up to the row's
+                            v[q] = pmul(v[q], pex2(padd(ci2, c2[q])));
+                            if constexpr (!SOFTPLUS) v[q] = pmul(v[q], *reinterpret_cast<const pair_t*>(dc.dt + j0 + k + 2 * q));
                             const float2 f = halves(v[q]);
                             const int j = k + 2 * q;
                             v[q] = pk(j <= lane ? f.x : 0.f, j + 1 <= lane ? f.y : 0.f);
+                        } else {
+                            v[q] = pmul(v[q], pmul(ci2, c2[q]));
                         }
                     }
                     split8<2>(v, [&](int t, const uint32_t (&w)[4]) {
