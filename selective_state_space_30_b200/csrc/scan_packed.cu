@@ -36,20 +36,21 @@ int tile_channels(int64_t N) {
     }
 }
 
-// The tensor-core form, where it covers the shape and the sequences are 64 tokens or more in the
+// The tensor-core form, where it covers the shape and the sequences are 32 tokens or more in the
 // mean: its blocks are 128 tokens long whatever a sequence fills of them (32 heads: 60 prompts of
-// 10 tokens 282 us against the scan's 170, 40 of 51 tokens 193 against 186, 20 of 100 tokens and
-// 8 heads 51 against 104, 6 of 680 tokens 115 against 399).
-bool on_tensor_cores(const ssm_dims_t& d) { return ssm::packed::ssd_packed_covers(d) && d.seqlen >= 64 * d.batch; }
+// 10 tokens 175 us against the scan's 159, of 20 tokens 175 against 174, 40 of 32 tokens 120 against
+// 124, of 51 tokens 122 against 192; 20 of 100 tokens and 8 heads 17 against 35).
+bool on_tensor_cores(const ssm_dims_t& d) { return ssm::packed::ssd_packed_covers(d) && d.seqlen >= 32 * d.batch; }
 
 // The tokens of a chunk, or kNoChunk: a function of the shape and the hint alone, so the same call
 // gives the same bits.  `share` is what each CTA slot of the machine gets of the (token, tile)
 // products.  Sequences are cut, into chunks of one share, where the longest is over four shares
 // and so would still run when everything else is done: one prompt of 8191 tokens x 1536 channels
 // takes 203 us cut at 352 tokens, 231 at 448, 292 at 672; 24 ragged prompts (16384 tokens x 4096
-// channels, the longest under two shares) 523 us uncut and 666 cut at 1184.  On the tensor cores a
-// middle chunk's first pass costs less than half of its second, so two and a half shares do: two
-// prompts of 4096 tokens, 32 heads, 195 us uncut and 138 cut at 768; six (two shares) 114 and 154.
+// channels, the longest under two shares) 492 us uncut and 666 cut at 1184.  On the tensor cores a
+// middle chunk's first pass costs less than half of its second, so three shares do: 4 prompts of
+// 4096 tokens in all, 32 heads, the longest of 3000 (3.3 shares), 116 us uncut and 91 cut at 896; 6,
+// the longest of 2241 (2.5 shares), 91 and 100, of 1508 (1.7) 65 and 99.
 int64_t choose_chunk(const ssm_dims_t& d, int64_t max_seqlen) {
     const bool ssd = on_tensor_cores(d);
     const int64_t ct = tile_channels(d.dstate), gd = d.dim / d.ngroups;
@@ -64,7 +65,7 @@ int64_t choose_chunk(const ssm_dims_t& d, int64_t max_seqlen) {
     if (q < least) q = least;
     const int64_t step = ssd ? 128 : 32;
     q = (q + step - 1) / step * step;
-    return longest > (ssd ? 5 * q / 2 : 4 * q) ? q : kNoChunk;
+    return longest > (ssd ? 3 : 4) * q ? q : kNoChunk;
 }
 
 bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

@@ -20,17 +20,26 @@
 // in j's 32-step stretch, whole stretches between, and the steps of i's stretch; within one
 // stretch it is a difference of two sums of at most 32 terms.
 //
-// Bound: the phases between the products, which threads compute one after the other, one CTA of 16
-// warps per SM.  Of a block's 6.6 us about 1.2 go into M, 0.9 into the outputs, 0.6 into X', 0.7 into
-// addresses of copies and 2.3 into the products and the barriers around them (tensor pipe 11 % busy).
-// Measured on one B200: 6 prompts of 4096 tokens, 32 heads 115 us (the scan kernel 400), one of 8192
-// tokens, 16 heads 121 (441).  Values in f32x2 pairs with log2 dt folded into the exponent, and whole
-// words of x, z and the outputs in the epilogue, brought a block from 9.2 to 6.6 us.  Tiles arrive by
-// 16-byte asynchronous copies into the 128-byte swizzle that the tensor cores read, each as soon as
-// its place is free: X a block ahead in a second buffer, B once G and S are done, C once C H is.
-// Rows off the 16-byte grid are shifted into place through registers.
+// Order of a block.  The products run under the threads' work: G, then S and C H while M is made from
+// G in tensor memory (M is Y's left operand there), Y while the state takes S and X' of the next
+// block is made.  Three barriers a block.
 //
-// Every wait for the tensor cores is bounded; one that ran out ends the CTA's work with NaN in the
+// Bound: the threads' phases, chains of few instructions over 16 warps, one CTA per SM.  Of a block's
+// 4.8 us about 0.4 go into waiting for G, 1.2 into M, 1.4 into the state and X', 1.3 into the outputs
+// (half of that silu's two MUFU operations) and 0.3 into the copies' orders.  Measured on one B200: 6 ragged
+// prompts of 4096 tokens, 32 heads 74 us (the scan kernel 400), one prompt of 8192 tokens, 16 heads 83
+// in chunks.  Steps, for the first of these: values in f32x2 pairs, log2 dt folded into the exponent and whole
+// words of x, z and the outputs in the epilogue 120 us; M in tensor memory instead of shared memory, so
+// that S need not have left its place, 104; the terms of X' and H side by side in one product each (a product
+// of 64 columns takes as long to read its left operand as one of 192), the products asked for by a warp that
+// M leaves idle and X' under Y 87; boxes of TMA instead of the threads' copies, and what seldom
+// runs out of line 79; weights across stretches as products 78; the rule on cutting 74.
+//
+// Tiles arrive in the 128-byte swizzle that the tensor cores read, each as soon as its place is free: X a
+// block ahead in a second buffer, B and C once G, S and C H are done, z once the outputs before it
+// have left.  Rows off the 16-byte grid are shifted into place through registers.
+//
+// Every wait for the tensor cores or a copy is bounded; one that ran out ends the CTA's work with NaN in the
 // rest of its outputs.
 #include <cuda.h>
 #include <cuda_bf16.h>

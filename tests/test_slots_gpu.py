@@ -202,7 +202,7 @@ def _chunk(ssm, p, n_seq, max_seqlen=0):
 
 def _tensor(dim, heads, N, dtype, total, n):
     """The calls that run on the tensor cores."""
-    return dtype == "bf16" and heads < dim and dim // heads == 64 and N == 128 and total >= 64 * n
+    return dtype == "bf16" and heads < dim and dim // heads == 64 and N == 128 and total >= 32 * n
 
 
 SCAN = [
