@@ -209,6 +209,30 @@ __device__ __forceinline__ void write_row(unsigned char* stage, int row, int e, 
     }
 }
 
+// Elements [a, b) of a 16-byte piece of V, in the largest aligned parts: up to the middle ever larger
+// ones, then ever smaller.
+template <int V, int ESZ>
+__device__ __forceinline__ void store_part(unsigned char* dst, const unsigned char* src, int a, int b) {
+    a = a < 0 ? 0 : a;
+    b = b > V ? V : b;
+    auto part = [&](auto word, int n) {
+        using Word = decltype(word);
+        *reinterpret_cast<Word*>(dst + a * ESZ) = *reinterpret_cast<const Word*>(src + a * ESZ);
+        a += n;
+    };
+    if constexpr (ESZ == 2) {
+        if ((a & 1) && a < b) part((unsigned short)0, 1);
+        if ((a & 2) && a + 2 <= b) part(0u, 2);
+        if (a + 4 <= b) part(uint2{}, 4);
+        if (a + 2 <= b) part(0u, 2);
+        if (a < b) part((unsigned short)0, 1);
+    } else {
+        if ((a & 1) && a < b) part(0u, 1);
+        if (a + 2 <= b) part(uint2{}, 2);
+        if (a < b) part(0u, 1);
+    }
+}
+
 // What a CTA works on: one channel tile of one chunk of one sequence.
 struct Task {
     int g, ci0, d0;          // group, first channel within it, first channel
@@ -269,22 +293,24 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
                     cp16(dst + Cf::piece_off(r0 + r, g), src + (int64_t)r * L * ESZ, 16);
             }
         } else {
-            for (int i = tid; i < rows * Cf::PIECES; i += NT) {
-                const int r = i / Cf::PIECES, g = i % Cf::PIECES;
-                const unsigned char* row = base + (int64_t)r * L * ESZ;
-                const int m = skew<T>(row);
-                const int ts = tb + g * V - m;
-                if (ts < tk.t1 && ts + V > tk.t0) {
-                    const unsigned char* src = row + (int64_t)ts * ESZ;
-                    unsigned char* dst = sb + Cf::piece_off(r0 + r, g);
-                    if (src >= lo) {
-                        const int64_t left = hi - src;
-                        cp16(ssm::smem_u32(dst), src, left < 16 ? (int)left : 16);
-                    } else {
-                        for (int e = 0; e < V; ++e)
-                            if (src + e * ESZ >= lo && src + e * ESZ < hi)
-                                *reinterpret_cast<T*>(dst + e * ESZ) = *reinterpret_cast<const T*>(src + e * ESZ);
-                    }
+            // eight lanes a row, those past its pieces idle; rows eight apart are alike on the grid
+            static_assert(Cf::PIECES <= 8 && 8 * Cf::ESZ % 16 == 0, "a thread's rows have one skew");
+            const int g = tid & 7, r1 = tid >> 3;
+            if (g >= Cf::PIECES) return;
+            const unsigned char* src = base + (int64_t)r1 * L * ESZ;
+            const int ts = tb + g * V - skew<T>(src);
+            if (ts >= tk.t1 || ts + V <= tk.t0) return;
+            src += (int64_t)ts * ESZ;
+            unsigned char* dst = sb + Cf::piece_off(r0 + r1, g);
+            const int64_t step = (int64_t)(NT / 8) * L * ESZ;
+            for (int r = r1; r < rows; r += NT / 8, src += step, dst += NT / 8 * Cf::PITCH) {
+                if (src >= lo) {
+                    const int64_t left = hi - src;
+                    cp16(ssm::smem_u32(dst), src, left < 16 ? (int)left : 16);
+                } else {
+                    for (int e = 0; e < V; ++e)
+                        if (src + e * ESZ >= lo && src + e * ESZ < hi)
+                            *reinterpret_cast<T*>(dst + e * ESZ) = *reinterpret_cast<const T*>(src + e * ESZ);
                 }
             }
         }
@@ -554,9 +580,7 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
                 if (e0 >= lo && e0 + V <= hi) {
                     *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
                 } else {
-                    for (int e = 0; e < V; ++e)
-                        if (e0 + e >= lo && e0 + e < hi)
-                            *reinterpret_cast<T*>(dst + e * ESZ) = *reinterpret_cast<const T*>(src + e * ESZ);
+                    store_part<V, ESZ>(dst, src, lo - e0, hi - e0);
                 }
             }
         }
