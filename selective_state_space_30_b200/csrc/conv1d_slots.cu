@@ -81,8 +81,7 @@ struct PackedConv {
     int log_tx;              // 16-byte pieces of a row that a CTA covers, a power of two
     int rows_per_thread;
     int silu;
-    int w_vec;               // w is 16-byte aligned
-    int aligned;             // so is every row of x and out
+    int aligned;             // every row of x and out is 16-byte aligned
 };
 
 // The 16 bytes at p, where they lie inside [lo, hi); elements outside read as zero.
@@ -160,20 +159,8 @@ template <int PW>
 struct RowPiece {
     uint32_t xw[PW + 4];
     unsigned char* out;
-    int64_t d;
     unsigned mask, nan;
 };
-
-template <typename T, int W>
-__device__ __forceinline__ void load_taps(const PackedConv& p, int64_t d, float (&w)[W]) {
-    if (W == 4 && p.w_vec) {
-        const float4 q = __ldg(reinterpret_cast<const float4*>(p.w) + d);
-        w[0] = q.x; w[1 % W] = q.y; w[2 % W] = q.z; w[3 % W] = q.w;
-    } else {
-#pragma unroll
-        for (int k = 0; k < W; ++k) w[k] = __ldg(p.w + d * W + k);
-    }
-}
 
 template <typename T>
 __device__ __forceinline__ void store_piece(unsigned char* out, unsigned mask, unsigned nan, float* o) {
@@ -240,20 +227,21 @@ __device__ __forceinline__ void sequence_bodies(const PackedConv& p, unsigned bi
     const int64_t t0 = tile * span - V;                 // token of bit 0: a piece may start up to V-1 tokens early
     const int bits = (int)span + V;
     for (int i = threadIdx.x; i < kWords; i += kThreads) live[i] = bad[i] = 0u;
-    if (p.aligned && tx >= 32) {
-        const int per = kTapRows / 2 / ty;                        // pairs that a thread row may walk
-        const int64_t d0 = (int64_t)rt * p.rows_per_thread * ty;
-        for (int i = threadIdx.x; i < p.rows_per_thread * ty * (W + 1); i += kThreads) {
-            const int row = i / (W + 1), k = i % (W + 1);
-            const int r = row / ty, y = row % ty;                 // r-th row of thread row y
-            // a pair's second row is its first where the channels end between them
-            int64_t d = d0 + row;
-            if (d >= p.dim) d -= ty;
-            if (d < p.dim) {
-                const float v = k < W ? __ldg(p.w + d * W + k) : p.bias ? __ldg(p.bias + d) : 0.f;
-                float2* q = tap_pairs + (y * per + r / 2) * (W + 1) + k;
-                (r & 1 ? q->y : q->x) = v;
-            }
+    // The rows' taps and biases in shared memory, as pairs of the rows that are worked on together:
+    // [pair][tap, then bias] of (row, row + ty), the last of an odd count twice.  (Loaded per row they
+    // cost a third of the instructions.)
+    const int per = kTapRows / 2 / ty;                            // pairs that a thread row may walk
+    const int64_t d0 = (int64_t)rt * p.rows_per_thread * ty;
+    for (int i = threadIdx.x; i < p.rows_per_thread * ty * (W + 1); i += kThreads) {
+        const int row = i / (W + 1), k = i % (W + 1);
+        const int r = row / ty, y = row % ty;                     // r-th row of thread row y
+        // a pair's second row is its first where the channels end between them
+        int64_t d = d0 + row;
+        if (d >= p.dim) d -= ty;
+        if (d < p.dim) {
+            const float v = k < W ? __ldg(p.w + d * W + k) : p.bias ? __ldg(p.bias + d) : 0.f;
+            float2* q = tap_pairs + (y * per + r / 2) * (W + 1) + k;
+            (r & 1 ? q->y : q->x) = v;
         }
     }
     __syncthreads();
@@ -303,6 +291,7 @@ __device__ __forceinline__ void sequence_bodies(const PackedConv& p, unsigned bi
     const bool edge = px == 0 || lane == 0;
     const int64_t dr = (int64_t)rt * p.rows_per_thread * ty + py;
     const int64_t step = ty * row_bytes;
+    const float2* taps = tap_pairs + py * per * (W + 1);
     if (p.aligned && tx >= 32) {
         // Every row starts on the 16-byte grid, so one mask serves all rows and a warp's pieces are
         // of one row.  Lanes behind the last token and rows behind the last one repeat the last
@@ -318,10 +307,6 @@ __device__ __forceinline__ void sequence_bodies(const PackedConv& p, unsigned bi
         if (__all_sync(0xffffffffu, mask == 0u)) return;
         if (t > p.total - V) t = p.total - V;
         const bool past = t > 0;
-        // The rows' taps and biases in shared memory, as pairs of the rows that are worked on
-        // together: [pair][tap, then bias] of (row, row + ty), the last of an odd count twice.
-        // (Loaded per row they cost a third of the instructions.)
-        const float2* taps = tap_pairs + py * (kTapRows / 2 / ty) * (W + 1);
         auto rows_of = [&](auto all_written) {
             const unsigned char* xp = lo + dr * row_bytes + t * ES;
             unsigned char* op = static_cast<unsigned char*>(p.out) + dr * row_bytes + t * ES;
@@ -423,7 +408,6 @@ __device__ __forceinline__ void sequence_bodies(const PackedConv& p, unsigned bi
         q.mask = row_ok ? __funnelshift_r(live[bit >> 5], live[(bit >> 5) + 1], bit & 31) & sel : 0u;
         q.nan = any_bad ? __funnelshift_r(bad[bit >> 5], bad[(bit >> 5) + 1], bit & 31) & q.mask : 0u;
         q.out = orow + t * ES;
-        q.d = row_ok ? d : 0;
         const unsigned char* xp = x0 + i * step + t * ES;
         uint32_t(&xw)[PW + 4] = q.xw;
         xw[PW] = piece[r].x; xw[PW + 1] = piece[r].y; xw[PW + 2] = piece[r].z; xw[PW + 3] = piece[r].w;
@@ -442,14 +426,11 @@ __device__ __forceinline__ void sequence_bodies(const PackedConv& p, unsigned bi
             }
         }
         if ((r & 1) && (rp[0].mask | rp[1].mask) != 0u) {
-            float wa[W], wb[W], o0[V], o1[V];
-            ssm::pair_t w[W];
-            load_taps<T, W>(p, rp[0].d, wa);
-            load_taps<T, W>(p, rp[1].d, wb);
+            float o0[V], o1[V];
+            ssm::pair_t w[W + 1];
 #pragma unroll
-            for (int k = 0; k < W; ++k) w[k] = ssm::pk(wa[k], wb[k]);
-            const ssm::pair_t bias = p.bias ? ssm::pk(__ldg(p.bias + rp[0].d), __ldg(p.bias + rp[1].d)) : ssm::pk(0.f);
-            conv_pieces<T, W, PW, SILU>(rp[0].xw, rp[1].xw, w, bias, o0, o1);
+            for (int k = 0; k <= W; ++k) w[k] = *reinterpret_cast<const ssm::pair_t*>(taps + (i >> 1) * (W + 1) + k);
+            conv_pieces<T, W, PW, SILU>(rp[0].xw, rp[1].xw, w, w[W], o0, o1);
             store_piece<T>(rp[0].out, rp[0].mask, rp[0].nan, o0);
             store_piece<T>(rp[1].out, rp[1].mask, rp[1].nan, o1);
         }
@@ -642,7 +623,6 @@ extern "C" int ssm_causal_conv1d_packed_fwd(int64_t dim, int64_t total, int64_t 
     p.cu = cu_seqlens; p.slots = slots; p.has_state = has_state;
     p.dim = dim; p.total = total; p.n_seq = n_seq; p.n_slots = n_slots; p.slot_stride = slot_stride;
     p.silu = silu ? 1 : 0;
-    p.w_vec = aligned_to(w, 16);
     p.aligned = total * (int64_t)esz % 16 == 0 && aligned_to(x, 16) && aligned_to(out, 16);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return io_dtype == SSM_BF16 ? launch_packed_t<__nv_bfloat16>(p, width, s) : launch_packed_t<float>(p, width, s);
