@@ -51,7 +51,7 @@
 #include "pair.cuh"
 #include "scan_packed.cuh"
 #include "ssd_packed.h"
-#include "tcgen05.cuh"
+#include "tcgen05_tmem.cuh"
 
 namespace ssm {
 namespace packed {
