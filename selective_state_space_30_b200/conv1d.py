@@ -52,5 +52,8 @@ def _causal_conv1d_function():
 
 
 def causal_conv1d_fn(x, w, bias=None, silu: bool = True):
-    """The convolution as a differentiable torch operation; its backward runs ssm_causal_conv1d_bwd."""
+    """The convolution as a differentiable torch operation; its backward runs ssm_causal_conv1d_bwd.
+
+    In a CUDA graph, capture the forward and its backward together, once the results of eager calls on the
+    same leaves are gone: torch ties a leaf's accumulation to the stream that first used it."""
     return _causal_conv1d_function().apply(x, w, bias, silu)

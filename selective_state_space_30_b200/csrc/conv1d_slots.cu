@@ -8,11 +8,13 @@
 // A sequence's first W-1 tokens take their earlier inputs from its slot (or zero), and its last
 // W-1 inputs replace the slot's.  HBM-bound: every input is read and every output written once.
 //
-// Measured on one B200, bf16, width 4: 32768 tokens in 32 prompts x 4096 channels 130 us (4.2 TB/s;
+// Measured on one B200, bf16, width 4: 32768 tokens in 32 prompts x 4096 channels 123 us (4.4 TB/s;
 // a copy through the same loop, width 1 without silu, 95 us), of which the prompts' first tokens are
-// 8 us; one token of 4 rows x 1536 channels 3.4 us in a graph.  Between them and the HBM time (82 us)
+// 8 us; 1013 tokens in 7 prompts x 1536 channels 7.6 us, one token of 4 rows x 1536 channels 2.8 us in a
+// graph.  Between them and the HBM time (82 us)
 // stand silu's two MUFU operations per output (60 us of that pipe) and the issue of the rest (110
-// instructions per 8 outputs).  64 registers (four CTAs an SM) 130 us, 80 registers 142.
+// instructions per 8 outputs).  With three CTAs an SM (80 registers) it took 142 us against 130 of four; inputs
+// asked for ahead of the mask changed nothing there and cost 0.6 us of the 7.6.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -183,7 +185,8 @@ __device__ __forceinline__ void store_piece(unsigned char* out, unsigned mask, u
 // The outputs of two rows' pieces.  The rows are the two halves of every f32x2 operation: a value
 // then sits in one register pair for all taps, where pairs of neighbouring tokens would need a
 // copy of it for every other tap (170 -> 163 us for 32768 tokens x 4096 channels in bf16; with the taps in shared
-// memory and silu decided at compile time 142, with four CTAs an SM 130).
+// memory and silu decided at compile time 142, with four CTAs an SM 130, with the taps of all rows
+// there, which shortens the code, 123).
 template <typename T, int W, int PW, bool SILU>
 __device__ __forceinline__ void conv_pieces(const uint32_t (&x0)[PW + 4], const uint32_t (&x1)[PW + 4],
                                             const ssm::pair_t* w, ssm::pair_t bias, float* o0, float* o1) {
