@@ -10,11 +10,11 @@
 //
 // Measured on one B200, bf16, width 4: 32768 tokens in 32 prompts x 4096 channels 123 us (4.4 TB/s;
 // a copy through the same loop, width 1 without silu, 95 us), of which the prompts' first tokens are
-// 8 us; 1013 tokens in 7 prompts x 1536 channels 7.6 us, one token of 4 rows x 1536 channels 2.8 us in a
+// 8 us; 1013 tokens in 7 prompts x 1536 channels 6.2 us, one token of 4 rows x 1536 channels 2.8 us in a
 // graph.  Between them and the HBM time (82 us)
 // stand silu's two MUFU operations per output (60 us of that pipe) and the issue of the rest (110
 // instructions per 8 outputs).  With three CTAs an SM (80 registers) it took 142 us against 130 of four; inputs
-// asked for ahead of the mask changed nothing there and cost 0.6 us of the 7.6.
+// asked for ahead of the mask changed nothing there and made the small call 0.6 us longer.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -372,7 +372,7 @@ __device__ __forceinline__ void sequence_bodies(const PackedConv& p, unsigned bi
     // pieces follow out's 16-byte grid; where x's differs the inputs are read by elements.  Every
     // lane runs every row (shuffles); rows past the last read nothing.  Several rows' pieces are
     // loaded before the first is used.
-    constexpr int U = 4;
+    constexpr int U = 2;
     for (int i0 = 0; i0 < p.rows_per_thread; i0 += U) {
       uint4 piece[U];
 #pragma unroll
@@ -460,8 +460,9 @@ int launch_packed(PackedConv p, cudaStream_t s) {
     while (p.log_tx < 7 && 1 << p.log_tx < pieces) ++p.log_tx;
     const int tx = 1 << p.log_tx, ty = kThreads / tx;
     const int64_t tt = p.total > 0 ? (pieces + tx - 1) / tx : 0;
-    // enough rows per CTA to carry the making of the mask, as long as 8 CTAs per SM remain
-    int rows = 4;
+    // enough rows per CTA to carry the making of the mask, as long as 8 CTAs per SM remain; two at least,
+    // which work together (1013 tokens x 1536 channels 6.2 us, with four 7.6)
+    int rows = 2;
     while (rows * ty < kTapRows && rows < 64 && tt * ((p.dim + ty - 1) / ty) / (2 * rows) >= 148 * 8) rows *= 2;
     p.rows_per_thread = rows;
     const int64_t rtiles = (p.dim + (int64_t)ty * rows - 1) / ((int64_t)ty * rows);

@@ -8,8 +8,8 @@
 // Every source is read before any destination is written, so swaps and chains need no order: a
 // CTA takes the same slice of bytes of every pair, stages all of them in shared memory, and
 // writes them after a barrier; no other CTA touches that slice.  HBM-bound: 64 moves and 32 clears of
-// 24 KB slots in 48 layers 36.6 us (5.2 TB/s of the 189 MB they cannot do without), a fork of one 96 KB
-// slot into 8 in 24 layers 6.5 us in a graph; 96 KB staged per CTA instead of 32 takes 55 us.
+// 24 KB slots in 48 layers 36.0 us (5.2 TB/s of the 189 MB they cannot do without), a fork of one 96 KB
+// slot into 8 in 24 layers 6.4 us in a graph; 96 KB staged per CTA instead of 32 takes 55 us.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kThreads) slots_copy_kernel(const CopyParams p
     const int first = q < n ? threadIdx.x / lanes : p.n_pairs, step = kThreads / lanes;
     base += q * 16;
     uint4* mine = reinterpret_cast<uint4*>(stage) + q;
-    for (int pr = first; pr < p.n_pairs; pr += step) {
+    auto read = [&](int pr) {
         const int s = __ldg(p.src + pr);
         uint4* to = mine + pr * (pitch / 16);
         if (s >= 0 && s < p.n_slots)
@@ -58,14 +58,30 @@ __global__ void __launch_bounds__(kThreads) slots_copy_kernel(const CopyParams p
                          : "memory");
         else
             *to = make_uint4(0u, 0u, 0u, 0u);
+        return s < p.n_slots;
+    };
+    auto write = [&](int pr, int d) {
+        if (d >= 0 && d < p.n_slots) *reinterpret_cast<uint4*>(base + d * p.slot_stride) = *(mine + pr * (pitch / 16));
+    };
+    // the first pairs' destinations are read beside their sources, not behind the barrier
+    constexpr int kKept = 4;
+    int to[kKept];
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+        const int pr = first + k * step;
+        to[k] = -1;
+        if (pr < p.n_pairs) {
+            const int d = __ldg(p.dst + pr);
+            if (read(pr)) to[k] = d;
+        }
     }
+    for (int pr = first + kKept * step; pr < p.n_pairs; pr += step) read(pr);
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    for (int pr = first; pr < p.n_pairs; pr += step) {
-        const int s = __ldg(p.src + pr), d = __ldg(p.dst + pr);
-        if (d >= 0 && d < p.n_slots && s < p.n_slots)
-            *reinterpret_cast<uint4*>(base + d * p.slot_stride) = *(mine + pr * (pitch / 16));
-    }
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) write(first + k * step, to[k]);
+    for (int pr = first + kKept * step; pr < p.n_pairs; pr += step)
+        write(pr, __ldg(p.src + pr) < p.n_slots ? __ldg(p.dst + pr) : -1);
 }
 
 // Any alignment.  The source's 16-byte pieces are staged as they lie; the destination's pieces
