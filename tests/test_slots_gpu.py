@@ -303,6 +303,34 @@ def test_scan_packed_cut_sequences(ssm, case):
     assert torch.equal(again, states) and torch.equal(out2, out)
 
 
+@pytest.mark.parametrize("z", [True, False])
+@pytest.mark.parametrize("lens,head,tail,hint", [
+    ([32], 0, 0, 0), ([40], 0, 0, 0), ([33, 31], 0, 0, 0), ([128], 0, 0, 0), ([127, 129], 0, 0, 0), ([300, 1, 211], 0, 0, 1),
+    ([7, 260, 250], 5, 6, 1), ([1024], 0, 0, 0), ([900, 3], 1, 8, 0)])
+def test_scan_packed_tensor_cores_on_the_grid(ssm, lens, head, tail, hint, z):
+    """Rows on the 16-byte grid, whose blocks come and go as boxes: buffers shorter than a box, sequences that
+    start and end inside one, neighbours and padding that hold NaN, cut sequences, no gate."""
+    gen = torch.Generator().manual_seed(28)
+    dim, N = 128, 128
+    cu, total, bounds = packing(lens, head, tail)
+    assert total % 8 == 0 and total >= 32 * len(lens)
+    p = _scan_inputs(gen, total, dim, 2, 2, N, "bf16", z=z)
+    states, out = rnd(gen, len(lens) + 1, dim, N), rnd(gen, dim, total, dtype="bf16")
+    slots, has = [i + 1 for i in range(len(lens))], [i % 2 for i in range(len(lens))]
+    if len(lens) > 2:
+        slots[1] = -1
+    ref, err, ref_pool, pool_err = sp.scan_packed(_plain(p), bounds, slots, has, f64(states), f64(out), chunk=128, tensor=True)
+    skip = [(0, head), (bounds[-1][1], total)] + [b for b, s in zip(bounds, slots) if s < 0]
+    for k in ("u", "delta", "B", "C", "z"):
+        if p[k] is not None:
+            for lo, hi in skip:
+                p[k][..., lo:hi] = float("nan")
+    got = _call(ssm, p, i32(cu), states, out, slots=i32(slots), has_state=torch.tensor(has, dtype=torch.uint8).cuda(),
+                max_seqlen=hint)
+    sp.check(f64(got), ref, err, "bf16", "out")
+    sp.check(f64(states), ref_pool, pool_err, "f32", "states")
+
+
 @pytest.mark.parametrize("dim,heads,N,head", [(32, 32, 16, 0), (64, 1, 128, 0), (128, 2, 128, 5)])
 def test_scan_packed_steps_of_either_sign(ssm, dim, heads, N, head):
     """Without softplus a step is what delta and the bias add up to: negative ones let the state grow."""
