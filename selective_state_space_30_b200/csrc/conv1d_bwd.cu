@@ -14,8 +14,8 @@
 //
 // Measured on one B200: 8 x 1536 x 2048 bf16, width 4, 43 us (3.5 TB/s; 23 us of HBM time), issue
 // 59 % busy with 14 of 64 warps an SM (128 registers hold two rows and the loads ahead); three CTAs an
-// SM with 84 registers 61 us.  2 x 768 x 1021 fp32 8.5 us in a graph, 9.6 with partials and a second
-// kernel (10.2 and 13.5 us a call).
+// SM with 84 registers 61 us.  2 x 768 x 1021 fp32 6.9 us in a graph with four warps a pair of channels,
+// 8.7 with eight, 9.6 with partials and a second kernel.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -155,6 +155,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) conv1d_bwd_kernel(const ConvBw
     constexpr int V = 16 / sizeof(T), H = W - 1, PW = Piece<T>::PW;
     __shared__ float sums[kWarps][2 * (W + 1)];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int warps = blockDim.x / 32;
     const int64_t d0 = blockIdx.x / p.n_split * 2, split = blockIdx.x % p.n_split, L = p.seqlen;
     const bool both = d0 + 1 < p.dim;                 // an odd last channel pairs with itself and writes once
     const int64_t d[2] = {d0, both ? d0 + 1 : d0};
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) conv1d_bwd_kernel(const ConvBw
     }
     const float2 bias = p.bias ? make_float2(__ldg(p.bias + d[0]), __ldg(p.bias + d[1])) : ssm::dup2(0.f);
     // the pair's stretches, one after the other over the warps of its CTAs
-    for (int64_t item = split * kWarps + warp; item < p.batch * p.n_seg; item += p.n_split * kWarps) {
+    for (int64_t item = split * warps + warp; item < p.batch * p.n_seg; item += p.n_split * warps) {
         const int64_t seg = item % p.n_seg, b = item / p.n_seg;
         const T *x[2], *go[2];
         T* dx[2];
@@ -325,8 +326,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) conv1d_bwd_kernel(const ConvBw
     __syncthreads();
     if (threadIdx.x < (both ? 2 : 1) * (W + 1)) {
         float a = sums[0][threadIdx.x];
-#pragma unroll
-        for (int q = 1; q < kWarps; ++q) a += sums[q][threadIdx.x];
+        for (int q = 1; q < warps; ++q) a += sums[q][threadIdx.x];
         const int r = threadIdx.x / (W + 1), k = threadIdx.x % (W + 1);
         if (p.n_split > 1) p.part[(split * p.dim + d0 + r) * (W + 1) + k] = a;
         else if (k < W) p.dw[(d0 + r) * W + k] = a;
@@ -356,24 +356,44 @@ __global__ void __launch_bounds__(256) conv1d_bwd_sum_kernel(const float* part, 
 
 struct Plan {
     int64_t tiles_per_seg, n_seg, n_split;
+    int warps;              // of a CTA
 };
 
-// A pair of channels is one CTA's where there are enough pairs for two CTAs on each of 148 SMs: its
-// sums then need no second kernel.  Fewer pairs are split over several CTAs, and rows into stretches
-// as far as the CTAs' warps need them.  The shape alone decides, so the sums' order is the shape's.
+// A pair of channels is one CTA's where there are enough pairs for two CTAs on each of 148 SMs: its sums
+// then need no second kernel.  The CTA has eight warps or four, whichever walk fewer tiles after one
+// another (2 x 768 x 1021 fp32, 384 pairs: four warps in one round 6.9 us, eight in two 8.7; 8 x 1536 x
+// 2048 bf16: three rounds of 8 tiles against two of 16).  Fewer pairs are split over several CTAs, and
+// rows into stretches as far as the CTAs' warps need them.  The shape alone decides, so the sums' order
+// is the shape's.
 Plan plan_of(int64_t batch, int64_t dim, int64_t seqlen, int io_dtype) {
-    const int64_t V = io_dtype == SSM_BF16 ? 8 : 4, pairs = (dim + 1) / 2;
+    const int64_t V = io_dtype == SSM_BF16 ? 8 : 4, pairs = (dim + 1) / 2, slots = 148 * 2;
     const int64_t tiles = (seqlen + V - 1 + 32 * V - 1) / (32 * V);
-    Plan q{1, 1, 1};
+    Plan q{1, 1, 1, kWarps};
     if (batch <= 0 || seqlen <= 0) return q;
-    const int64_t ctas = (148 * 2 + pairs - 1) / pairs;
-    int64_t seg = (ctas * kWarps + batch - 1) / batch;
-    if (seg > tiles) seg = tiles;
-    q.tiles_per_seg = (tiles + seg - 1) / seg;
-    q.n_seg = (tiles + q.tiles_per_seg - 1) / q.tiles_per_seg;
-    const int64_t most = (batch * q.n_seg + kWarps - 1) / kWarps;
-    q.n_split = ctas < most ? ctas : most;
-    return q;
+    auto stretches = [&](int64_t warps) {
+        Plan r = q;
+        int64_t seg = (warps + batch - 1) / batch;
+        if (seg > tiles) seg = tiles;
+        r.tiles_per_seg = (tiles + seg - 1) / seg;
+        r.n_seg = (tiles + r.tiles_per_seg - 1) / r.tiles_per_seg;
+        return r;
+    };
+    if (pairs <= slots) {
+        const int64_t ctas = (slots + pairs - 1) / pairs;
+        q = stretches(ctas * kWarps);
+        const int64_t most = (batch * q.n_seg + kWarps - 1) / kWarps;
+        q.n_split = ctas < most ? ctas : most;
+        return q;
+    }
+    auto walked = [&](const Plan& r) {
+        const int64_t at_once = slots * kWarps / r.warps, rounds = (pairs + at_once - 1) / at_once;
+        // (a stretch's start costs about a tile)
+        return rounds * ((batch * r.n_seg + r.warps - 1) / r.warps) * (r.tiles_per_seg + 1);
+    };
+    const Plan whole = stretches(kWarps);
+    Plan half = stretches(kWarps / 2);
+    half.warps = kWarps / 2;
+    return walked(half) < walked(whole) ? half : whole;
 }
 
 bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -389,24 +409,24 @@ int check_shape(int64_t batch, int64_t dim, int64_t seqlen, int32_t width, int32
 }
 
 template <typename T, int W>
-int launch(const ConvBwd& p, bool aligned, cudaStream_t s) {
+int launch(const ConvBwd& p, int warps, bool aligned, cudaStream_t s) {
     const int64_t ctas = (p.dim + 1) / 2 * p.n_split;
     if (ctas > 0x7FFFFFFF) return SSM_ERR_UNSUPPORTED;
     const unsigned g = (unsigned)ctas;
-    if (aligned && p.silu) conv1d_bwd_kernel<T, W, true, true><<<g, 32 * kWarps, 0, s>>>(p);
-    else if (aligned) conv1d_bwd_kernel<T, W, true, false><<<g, 32 * kWarps, 0, s>>>(p);
-    else if (p.silu) conv1d_bwd_kernel<T, W, false, true><<<g, 32 * kWarps, 0, s>>>(p);
-    else conv1d_bwd_kernel<T, W, false, false><<<g, 32 * kWarps, 0, s>>>(p);
+    if (aligned && p.silu) conv1d_bwd_kernel<T, W, true, true><<<g, 32 * warps, 0, s>>>(p);
+    else if (aligned) conv1d_bwd_kernel<T, W, true, false><<<g, 32 * warps, 0, s>>>(p);
+    else if (p.silu) conv1d_bwd_kernel<T, W, false, true><<<g, 32 * warps, 0, s>>>(p);
+    else conv1d_bwd_kernel<T, W, false, false><<<g, 32 * warps, 0, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
 }
 
 template <typename T>
-int launch_t(const ConvBwd& p, int width, bool aligned, cudaStream_t s) {
+int launch_t(const ConvBwd& p, int warps, int width, bool aligned, cudaStream_t s) {
     switch (width) {
-        case 1: return launch<T, 1>(p, aligned, s);
-        case 2: return launch<T, 2>(p, aligned, s);
-        case 3: return launch<T, 3>(p, aligned, s);
-        case 4: return launch<T, 4>(p, aligned, s);
+        case 1: return launch<T, 1>(p, warps, aligned, s);
+        case 2: return launch<T, 2>(p, warps, aligned, s);
+        case 3: return launch<T, 3>(p, warps, aligned, s);
+        case 4: return launch<T, 4>(p, warps, aligned, s);
         default: return SSM_ERR_UNSUPPORTED;
     }
 }
@@ -447,7 +467,7 @@ extern "C" int ssm_causal_conv1d_bwd(int64_t batch, int64_t dim, int64_t seqlen,
     p.tiles_per_seg = q.tiles_per_seg; p.n_seg = q.n_seg; p.n_split = q.n_split;
     p.silu = silu ? 1 : 0;
     const bool aligned = seqlen * (int64_t)esz % 16 == 0 && aligned_to(x, 16) && aligned_to(dout, 16) && aligned_to(dx, 16);
-    const int r = io_dtype == SSM_BF16 ? launch_t<__nv_bfloat16>(p, width, aligned, s) : launch_t<float>(p, width, aligned, s);
+    const int r = io_dtype == SSM_BF16 ? launch_t<__nv_bfloat16>(p, q.warps, width, aligned, s) : launch_t<float>(p, q.warps, width, aligned, s);
     if (r != SSM_OK || q.n_split == 1) return r;
     const int64_t n = dim * (width + 1);
     conv1d_bwd_sum_kernel<<<(unsigned)((n + 31) / 32), dim3(32, 8), 0, s>>>(p.part, q.n_split, dim, width, dw, dbias);

@@ -201,9 +201,10 @@ def conv_bwd(x, w, bias, dout, use_silu):
     dxerr += W * U * dxmag
     dw = np.stack([(dv * xp[:, :, k:k + L]).sum((0, 2)) for k in range(W)], 1)
     n = Bt * L
-    # additions that a value takes part in: a lane's tokens of its share of the batch (an eighth, rounded up), its
-    # warp's lanes, eight warps, and up to 296 partials by eight threads each
-    depth = min(n, (Bt // 8 + 1) * (L // 32 + 16) + 5 + 8 + 37 + 8)
+    # additions that a value takes part in: a lane's tokens of its share of the batch (a quarter, rounded up; of a
+    # row of t tiles of at most 256 tokens up to t + 2, eight tokens a lane each), its warp's lanes, eight warps,
+    # and up to 296 partials by eight threads each
+    depth = min(n, (Bt // 4 + 1) * (L // 32 + 32) + 5 + 8 + 37 + 8)
     dwerr = np.stack([(dverr * np.abs(xp[:, :, k:k + L])).sum((0, 2)) +
                       depth * U * np.abs(dv * xp[:, :, k:k + L]).sum((0, 2)) for k in range(W)], 1)
     db = dv.sum((0, 2))
