@@ -532,8 +532,7 @@ int ssm_state_slots_copy(void* pool, int64_t n_layers, int64_t n_slots, int64_t 
  * dx is (batch, dim, seqlen) in io_dtype; dw (dim, width) and dbias (dim, nullable: not computed)
  * are fp32, summed in a fixed order.  bias is the forward's (NULL: zero).  `workspace` (device,
  * 4-byte aligned, caller-owned) has at least ssm_causal_conv1d_bwd_workspace_size bytes (0 bytes,
- * with one kernel instead of two, where there are channels enough to fill the GPU: it may then be
- * NULL); one workspace must not serve two calls at once.  Kernels on `stream`; the call allocates
+ * with one kernel instead of two, but for few channels with long rows: it may then be NULL); one workspace must not serve two calls at once.  Kernels on `stream`; the call allocates
  * nothing.  dx must not overlap x or dout.  width is 1 to 4, else SSM_ERR_UNSUPPORTED;
  * SSM_ERR_INVALID_ARG for a bad shape or dtype, a pointer off its element's alignment, a
  * workspace that is too small, or a NULL w, dw, x, dout or dx.

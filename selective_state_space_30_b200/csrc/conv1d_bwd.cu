@@ -359,41 +359,35 @@ struct Plan {
     int warps;              // of a CTA
 };
 
-// A pair of channels is one CTA's where there are enough pairs for two CTAs on each of 148 SMs: its sums
-// then need no second kernel.  The CTA has eight warps or four, whichever walk fewer tiles after one
-// another (2 x 768 x 1021 fp32, 384 pairs: four warps in one round 6.9 us, eight in two 8.7; 8 x 1536 x
-// 2048 bf16: three rounds of 8 tiles against two of 16).  Fewer pairs are split over several CTAs, and
-// rows into stretches as far as the CTAs' warps need them.  The shape alone decides, so the sums' order
-// is the shape's.
+// A pair of channels is one CTA's, whose sums then need no second kernel, of eight warps or of four,
+// whichever walk fewer tiles after one another (2 x 768 x 1021 fp32, 384 pairs: four warps in one round
+// 6.9 us, eight in two 8.7; 8 x 1536 x 2048 bf16: three rounds of 8 tiles against two of 16).  Where few
+// pairs leave SMs idle over long rows a pair is split over several CTAs: the second kernel costs about four
+// tiles' time (4 x 280 x 4096: fp32, 18 tiles against 10, 23 us whole and 19 split; bf16, 10 against 6, 12.3
+// and 13.7).  Rows are cut into stretches as far as the warps need them.  The shape alone decides, so the
+// sums' order is the shape's.
 Plan plan_of(int64_t batch, int64_t dim, int64_t seqlen, int io_dtype) {
-    const int64_t V = io_dtype == SSM_BF16 ? 8 : 4, pairs = (dim + 1) / 2, slots = 148 * 2;
+    const int64_t V = io_dtype == SSM_BF16 ? 8 : 4, pairs = (dim + 1) / 2, slots = 148 * 2;   // two CTAs of eight warps an SM
     const int64_t tiles = (seqlen + V - 1 + 32 * V - 1) / (32 * V);
-    Plan q{1, 1, 1, kWarps};
-    if (batch <= 0 || seqlen <= 0) return q;
-    auto stretches = [&](int64_t warps) {
-        Plan r = q;
-        int64_t seg = (warps + batch - 1) / batch;
+    if (batch <= 0 || seqlen <= 0) return {1, 1, 1, kWarps};
+    auto plan = [&](int warps, int64_t ctas) {
+        int64_t seg = (warps * ctas + batch - 1) / batch;
         if (seg > tiles) seg = tiles;
-        r.tiles_per_seg = (tiles + seg - 1) / seg;
+        Plan r{(tiles + seg - 1) / seg, 1, 1, warps};
         r.n_seg = (tiles + r.tiles_per_seg - 1) / r.tiles_per_seg;
+        const int64_t most = (batch * r.n_seg + warps - 1) / warps;
+        r.n_split = ctas < most ? ctas : most;
         return r;
     };
-    if (pairs <= slots) {
-        const int64_t ctas = (slots + pairs - 1) / pairs;
-        q = stretches(ctas * kWarps);
-        const int64_t most = (batch * q.n_seg + kWarps - 1) / kWarps;
-        q.n_split = ctas < most ? ctas : most;
-        return q;
-    }
     auto walked = [&](const Plan& r) {
-        const int64_t at_once = slots * kWarps / r.warps, rounds = (pairs + at_once - 1) / at_once;
-        // (a stretch's start costs about a tile)
-        return rounds * ((batch * r.n_seg + r.warps - 1) / r.warps) * (r.tiles_per_seg + 1);
+        const int64_t at_once = slots * kWarps / r.warps, rounds = (pairs * r.n_split + at_once - 1) / at_once;
+        const int64_t warps = r.warps * r.n_split;
+        return rounds * ((batch * r.n_seg + warps - 1) / warps) * (r.tiles_per_seg + 1);   // (a start costs about a tile)
     };
-    const Plan whole = stretches(kWarps);
-    Plan half = stretches(kWarps / 2);
-    half.warps = kWarps / 2;
-    return walked(half) < walked(whole) ? half : whole;
+    const Plan eight = plan(kWarps, 1), four = plan(kWarps / 2, 1);
+    const Plan one = walked(four) < walked(eight) ? four : eight;
+    const Plan split = plan(kWarps, slots / pairs > 1 ? slots / pairs : 1);
+    return walked(one) - walked(split) > 4 ? split : one;
 }
 
 bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

@@ -23,6 +23,8 @@ CASES = [
     (1, 3, 5000, 4, "f32", True, True, False),       # stretches
     (1, 2, 8195, 4, "bf16", True, True, True),
     (40, 16, 130, 4, "bf16", True, False, False),    # many partials
+    (1, 4, 20000, 4, "f32", True, True, False),
+    (1, 3, 40001, 3, "bf16", True, True, True),
     (2, 768, 301, 4, "f32", True, True, False),      # four warps a pair of channels
     (2, 601, 301, 4, "f32", True, True, True),       # and a last pair of one channel
     (3, 605, 900, 2, "bf16", True, False, False),
