@@ -389,7 +389,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
         if (from_slot) H[k] = p.states[(int64_t)tk.slot * p.slot_stride + d * kN + row];
         if (from_before) H[k] = __ldcg(p.ws_h + ((int64_t)(tk.chunk_id - tk.k) * p.dim + d) * kN + row);
         if constexpr (!LOCAL)
-            if ((k & 1) == 0) Dv[k / 2] = p.D ? __ldg(p.D + d + (lane & 1)) : 0.f;
+            if ((k & 4) == 0) Dv[k / 8 * 4 + (k & 3)] = p.D ? __ldg(p.D + d + 4 * (lane & 1)) : 0.f;
     }
     if (from_before) {
         // join the chunks before: the first holds a state, the later ones (decay, state from zero)
@@ -613,19 +613,20 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
             const unsigned char* xt = sX + (row >> 6) * 8192;
             unsigned char* zt = sZ + (row >> 6) * 8192;
             // neighbouring lanes trade a channel, so that each has two steps of one: whole words of
-            // x, z and the outputs
+            // x, z and the outputs (channels four apart, whose rows the swizzle puts into different banks)
             const bool odd = lane & 1;
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-                float v0 = __uint_as_float(yv[k]), v1 = __uint_as_float(yv[k + 1]);
+            for (int i = 0; i < 8; ++i) {
+                const int k = i / 4 * 8 + i % 4;
+                float v0 = __uint_as_float(yv[k]), v1 = __uint_as_float(yv[k + 4]);
                 if (with_state) {
                     v0 = fmaf(e, __uint_as_float(cv[k]), v0);
-                    v1 = fmaf(e, __uint_as_float(cv[k + 1]), v1);
+                    v1 = fmaf(e, __uint_as_float(cv[k + 4]), v1);
                 }
                 const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-                const uint32_t at = tc::sw128_off(p0 + k + (odd ? 1u : 0u), row & 62u);
+                const uint32_t at = tc::sw128_off(p0 + k + (odd ? 4u : 0u), row & 62u);
                 const uint32_t xw = *reinterpret_cast<const uint32_t*>(xt + at);
-                pair_t v = pfma(pk(Dv[k / 2]), pk(__uint_as_float(xw << 16), __uint_as_float(xw & 0xFFFF0000u)),
+                pair_t v = pfma(pk(Dv[i]), pk(__uint_as_float(xw << 16), __uint_as_float(xw & 0xFFFF0000u)),
                                 odd ? pk(got, v1) : pk(v0, got));
                 uint32_t* zo = reinterpret_cast<uint32_t*>(zt + at);
                 if (gate) {
