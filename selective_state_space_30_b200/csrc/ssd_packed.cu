@@ -27,13 +27,13 @@
 // Bound: the threads' phases, chains of few instructions over 16 warps, one CTA per SM.  Of a block's
 // 4.8 us about 0.4 go into waiting for G, 1.2 into M, 1.4 into the state and X', 1.3 into the outputs
 // (half of that silu's two MUFU operations) and 0.3 into the copies' orders.  Measured on one B200: 6 ragged
-// prompts of 4096 tokens, 32 heads 74 us (the scan kernel 400), one prompt of 8192 tokens, 16 heads 83
+// prompts of 4096 tokens, 32 heads 73 us (the scan kernel 400), one prompt of 8192 tokens, 16 heads 83
 // in chunks.  Steps, for the first of these: values in f32x2 pairs, log2 dt folded into the exponent and whole
 // words of x, z and the outputs in the epilogue 120 us; M in tensor memory instead of shared memory, so
 // that S need not have left its place, 104; the terms of X' and H side by side in one product each (a product
 // of 64 columns takes as long to read its left operand as one of 192), the products asked for by a warp that
 // M leaves idle and X' under Y 87; boxes of TMA instead of the threads' copies, and what seldom
-// runs out of line 79; weights across stretches as products 78; the rule on cutting 74.
+// runs out of line 79; weights across stretches as products 78; the rule on cutting 74; epilogue rows in different banks, maps asked for early 73.
 //
 // Tiles arrive in the 128-byte swizzle that the tensor cores read, each as soon as its place is free: X a
 // block ahead in a second buffer, B and C once G, S and C H are done, z once the outputs before it
@@ -689,6 +689,13 @@ template <bool SOFTPLUS>
 __global__ void __launch_bounds__(kThreads, 1) ssd_packed_kernel(const PackedParams p, const __grid_constant__ SsdMaps maps) {
     extern __shared__ __align__(1024) unsigned char ssd_smem[];
     unsigned char* smem = ssd_smem + ((1024u - (smem_u32(ssd_smem) & 1023u)) & 1023u);
+    if (threadIdx.x == 0 && p.grid16) {
+        // the maps on their way while the CTA finds its task
+        const CUtensorMap* m[5] = {&maps.u, &maps.B, &maps.C, p.z ? &maps.z : &maps.u, &maps.out};
+#pragma unroll
+        for (int i = 0; i < 5; ++i)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m[i])) : "memory");
+    }
     const unsigned h = blockIdx.x % p.n_tiles;
     Task tk;
     tk.d0 = (int)h * kP;
