@@ -564,6 +564,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
         }
         if constexpr (!LOCAL) stage_z(c);
         stage_bc(c + 1);
+        __syncwarp();                                   // (one lane asked for the boxes)
         // ---- the state (Y runs)
         uint32_t cv[LOCAL ? 8 : 16];                    // C H
         {

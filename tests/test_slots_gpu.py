@@ -331,6 +331,46 @@ def test_scan_packed_tensor_cores_on_the_grid(ssm, lens, head, tail, hint, z):
     sp.check(f64(states), ref_pool, pool_err, "f32", "states")
 
 
+@pytest.mark.parametrize("total", [520, 523])
+def test_scan_packed_tensor_cores_replayed_and_at_once(ssm, total):
+    """One graph serves other lengths (bounds out of order among them), and calls on two streams at once, each
+    with its own pool, give what they give alone; all bit for bit."""
+    gen = torch.Generator().manual_seed(29)
+    dim, N = 128, 128
+    cu = i32([0, 300, 301, total])
+    ps = [_scan_inputs(gen, total, dim, 2, 1, N, "bf16") for _ in range(2)]
+    states, out = torch.zeros(3, dim, N, device="cuda"), torch.zeros(dim, total, device="cuda", dtype=torch.bfloat16)
+    _call(ssm, ps[0], cu, states, out, max_seqlen=100)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _call(ssm, ps[0], cu, states, out, max_seqlen=100)
+    for bounds in ([0, 300, 301, total], [0, 0, 0, 0], [5, 130, 258, 515], [0, total, total, total], [9, 5000, -3, 200]):
+        want_s, want = torch.zeros_like(states), torch.zeros_like(out)
+        _call(ssm, ps[0], i32(bounds), want_s, want, max_seqlen=100)
+        states.zero_()
+        out.zero_()
+        cu.copy_(i32(bounds))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(states, want_s), bounds
+    cu.copy_(i32([0, 300, 301, total]))
+    alone = []
+    for p in ps:
+        s = torch.zeros_like(states)
+        alone.append((_call(ssm, p, cu, s, None), s))
+    streams = [torch.cuda.Stream() for _ in ps]
+    for _ in range(5):
+        torch.cuda.synchronize()
+        both = []
+        for p, stream in zip(ps, streams):
+            with torch.cuda.stream(stream):
+                s = torch.zeros_like(states)
+                both.append((_call(ssm, p, cu, s, None), s))
+        torch.cuda.synchronize()
+        for got, want in zip(both, alone):
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 @pytest.mark.parametrize("dim,heads,N,head", [(32, 32, 16, 0), (64, 1, 128, 0), (128, 2, 128, 5)])
 def test_scan_packed_steps_of_either_sign(ssm, dim, heads, N, head):
     """Without softplus a step is what delta and the bias add up to: negative ones let the state grow."""
