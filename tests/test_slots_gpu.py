@@ -352,7 +352,10 @@ def test_scan_packed_tensor_cores_replayed_and_at_once(ssm, total):
         cu.copy_(i32(bounds))
         graph.replay()
         torch.cuda.synchronize()
-        assert torch.equal(out, want) and torch.equal(states, want_s), bounds
+        assert torch.equal(states, want_s), bounds
+        # out of order: [9, total) and [0, 200) are two sequences' tokens, and either's outputs may stay where both write
+        once = slice(200, total) if min(bounds) < 0 else slice(0, total)
+        assert torch.equal(out[:, once], want[:, once]), bounds
     cu.copy_(i32([0, 300, 301, total]))
     alone = []
     for p in ps:
