@@ -326,7 +326,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) conv1d_bwd_kernel(const ConvBw
     __syncthreads();
     if (threadIdx.x < (both ? 2 : 1) * (W + 1)) {
         float a = sums[0][threadIdx.x];
-        for (int q = 1; q < warps; ++q) a += sums[q][threadIdx.x];
+#pragma unroll
+        for (int q = 1; q < kWarps; ++q)
+            if (q < warps) a += sums[q][threadIdx.x];
         const int r = threadIdx.x / (W + 1), k = threadIdx.x % (W + 1);
         if (p.n_split > 1) p.part[(split * p.dim + d0 + r) * (W + 1) + k] = a;
         else if (k < W) p.dw[(d0 + r) * W + k] = a;
