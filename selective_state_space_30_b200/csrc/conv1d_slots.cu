@@ -238,10 +238,8 @@ __device__ __forceinline__ void sequence_bodies(const PackedConv& p, unsigned bi
     for (int i = threadIdx.x; i < p.rows_per_thread * ty * (W + 1); i += kThreads) {
         const int row = i / (W + 1), k = i % (W + 1);
         const int r = row / ty, y = row % ty;                     // r-th row of thread row y
-        // a pair's second row is its first where the channels end between them
-        int64_t d = d0 + row;
-        if (d >= p.dim) d -= ty;
-        if (d < p.dim) {
+        const int64_t d = ssm::tap_channel(d0, row, ty, p.dim);
+        if (d >= 0) {
             const float v = k < W ? __ldg(p.w + d * W + k) : p.bias ? __ldg(p.bias + d) : 0.f;
             float2* q = tap_pairs + (y * per + r / 2) * (W + 1) + k;
             (r & 1 ? q->y : q->x) = v;

@@ -1,6 +1,7 @@
 #pragma once
 // What the operators on packed prompts and on pools of state slots share: the reading of
-// cu_seqlens and of slot indices, which live on the device and so are checked there.
+// cu_seqlens and of slot indices, which live on the device and so are checked there, and index
+// arithmetic that a test on the CPU walks through.
 #include <cstdint>
 
 namespace ssm {
@@ -25,6 +26,15 @@ __device__ __forceinline__ TokenRange token_range(const int* cu, int64_t i, int6
     lo = lo < 0 ? 0 : lo > total ? total : lo;
     hi = hi < lo ? lo : hi > total ? total : hi;
     return {lo, hi};
+}
+
+// A CTA of the packed convolution works on `rows` channels from d0 on, in steps of ty, the channels of
+// two steps as one pair: the channel whose taps row `row` of it keeps, or -1.  Where the channels end
+// between the two, the second is the first once more; a first row behind the last channel has none.
+__host__ __device__ __forceinline__ int64_t tap_channel(int64_t d0, int row, int ty, int64_t dim) {
+    const int64_t d = d0 + row;
+    if (d < dim) return d;
+    return (row / ty & 1) && d - ty < dim ? d - ty : -1;
 }
 
 }  // namespace ssm

@@ -222,3 +222,67 @@ def test_plain_conv_is_the_oracles():
     o3, _, p3 = sp.conv_packed(x[:, 2:].astype(np.float64), w.astype(np.float64), b.astype(np.float64), True, [(0, 18)], [0], [1],
                                p2, np.zeros((3, 18)))
     assert np.allclose(np.concatenate([o2[:, :2], o3], 1), out, rtol=1e-13, atol=1e-15) and np.array_equal(p3, pool)
+
+
+# ------------------------------------------------- index arithmetic of the kernels, compiled for the CPU
+
+@pytest.fixture(scope="module")
+def indexes(tmp_path_factory):
+    """csrc/slots.h, whose functions read and compute indexes alone, as host code."""
+    import os
+    import subprocess
+    from selective_state_space_30_b200 import build
+    d = tmp_path_factory.mktemp("slots_h")
+    src = d / "slots_h.cpp"
+    src.write_text("""
+#define __host__
+#define __device__
+#define __forceinline__ inline
+template <typename T> T __ldg(const T* p) { return *p; }
+#include "slots.h"
+extern "C" long long tap_channel(long long d0, int row, int ty, long long dim) {
+    return ssm::tap_channel(d0, row, ty, dim);
+}
+extern "C" void token_range(const int* cu, long long i, long long total, long long* out) {
+    const ssm::TokenRange r = ssm::token_range(cu, i, total);
+    out[0] = r.lo;
+    out[1] = r.hi;
+}
+""")
+    lib = d / "slots_h.so"
+    subprocess.run([os.environ.get("CXX", "g++"), "-std=c++17", "-O1", "-fPIC", "-shared", f"-I{build.CSRC}", str(src), "-o",
+                    str(lib)], check=True)
+    so = ctypes.CDLL(str(lib))
+    so.tap_channel.restype = ctypes.c_longlong
+    so.tap_channel.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_int, ctypes.c_longlong]
+    so.token_range.argtypes = [ctypes.POINTER(ctypes.c_int), ctypes.c_longlong, ctypes.c_longlong,
+                               ctypes.POINTER(ctypes.c_longlong)]
+    return so
+
+
+def test_packed_conv_taps_stay_inside(indexes):
+    """Every channel whose taps a CTA of the packed convolution reads exists, and every pair that it computes
+    with has both: down to one channel, for every split of the threads into rows."""
+    for ty in (2, 4, 8, 16):
+        for rows in (2, 4, 16):
+            for dim in (*range(1, 3 * ty + 2), 2 * rows * ty + 1, rows * ty, rows * ty - 1):
+                for d0 in range(0, dim, rows * ty):
+                    got = [indexes.tap_channel(d0, r, ty, dim) for r in range(rows * ty)]
+                    assert all(-1 <= d < dim for d in got), (ty, rows, dim, d0)
+                    for r in range(rows * ty):
+                        if d0 + r < dim:
+                            assert got[r] == d0 + r
+                            if r // ty % 2 == 0:                       # its pair's second row
+                                assert got[r + ty] == (d0 + r + ty if d0 + r + ty < dim else d0 + r), (ty, rows, dim, d0, r)
+
+
+def test_token_ranges_are_clamped(indexes):
+    big = 2 ** 31 - 1
+    bounds = [0, 50, 20, big, -big - 1, 7, 64, 64]
+    cu = (ctypes.c_int * len(bounds))(*bounds)
+    out = (ctypes.c_longlong * 2)()
+    for total in (0, 5, 64):
+        for i in range(len(bounds) - 1):
+            indexes.token_range(cu, i, total, out)
+            lo = min(max(bounds[i], 0), total)
+            assert (out[0], out[1]) == (lo, min(max(bounds[i + 1], lo), total))
