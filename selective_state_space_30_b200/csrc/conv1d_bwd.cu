@@ -232,6 +232,16 @@ __global__ void __launch_bounds__(32 * kWarps, 2) conv1d_bwd_kernel(const ConvBw
                 next[0] = load(0, tile - 1);
                 next[1] = load(1, tile - 1);
             }
+            // tokens of the lane's pieces up to the rows' ends.  Behind an end dv is zero, and the inputs that
+            // its sums would meet there, the last ones of the row, read as zero too: an infinity or a
+            // NaN among them stays out of the taps that it does not belong to
+            int64_t left[2];
+            bool tail = false;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                left[r] = L - ((tile * 32 + lane) * V - m[r]);
+                tail = tail || L < (tile + 1) * 32 * V - m[r];
+            }
             // tokens t - 4 .. t + V - 1 of x; t .. t + V + H - 1 of dv
             float2 xv[4 + V], dv[V + H];
 #pragma unroll
@@ -243,6 +253,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) conv1d_bwd_kernel(const ConvBw
                 for (int i = 0; i < PW; ++i) {
                     bw[i] = __shfl_up_sync(0xffffffffu, xw[4 - PW + i], 1);
                     if (lane == 0) bw[i] = cur[r].before[i];
+                    if (ALIGNED && left[r] <= 0) bw[i] = 0u;
                 }
                 float xb[4], xc[V], gc[V];
                 unpack<T, 4>(bw, xb);
@@ -256,9 +267,16 @@ __global__ void __launch_bounds__(32 * kWarps, 2) conv1d_bwd_kernel(const ConvBw
                     (r ? dv[e].y : dv[e].x) = gc[e];
                 }
             }
-            const float2* xh = xv + 4 - H;                // xh[e + k] meets w[k] at token e
+            float2* xh = xv + 4 - H;                      // xh[e + k] meets w[k] at token e
 #pragma unroll
             for (int e = 0; e < V; ++e) {
+                if (!ALIGNED && tail) {
+#pragma unroll
+                    for (int k = 0; k < H; ++k) {
+                        if (e >= left[0]) xh[e + k].x = 0.f;
+                        if (e >= left[1]) xh[e + k].y = 0.f;
+                    }
+                }
                 float2 v = bias;
 #pragma unroll
                 for (int k = 0; k < W; ++k) v = ssm::fma2(w[k], xh[e + k], v);

@@ -132,3 +132,24 @@ def test_conv_bwd_no_tokens():
         x = torch.zeros(shape, dtype=IO["bf16"], device="cuda")
         g = ssm.causal_conv1d_bwd(x, torch.ones(4, 4, device="cuda"), x)
         assert g["dx"].shape == shape and not g["dw"].any() and not g["dbias"].any()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("case", [
+    (2, 40, 64, 4, "bf16", False, True, False), (2, 24, 67, 4, "bf16", False, True, False),
+    (3, 8, 96, 3, "f32", False, True, False), (1, 5, 1, 4, "bf16", False, True, False), (2, 7, 2, 4, "f32", False, False, False),
+    (2, 9, 515, 2, "bf16", False, True, True), (1, 3, 5001, 4, "f32", False, True, False), (2, 9, 256, 4, "bf16", False, True, False),
+    (2, 601, 257, 4, "f32", False, True, True), (1, 4, 20000, 4, "bf16", False, True, False)], ids=str)
+def test_conv_bwd_last_input_not_finite(case, bad):
+    """The last input of a row meets the last tap alone: the other taps' gradients stay finite."""
+    import selective_state_space_30_b200 as ssm
+    x, w, b, g, silu, dtype = _inputs(case)
+    x[..., -1] = bad
+    with np.errstate(invalid="ignore"):
+        ref, err = sp.conv_bwd(f64(x), f64(w), f64(b) if b is not None else np.zeros(w.shape[0]), f64(g), silu)
+    assert np.isfinite(ref[1][:, :-1]).all() and not np.isfinite(ref[1][:, -1]).any()
+    got = ssm.causal_conv1d_bwd(x, w, g, bias=b, silu=silu)
+    sp.check(f64(got["dx"]), ref[0], err[0], dtype, "dx")
+    sp.check(f64(got["dw"])[:, :-1], ref[1][:, :-1], err[1][:, :-1], "f32", "dw")
+    assert not np.isfinite(f64(got["dw"])[:, -1]).any()
+    sp.check(f64(got["dbias"]), ref[2], err[2], "f32", "dbias")
