@@ -496,7 +496,8 @@ int ssm_selective_scan_packed_fwd(const ssm_dims_t* dims, const void* u, const v
  * ssm_selective_state_update's.  states must be 16-byte aligned and slot_stride a multiple of 4,
  * B and C 8-byte (bf16) or 16-byte (fp32) aligned, and A 16-byte aligned in the per-channel
  * layout; otherwise SSM_ERR_UNSUPPORTED.  One kernel.  SSM_ERR_INVALID_ARG for a NULL required
- * pointer (states, u, delta, A, B, C, out), seqlen != 1, or a bad shape or stride.
+ * pointer (states, u, delta, A, B, C, out), a pointer off its element's alignment, seqlen != 1, or
+ * a bad shape or stride.
  */
 int ssm_selective_state_update_slots(const ssm_dims_t* dims, float* states, const int32_t* slots,
                                      int64_t n_slots, int64_t slot_stride, const void* u, const void* delta,
@@ -517,7 +518,8 @@ int ssm_selective_state_update_slots(const ssm_dims_t* dims, float* states, cons
  * device.  A pair with src >= n_slots, dst < 0 or dst >= n_slots is skipped.  Destinations must
  * be distinct: with one named twice, which pair's bytes stay is unspecified, byte by byte.
  * One kernel, which allocates nothing.  SSM_ERR_UNSUPPORTED for n_pairs > 4096;
- * SSM_ERR_INVALID_ARG for a NULL pool, src or dst, a negative size or overlapping slots.
+ * SSM_ERR_INVALID_ARG for a NULL pool, src or dst, src or dst off the 4-byte grid, a negative size or
+ * overlapping slots.
  */
 int ssm_state_slots_copy(void* pool, int64_t n_layers, int64_t n_slots, int64_t slot_bytes, int64_t slot_stride,
                          int64_t layer_stride, const int32_t* src, const int32_t* dst, int64_t n_pairs,

@@ -22,9 +22,12 @@
 #include <cstdint>
 
 #include "scan_kernel.cuh"   // f32x2 operations, ex2_approx, rcp_approx
+#include "slots.h"           // all_aligned
 #include "ssm_scan.h"
 
 namespace {
+
+using ssm::all_aligned;
 
 constexpr int kMaxWidth = 4;
 constexpr int kWarps = 8;
@@ -410,8 +413,6 @@ Plan plan_of(int64_t batch, int64_t dim, int64_t seqlen, int io_dtype) {
     return walked(one) - walked(split) > 4 ? split : one;
 }
 
-bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 int check_shape(int64_t batch, int64_t dim, int64_t seqlen, int32_t width, int32_t io_dtype) {
     if (batch < 0 || dim <= 0 || seqlen < 0) return SSM_ERR_INVALID_ARG;
     if (io_dtype != SSM_F32 && io_dtype != SSM_BF16) return SSM_ERR_INVALID_ARG;
@@ -469,7 +470,7 @@ extern "C" int ssm_causal_conv1d_bwd(int64_t batch, int64_t dim, int64_t seqlen,
     if (tokens && (!x || !dout || !dx || dx == x || dx == dout)) return SSM_ERR_INVALID_ARG;
     if (need > 0 && (!workspace || workspace_bytes < need)) return SSM_ERR_INVALID_ARG;
     const uintptr_t esz = io_dtype == SSM_BF16 ? 2 : 4;
-    if (!aligned_to(x, esz) || !aligned_to(dout, esz) || !aligned_to(dx, esz) || !aligned_to(workspace, 4))
+    if (!all_aligned(esz, {x, dout, dx}) || !all_aligned(4, {w, bias, dw, dbias, workspace}))
         return SSM_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     // without tokens every gradient is an empty sum: the kernel finds no stretch and writes zeros
@@ -480,7 +481,7 @@ extern "C" int ssm_causal_conv1d_bwd(int64_t batch, int64_t dim, int64_t seqlen,
     p.batch = tokens ? batch : 0; p.dim = dim; p.seqlen = seqlen;
     p.tiles_per_seg = q.tiles_per_seg; p.n_seg = q.n_seg; p.n_split = q.n_split;
     p.silu = silu ? 1 : 0;
-    const bool aligned = seqlen * (int64_t)esz % 16 == 0 && aligned_to(x, 16) && aligned_to(dout, 16) && aligned_to(dx, 16);
+    const bool aligned = seqlen * (int64_t)esz % 16 == 0 && all_aligned(16, {x, dout, dx});
     const int r = io_dtype == SSM_BF16 ? launch_t<__nv_bfloat16>(p, q.warps, width, aligned, s) : launch_t<float>(p, q.warps, width, aligned, s);
     if (r != SSM_OK || q.n_split == 1) return r;
     const int64_t n = dim * (width + 1);

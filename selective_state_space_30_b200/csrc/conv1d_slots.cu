@@ -28,6 +28,8 @@
 
 namespace {
 
+using ssm::aligned_to;
+using ssm::all_aligned;
 constexpr int kMaxWidth = 4;
 constexpr int kThreads = 256;
 constexpr int kMaxGridY = 65535;
@@ -601,8 +603,6 @@ int launch_update_t(const TokenConv& p, int width, bool vec, cudaStream_t s) {
     }
 }
 
-bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 }  // namespace
 
 extern "C" int ssm_causal_conv1d_packed_fwd(int64_t dim, int64_t total, int64_t n_seq, int32_t width, int32_t io_dtype,
@@ -619,13 +619,13 @@ extern "C" int ssm_causal_conv1d_packed_fwd(int64_t dim, int64_t total, int64_t 
     if (total > 0 && (!x || !out || x == out)) return SSM_ERR_INVALID_ARG;
     if (width > 1 && slot_stride < dim * (width - 1)) return SSM_ERR_INVALID_ARG;
     const uintptr_t esz = io_dtype == SSM_BF16 ? 2 : 4;
-    if (!aligned_to(x, esz) || !aligned_to(out, esz) || !aligned_to(states, esz)) return SSM_ERR_INVALID_ARG;
+    if (!all_aligned(esz, {x, out, states}) || !all_aligned(4, {w, bias, cu_seqlens, slots})) return SSM_ERR_INVALID_ARG;
     PackedConv p{};
     p.x = x; p.w = w; p.bias = bias; p.out = out; p.states = states;
     p.cu = cu_seqlens; p.slots = slots; p.has_state = has_state;
     p.dim = dim; p.total = total; p.n_seq = n_seq; p.n_slots = n_slots; p.slot_stride = slot_stride;
     p.silu = silu ? 1 : 0;
-    p.aligned = total * (int64_t)esz % 16 == 0 && aligned_to(x, 16) && aligned_to(out, 16);
+    p.aligned = total * (int64_t)esz % 16 == 0 && all_aligned(16, {x, out});
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return io_dtype == SSM_BF16 ? launch_packed_t<__nv_bfloat16>(p, width, s) : launch_packed_t<float>(p, width, s);
 }
@@ -641,9 +641,8 @@ extern "C" int ssm_causal_conv1d_update(int64_t batch, int64_t dim, int32_t widt
     if (!x || !w || !out || (width > 1 && !states)) return SSM_ERR_INVALID_ARG;
     if (width > 1 && slot_stride < dim * (width - 1)) return SSM_ERR_INVALID_ARG;
     const int64_t esz = io_dtype == SSM_BF16 ? 2 : 4, V = 16 / esz;
-    if (!aligned_to(x, esz) || !aligned_to(out, esz) || !aligned_to(states, esz)) return SSM_ERR_INVALID_ARG;
-    const bool vec = dim % V == 0 && aligned_to(x, 16) && aligned_to(out, 16) && aligned_to(states, 16) &&
-                     slot_stride % V == 0;
+    if (!all_aligned(esz, {x, out, states}) || !all_aligned(4, {w, bias, slots})) return SSM_ERR_INVALID_ARG;
+    const bool vec = dim % V == 0 && all_aligned(16, {x, out, states}) && slot_stride % V == 0;
     TokenConv p{};
     p.x = x; p.w = w; p.bias = bias; p.out = out; p.states = states; p.slots = slots;
     p.batch = batch; p.dim = dim; p.n_slots = n_slots; p.slot_stride = slot_stride; p.silu = silu ? 1 : 0;

@@ -20,6 +20,8 @@
 
 namespace {
 
+using ssm::aligned_to;
+using ssm::all_aligned;
 using ssm::ex2_approx;
 using ssm::kLog2e;
 constexpr int kThreads = 64;
@@ -158,8 +160,6 @@ int launch(const StepParams& p, int64_t N, cudaStream_t s) {
     }
 }
 
-bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 }  // namespace
 
 extern "C" int ssm_selective_state_update_slots(const ssm_dims_t* dims, float* states, const int32_t* slots,
@@ -180,8 +180,8 @@ extern "C" int ssm_selective_state_update_slots(const ssm_dims_t* dims, float* s
     if (!states || !u || !delta || !A || !B || !C || !out) return SSM_ERR_INVALID_ARG;
     if (slot_stride < d.dim * N) return SSM_ERR_INVALID_ARG;
     const uintptr_t esz = d.io_dtype == SSM_BF16 ? 2 : 4;
-    for (const void* t : {u, delta, z, static_cast<const void*>(out)})
-        if (!aligned_to(t, esz)) return SSM_ERR_INVALID_ARG;
+    if (!all_aligned(esz, {u, delta, B, C, z, out}) || !all_aligned(4, {states, slots, A, D, delta_bias}))
+        return SSM_ERR_INVALID_ARG;
     // four states move as one 16-byte (state, A, fp32 B and C) or 8-byte (bf16 B and C) piece
     if (!aligned_to(states, 16) || slot_stride % 4 || !aligned_to(B, 4 * esz) || !aligned_to(C, 4 * esz) ||
         (d.nheads == d.dim && !aligned_to(A, 16)))

@@ -19,6 +19,8 @@ SSM_PACKED_EXTERN(128)
 
 namespace {
 
+using ssm::aligned_to;
+using ssm::all_aligned;
 using ssm::packed::launch_n;
 using ssm::packed::PackedCfg;
 using ssm::packed::PackedParams;
@@ -67,8 +69,6 @@ int64_t choose_chunk(const ssm_dims_t& d, int64_t max_seqlen) {
     q = (q + step - 1) / step * step;
     return longest > (ssd ? 3 : 4) * q ? q : kNoChunk;
 }
-
-bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 template <typename T>
 int launch_t(PackedParams& p, int64_t N, bool aligned, cudaStream_t s) {
@@ -137,8 +137,8 @@ extern "C" int ssm_selective_scan_packed_fwd(const ssm_dims_t* dims, const void*
     if (d.seqlen > 0 && (!u || !delta || !B || !C || !out)) return SSM_ERR_INVALID_ARG;
     if (slot_stride < d.dim * d.dstate) return SSM_ERR_INVALID_ARG;
     const size_t esz = d.io_dtype == SSM_BF16 ? 2 : 4;
-    for (const void* t : {u, delta, B, C, z, static_cast<const void*>(out)})
-        if (!aligned_to(t, esz)) return SSM_ERR_INVALID_ARG;
+    if (!all_aligned(esz, {u, delta, B, C, z, out}) || !all_aligned(4, {A, D, delta_bias, cu_seqlens, slots, states}))
+        return SSM_ERR_INVALID_ARG;
     const Work w = work_of(d, max_seqlen);
     if (w.bytes > 0 && (!workspace || workspace_bytes < w.bytes || !aligned_to(workspace, 16))) return SSM_ERR_INVALID_ARG;
     PackedParams p{};
@@ -153,8 +153,7 @@ extern "C" int ssm_selective_scan_packed_fwd(const ssm_dims_t* dims, const void*
     p.chunk = w.chunk; p.n_chunks = w.n_chunks;
     p.softplus = softplus ? 1 : 0;
     p.state_vec = aligned_to(states, 16) && slot_stride % 4 == 0;
-    bool aligned = d.seqlen * (int64_t)esz % 16 == 0;
-    for (const void* t : {u, delta, B, C, z, static_cast<const void*>(out)}) aligned = aligned && aligned_to(t, 16);
+    const bool aligned = d.seqlen * (int64_t)esz % 16 == 0 && all_aligned(16, {u, delta, B, C, z, out});
     p.grid16 = aligned;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (on_tensor_cores(d)) return ssm::packed::ssd_packed_launch(p, s);

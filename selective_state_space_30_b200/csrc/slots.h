@@ -3,8 +3,17 @@
 // cu_seqlens and of slot indices, which live on the device and so are checked there, and index
 // arithmetic that a test on the CPU walks through.
 #include <cstdint>
+#include <initializer_list>
 
 namespace ssm {
+
+// Whether each of the pointers (a null one too) lies on a boundary of n bytes, a power of two.
+inline bool all_aligned(uintptr_t n, std::initializer_list<const void*> pointers) {
+    for (const void* p : pointers)
+        if (reinterpret_cast<uintptr_t>(p) & (n - 1)) return false;
+    return true;
+}
+inline bool aligned_to(const void* p, uintptr_t n) { return all_aligned(n, {p}); }
 
 // What a slot index says about its row or sequence.
 //   kSlotLive   0 <= slot < n_slots

@@ -15,6 +15,7 @@
 #include <cstdint>
 
 #include "scan_kernel.cuh"   // smem_u32
+#include "slots.h"         // all_aligned
 #include "ssm_scan.h"
 
 namespace {
@@ -152,7 +153,7 @@ extern "C" int ssm_state_slots_copy(void* pool, int64_t n_layers, int64_t n_slot
     if (n_slots > 0x7FFFFFFF || slot_bytes > ((int64_t)1 << 40) || n_layers > (1 << 20)) return SSM_ERR_INVALID_ARG;
     if (n_pairs > kMaxPairs) return SSM_ERR_UNSUPPORTED;
     if (n_pairs == 0 || n_layers == 0 || slot_bytes == 0 || n_slots == 0) return SSM_OK;
-    if (!pool || !src || !dst) return SSM_ERR_INVALID_ARG;
+    if (!pool || !src || !dst || !ssm::all_aligned(4, {src, dst})) return SSM_ERR_INVALID_ARG;
     // sizes whose products stay far inside 64 bits
     if (slot_stride < slot_bytes || slot_stride > ((int64_t)1 << 46) / n_slots) return SSM_ERR_INVALID_ARG;
     if (n_layers > 1 && (layer_stride < 0 || layer_stride > ((int64_t)1 << 46) / n_layers)) return SSM_ERR_INVALID_ARG;

@@ -286,3 +286,35 @@ def test_token_ranges_are_clamped(indexes):
             indexes.token_range(cu, i, total, out)
             lo = min(max(bounds[i], 0), total)
             assert (out[0], out[1]) == (lo, min(max(bounds[i + 1], lo), total))
+
+
+def test_pointers_off_their_elements_are_refused(ssm):
+    """Every array of the slot operators and of the convolution's gradients, the fp32 and int32 ones too: a
+    pointer off its element's alignment must not reach a kernel."""
+    inv = ssm.SSM_ERR_INVALID_ARG
+    scan = ssm.make_dims(2, 32, 64, 16, 0, 1, ssm.SSM_BF16)
+    step = ssm.make_dims(2, 32, 1, 16, 0, 1, ssm.SSM_BF16)
+    need = ssm.ssm_causal_conv1d_bwd_workspace_size(40, 8, 30, 4, ssm.SSM_BF16)
+    # (entry point, its arguments, its pointers' places)
+    calls = [
+        (ssm.ssm_causal_conv1d_packed_fwd, [8, 20, 2, 4, ssm.SSM_BF16, A16, A16, A16, True, A16, A16, A16, A16, 3, 24, 2 * A16],
+         dict(x=5, w=6, bias=7, cu_seqlens=9, slots=10, states=12, out=15)),
+        (ssm.ssm_causal_conv1d_update, [2, 8, 4, ssm.SSM_F32, A16, A16, A16, True, A16, A16, 3, 24, 2 * A16],
+         dict(x=4, w=5, bias=6, slots=8, states=9, out=12)),
+        (ssm.ssm_selective_scan_packed_fwd, [scan, A16, A16, A16, A16, A16, A16, A16, A16, True, A16, A16, A16, A16, 4, 512, 0,
+                                             2 * A16, None, 0],
+         dict(u=1, delta=2, A=3, B=4, C=5, D=6, z=7, delta_bias=8, cu_seqlens=10, slots=11, states=13, out=17)),
+        (ssm.ssm_selective_state_update_slots, [step, A16, A16, 4, 512, A16, A16, A16, A16, A16, A16, A16, A16, True, 2 * A16],
+         dict(states=1, slots=2, u=5, delta=6, A=7, B=8, C=9, D=10, z=11, delta_bias=12, out=14)),
+        (ssm.ssm_state_slots_copy, [A16, 2, 4, 64, 64, 256, A16, A16, 3], dict(src=6, dst=7)),
+        (ssm.ssm_causal_conv1d_bwd, [40, 8, 30, 4, ssm.SSM_BF16, A16, A16, A16, True, A16, 2 * A16, A16, A16, A16, need],
+         dict(x=5, w=6, bias=7, dout=9, dx=10, dw=11, dbias=12, workspace=13)),
+    ]
+    for fn, args, at in calls:
+        for name, i in at.items():
+            off = args[:i] + [args[i] + 1] + args[i + 1:]
+            assert fn(*off, check=False) == inv, (fn.__name__, name)
+            if name not in ("x", "u", "delta", "B", "C", "z", "out", "dout", "dx"):    # four-byte elements
+                off[i] = args[i] + 2
+                if name != "states" or fn is not ssm.ssm_causal_conv1d_packed_fwd:     # (that one's are bf16)
+                    assert fn(*off, check=False) == inv, (fn.__name__, name)
