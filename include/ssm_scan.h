@@ -438,7 +438,7 @@ int ssm_selective_scan_bwd_test_hooks(int stall, int64_t wait_budget_us);
  * history, and the sequence's last width - 1 inputs replace that history (inputs of a sequence
  * shorter than that join what the slot held).  states: the pool, slot s at s * slot_stride, a
  * slot being (dim, width - 1) in io_dtype, the oldest input first; not used for width 1.
- * width is 1 to 4, else SSM_ERR_UNSUPPORTED.  out must not overlap x.  One kernel.
+ * width is 1 to 4, else SSM_ERR_UNSUPPORTED.  out must not overlap an input or the pool.  One kernel.
  * SSM_ERR_INVALID_ARG for a bad size, stride or dtype, a pointer off its element's alignment,
  * a NULL w, cu_seqlens, states (width > 1), x or out (total > 0), or out == x.
  */
@@ -450,7 +450,8 @@ int ssm_causal_conv1d_packed_fwd(int64_t dim, int64_t total, int64_t n_seq, int3
 
 /*
  * The same convolution for one new token of each row: x and out are (batch, dim); each row's
- * history is read from its slot and moved on by the token.  One kernel.  Errors as above.
+ * history is read from its slot and moved on by the token.  One kernel.  out may be x itself, and
+ * must not overlap an input or the pool otherwise.  Errors as above, but for out == x.
  */
 int ssm_causal_conv1d_update(int64_t batch, int64_t dim, int32_t width, int32_t io_dtype, const void* x,
                              const float* w, const float* bias, int silu, const int32_t* slots, void* states,
@@ -477,7 +478,7 @@ int ssm_causal_conv1d_update(int64_t batch, int64_t dim, int32_t width, int32_t 
  * a token of u reaches every token of its block and sequence, the earlier ones too, and a wait for
  * the tensor cores or a copy that runs out (half a second) leaves NaN in the rest of that head's outputs.
  *
- * out must not overlap an input.  SSM_ERR_INVALID_ARG for a bad shape or stride, a pointer off its
+ * out must not overlap an input or the pool.  SSM_ERR_INVALID_ARG for a bad shape or stride, a pointer off its
  * element's alignment, a workspace that is too small, or a NULL A, cu_seqlens, states, or u,
  * delta, B, C, out (seqlen > 0).
  */
@@ -493,7 +494,8 @@ int ssm_selective_scan_packed_fwd(const ssm_dims_t* dims, const void* u, const v
 /*
  * ssm_selective_state_update with the states in slots of a pool: row b's state is slot slots[b],
  * updated in place.  dims->seqlen must be 1; the inputs' layouts are
- * ssm_selective_state_update's.  states must be 16-byte aligned and slot_stride a multiple of 4,
+ * ssm_selective_state_update's.  out may be u or z itself, and must not overlap an input or the
+ * pool otherwise.  states must be 16-byte aligned and slot_stride a multiple of 4,
  * B and C 8-byte (bf16) or 16-byte (fp32) aligned, and A 16-byte aligned in the per-channel
  * layout; otherwise SSM_ERR_UNSUPPORTED.  One kernel.  SSM_ERR_INVALID_ARG for a NULL required
  * pointer (states, u, delta, A, B, C, out), a pointer off its element's alignment, seqlen != 1, or

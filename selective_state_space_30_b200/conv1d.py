@@ -7,7 +7,8 @@ from ._frontend import load, on_stream
 
 def causal_conv1d_fwd(x, w, bias=None, silu: bool = True, out=None, stream=None):
     """out[b,d,t] = act(bias[d] + sum_k w[d,k] x[b,d,t-width+1+k]) on CUDA tensors: x (batch, dim, seqlen)
-    bf16 or fp32, w (dim, width) and bias fp32."""
+    bf16 or fp32, w (dim, width) and bias fp32.  out must not overlap an input: each output needs the inputs
+    before its own."""
     f = load().conv_fwd
     return f(x, w, bias, silu, out) if stream is None else on_stream(f, stream, x, x, w, bias, silu, out)
 

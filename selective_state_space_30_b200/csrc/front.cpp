@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <initializer_list>
 #include <string>
 
 #include "ssm_scan.h"
@@ -146,12 +147,25 @@ void need_workspace(const Arg& ws, int device) {
     if (ws && (!ws->is_cuda() || ws->get_device() != device || !ws->is_contiguous()))
         refuse("%s must be contiguous and on the device of the other tensors%s", ws.name);
 }
-// Two contiguous tensors, or one and nothing, that share no byte.
-void need_apart(const Arg& out, const Arg& in) {
-    if (!out || !in) return;
-    const char *a = static_cast<const char*>(out.ptr()), *b = static_cast<const char*>(in.ptr());
-    if (a < b + in->numel() * in->element_size() && b < a + out->numel() * out->element_size())
-        refuse("%s must not overlap %s", out.name, in.name);
+// The bytes from a tensor's first element to behind its last one, wherever its dimensions lie.
+struct Span {
+    const char *lo, *hi;
+    explicit Span(const Tensor& t) : lo(static_cast<const char*>(t.data_ptr())), hi(lo) {
+        if (t.numel() == 0) return;
+        int64_t last = 0;
+        for (int64_t i = 0; i < t.dim(); ++i) last += (t.size(i) - 1) * t.stride(i);
+        hi = lo + (last + 1) * t.element_size();
+    }
+    bool meets(const Span& o) const { return lo < o.hi && o.lo < hi; }
+};
+// What is written must share no byte with what is read (`out` given: an output of the call's own never does).
+// `in_place`: it may be that very tensor, where each thread reads its elements before it writes them.
+void need_apart(const Arg& out, std::initializer_list<const Arg*> read, bool in_place = false) {
+    if (!out) return;
+    const Span o(*out);
+    for (const Arg* in : read)
+        if (*in && !(in_place && out.ptr() == in->ptr()) && o.meets(Span(**in)))
+            refuse(in_place ? "%s must not overlap %s but for being the same tensor" : "%s must not overlap %s", out.name, in->name);
 }
 size_t bytes_of(const Tensor& t) { return (size_t)t.numel() * t.element_size(); }
 
@@ -197,6 +211,7 @@ PyObject* conv_fwd(PyObject* const* v) {
     const int64_t width = need_taps(w, bias, x->size(1), dev, false);
     const int32_t io = io_code(x);
     need(out, x->scalar_type(), x->sizes(), dev);
+    need_apart(out, {&x, &w, &bias});
     const Launch on(dev);
     Tensor o = out_or(out, *x, false);
     check(entry.conv_fwd(x->size(0), x->size(1), x->size(2), (int32_t)width, io, x.ptr(), f32(w), f32(bias), silu,
@@ -236,7 +251,7 @@ PyObject* conv_packed(PyObject* const* v) {
     need(out, x->scalar_type(), x->sizes(), dev);
     const int64_t stride = pool_stride(states, x->scalar_type(), dim, width - 1, dev);
     need_indices(n, dev, cu, slots, has);
-    need_apart(out, x);
+    need_apart(out, {&x, &w, &bias, &states, &cu, &slots, &has});
     const Launch on(dev);
     Tensor o = out_or(out, *x, true);
     check(entry.conv_packed(dim, total, n, (int32_t)width, io, x.ptr(), f32(w), f32(bias), silu, i32(cu), i32(slots), u8(has),
@@ -255,6 +270,8 @@ PyObject* conv_update(PyObject* const* v) {
     need(out, x->scalar_type(), x->sizes(), dev);
     const int64_t stride = pool_stride(states, x->scalar_type(), dim, width - 1, dev);
     need(slots, at::kInt, {batch}, dev);
+    need_apart(out, {&x}, true);
+    need_apart(out, {&w, &bias, &states, &slots});
     const Launch on(dev);
     Tensor o = out_or(out, *x, true);
     check(entry.conv_update(batch, dim, (int32_t)width, io, x.ptr(), f32(w), f32(bias), silu, i32(slots), states.ptr(),
@@ -289,7 +306,7 @@ PyObject* scan_packed(PyObject* const* v) {
     const int64_t stride = pool_stride(states, at::kFloat, dim, N, dev);
     need_indices(n, dev, cu, slots, has);
     need_workspace(ws, dev);
-    for (const Arg* in : {&u, &delta, &B, &C, &z}) need_apart(out, *in);
+    need_apart(out, {&u, &delta, &B, &C, &z, &A, &D, &bias, &states, &cu, &slots, &has, &ws});
     const ssm_dims_t d = {n, dim, total, N, heads, groups, io, 0};
     const Launch on(dev);
     size_t bytes = 0;
@@ -328,6 +345,8 @@ PyObject* state_update(PyObject* const* v) {
     need(out, type, {batch, dim}, dev);
     need(slots, at::kInt, {batch}, dev);
     const int64_t stride = pool_stride(states, at::kFloat, dim, N, dev);
+    need_apart(out, {&u, &z}, true);
+    need_apart(out, {&delta, &B, &C, &A, &D, &bias, &states, &slots});
     const ssm_dims_t d = {batch, dim, 1, N, heads, groups, io, 0};
     const Launch on(dev);
     Tensor o = out_or(out, *u, true);

@@ -6,7 +6,8 @@ a negative slot marks a padding row.  Pools are (n_slots, ...) tensors whose slo
 and may lie apart (a layer's view of a pool that holds several layers).  The calls update the
 pools in place, run on `stream` (default: the device's current one) and can be captured into a
 CUDA graph.  `out` is allocated with torch unless given, zeroed so that padding reads as zero; a
-workspace is allocated unless given.  Tensors of another type, shape, device or layout are refused
+workspace is allocated unless given.  An `out` that is given shares no memory with what the call reads
+(the single-token calls may write over x, u or z: out being that very tensor).  Tensors of another type, shape, device or layout are refused
 with ValueError, what the library refuses with SsmError.  The checks and calls are compiled
 (csrc/front.cpp).
 """

@@ -830,3 +830,60 @@ def test_front_end_refusals(ssm):
         ssm.state_slots_copy(pool, i32([-1] * 5000), i32([0] * 5000))
     with pytest.raises(ValueError, match="dout must"):
         ssm.causal_conv1d_bwd(t(1, 8, 4), w, t(1, 8, 5))
+
+
+def test_overlapping_outputs_are_refused_everywhere(ssm):
+    """Outputs on what a call reads: the batch convolution, the single-token calls, and the pools and weights of
+    the packed ones.  The single-token calls may write over their own x, u or z, and give the same then."""
+    gen = torch.Generator().manual_seed(6)
+    w, b = rnd(gen, 8, 4), rnd(gen, 8)
+    x = rnd(gen, 2, 8, 40)
+    buf = torch.zeros(4 * 640, device="cuda")
+    for a, out in ((x, x), (buf[:640].view(2, 8, 40), buf[1:641].view(2, 8, 40)), (buf[600:1240].view(2, 8, 40), buf[:640].view(2, 8, 40))):
+        with pytest.raises(ValueError, match="out must not overlap x"):
+            ssm.causal_conv1d_fwd(a, w, b, out=out)
+    assert torch.equal(ssm.causal_conv1d_fwd(x, w, b, out=buf[:640].view(2, 8, 40)), ssm.causal_conv1d_fwd(x, w, b))
+    # the packed convolution on its pool, its taps and its lengths
+    px, cu = rnd(gen, 8, 40), i32([0, 15, 40])
+    flat = torch.zeros(8 * 40 + 48, device="cuda")
+    for out, kw, word in ((flat[:320].view(8, 40), dict(conv_states=flat[300:348].view(2, 8, 3)), "conv_states"),
+                          (flat[:320].view(8, 40), dict(w=flat[316:348].view(8, 4)), "w"),
+                          (flat[:320].view(8, 40), dict(conv_states=torch.as_strided(flat, (2, 8, 3), (300, 3, 1), 10)), "conv_states")):
+        with pytest.raises(ValueError, match=f"out must not overlap {word}"):
+            ssm.causal_conv1d_packed(**{**dict(x=px, w=w, cu_seqlens=cu, conv_states=rnd(gen, 2, 8, 3), out=out), **kw})
+    p = _scan_inputs(gen, 40, 8, 8, 1, 8, "f32")
+    with pytest.raises(ValueError, match="out must not overlap states"):
+        _call(ssm, p, cu, flat[:128].view(2, 8, 8), flat[:320].view(8, 40))
+    with pytest.raises(ValueError, match="out must not overlap A"):
+        _call(ssm, dict(p, A=flat[304:368].view(8, 8)), cu, rnd(gen, 2, 8, 8), flat[:320].view(8, 40))
+    # single tokens
+    tx, pool = rnd(gen, 5, 8), rnd(gen, 5, 8, 3)
+    t = torch.zeros(200, device="cuda")
+    with pytest.raises(ValueError, match="out must not overlap x"):
+        ssm.causal_conv1d_update(t[:40].view(5, 8), w, pool, out=t[8:48].view(5, 8))
+    with pytest.raises(ValueError, match="out must not overlap conv_states"):
+        ssm.causal_conv1d_update(tx, w, t[:120].view(5, 8, 3), out=t[100:140].view(5, 8))
+    over, pools = tx.clone(), (pool.clone(), pool.clone())
+    want = ssm.causal_conv1d_update(tx, w, pools[0], bias=b)
+    assert torch.equal(ssm.causal_conv1d_update(over, w, pools[1], bias=b, out=over), want) and torch.equal(*pools)
+    q = _scan_inputs(gen, 5, 8, 8, 1, 8, "f32", prompts=False)
+    states = rnd(gen, 5, 8, 8)
+
+    def step(st, out, **kw):
+        a = {**q, **kw}
+        return ssm.selective_state_update_slots(st, a["u"], a["delta"], a["A"], a["B"], a["C"], D=a["D"], z=a["z"],
+                                                delta_bias=a["delta_bias"], out=out)
+
+    for k in ("delta", "B", "C"):
+        with pytest.raises(ValueError, match=f"out must not overlap {k}"):
+            step(states, q[k].view(5, 8))
+    for k in ("u", "z"):
+        with pytest.raises(ValueError, match=f"out must not overlap {k}"):
+            step(states, t[1:41].view(5, 8), **{k: t[:40].view(5, 8)})
+    with pytest.raises(ValueError, match="out must not overlap states"):
+        step(buf[:320].view(5, 8, 8), buf[280:320].view(5, 8))
+    first = states.clone()
+    want = step(first, None)
+    for k in ("u", "z"):
+        again, over = states.clone(), q[k].clone()
+        assert torch.equal(step(again, over, **{k: over}), want) and torch.equal(again, first)
