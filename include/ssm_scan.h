@@ -414,8 +414,9 @@ int ssm_selective_scan_bwd_test_hooks(int stall, int64_t wait_budget_us);
  *   cu_seqlens  (n_seq + 1) int32, device: sequence i is the tokens [cu_seqlens[i],
  *               cu_seqlens[i+1]) of the packed buffer.  A length may be zero.  Tokens ahead of
  *               the first and behind the last sequence change nothing and are not written.
- *               Bounds that lie outside the buffer or run backwards are clamped to it (where
- *               sequences then share tokens, either's outputs stay).
+ *               Bounds that lie outside the buffer or run backwards are clamped to it: each sequence
+ *               runs over its clamped range (where sequences then share tokens, either's outputs
+ *               stay; the convolution of more than 1024 sequences may leave them unwritten).
  *   slots       (n_seq or batch) int32, device, nullable: the slot of each sequence or row;
  *               NULL means slot i for i.  A negative slot marks padding: nothing is written for
  *               it, its outputs stay as they were.  A slot >= n_slots touches no state and its

@@ -614,12 +614,15 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
 // last one.  Items go by sequence, the long ones first so that no long one starts last: sequences
 // are ranked by the bucket of their length (two per octave) and within it by number.  Cut
 // sequences have ceil(length / chunk) items each, at least one, and keep their own order, which
-// their chunks' places in the workspace follow.
-__device__ __forceinline__ bool find_item(const PackedParams& p, int64_t x, int64_t* sh, int nt, int64_t& seq, int64_t& k) {
+// their chunks' places in the workspace follow.  `cut`: whether this call cuts.  The workspace and the
+// grid have room for the chunks of sequences that share no token; where bounds run backwards and there
+// would be more, every sequence is one item.
+__device__ __forceinline__ bool find_item(const PackedParams& p, int64_t x, int64_t* sh, int nt, int64_t& seq, int64_t& k,
+                                          bool& cut) {
     // sh: [0] sequence, [1] item of it, [2 ..] warp sums, [34 ..] counts of the buckets
     constexpr int kBuckets = 64;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt / 32;
-    const bool cut = p.chunk > 0;
+    cut = p.chunk > 0;
     if (p.n_seq <= 32) {
         // few sequences, one per lane: every warp finds the item by itself, by exact length
         int64_t len = -1;
@@ -627,7 +630,7 @@ __device__ __forceinline__ bool find_item(const PackedParams& p, int64_t x, int6
             const TokenRange r = token_range(p.cu, lane, p.total);
             len = r.hi - r.lo;
         }
-        int first, n;                                   // the lane's sequence has items [first, first + n)
+        int first = 0, n = 0;                           // the lane's sequence has items [first, first + n)
         if (cut) {
             n = len > 0 ? (int)((len + p.chunk - 1) / p.chunk) : len == 0;
             int inc = n;
@@ -637,7 +640,9 @@ __device__ __forceinline__ bool find_item(const PackedParams& p, int64_t x, int6
                 if (lane >= m) inc += v;
             }
             first = inc - n;
-        } else {
+            cut = __shfl_sync(0xffffffffu, inc, 31) <= p.n_chunks;
+        }
+        if (!cut) {
             n = len >= 0;
             first = 0;
             const int l = (int)len;
@@ -660,6 +665,20 @@ __device__ __forceinline__ bool find_item(const PackedParams& p, int64_t x, int6
         return kBuckets - 2 - 2 * e - half;             // the longest come first
     };
     int want = 0;
+    if (cut) {
+        unsigned long long* total = reinterpret_cast<unsigned long long*>(sh);
+        if (tid == 0) *total = 0ull;
+        __syncthreads();
+        int64_t n = 0;
+        for (int64_t i = tid; i < p.n_seq; i += nt) {
+            const TokenRange r = token_range(p.cu, i, p.total);
+            n += r.hi > r.lo ? (r.hi - r.lo + p.chunk - 1) / p.chunk : 1;
+        }
+        atomicAdd(total, (unsigned long long)n);
+        __syncthreads();
+        cut = *total <= (unsigned long long)p.n_chunks;
+        __syncthreads();
+    }
     if (!cut) {
         for (int i = tid; i < kBuckets; i += nt) count[i] = 0u;
         __syncthreads();
@@ -713,13 +732,14 @@ enum Run { kRunNone, kRunFull, kRunLocal };
 template <typename T>
 __device__ __forceinline__ Run find_run(const PackedParams& p, int64_t x, int64_t* sh, int nt, Task& tk) {
     int64_t seq, k;
+    bool cut;
     tk.chunk_id = (int)x;
-    if (!find_item(p, x, sh, nt, seq, k)) return kRunNone;
+    if (!find_item(p, x, sh, nt, seq, k, cut)) return kRunNone;
     const TokenRange r = token_range(p.cu, seq, p.total);
     const int64_t t0 = r.lo + k * p.chunk;
     tk.k = (int)k;
     tk.t0 = (int)t0;
-    tk.t1 = (int)(p.chunk > 0 && r.hi - t0 > p.chunk ? t0 + p.chunk : r.hi);
+    tk.t1 = (int)(cut && r.hi - t0 > p.chunk ? t0 + p.chunk : r.hi);
     tk.last = tk.t1 == r.hi;
     tk.slot = p.slots ? __ldg(p.slots + seq) : (int)seq;
     tk.has = p.has_state && __ldg(p.has_state + seq) != 0;

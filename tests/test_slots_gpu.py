@@ -887,3 +887,30 @@ def test_overlapping_outputs_are_refused_everywhere(ssm):
     for k in ("u", "z"):
         again, over = states.clone(), q[k].clone()
         assert torch.equal(step(again, over, **{k: over}), want) and torch.equal(again, first)
+
+
+@pytest.mark.parametrize("dim,heads,N,T", [(32, 32, 16, 1200), (32, 32, 16, 1203), (64, 1, 128, 1200), (64, 1, 128, 1199)])
+@pytest.mark.parametrize("many", [False, True])
+def test_scan_packed_cut_with_shared_tokens(ssm, dim, heads, N, T, many):
+    """Bounds that run backwards where sequences would be cut: each sequence still runs over its own clamped
+    range, from its own slot to its own slot, however many chunks that would be."""
+    gen = torch.Generator().manual_seed(32)
+    p = _scan_inputs(gen, T, dim, heads, 1, N, "bf16")
+    cu = [0, T, 0, T, 5, 10 ** 6, -7, 300]
+    if many:                                             # more sequences than a warp's lanes
+        cu = cu + [T] * 30
+    n = len(cu) - 1
+    hint = 0 if not many else T
+    assert _chunk(ssm, p, n, hint) > 0, "this case is here for the cut path"
+    bounds = [(min(max(a, 0), T), min(max(b, min(max(a, 0), T)), T)) for a, b in zip(cu, cu[1:])]
+    states, out = rnd(gen, n + 1, dim, N), rnd(gen, dim, T, dtype="bf16")
+    slots = np.random.default_rng(3).permutation(n + 1)[:n].tolist()
+    has = [0] * n
+    _, _, ref_pool, pool_err = sp.scan_packed(_plain(p), bounds, slots, has, f64(states), f64(out),
+                                              tensor=_tensor(dim, heads, N, "bf16", T, n))
+    _call(ssm, p, i32(cu), states, out, slots=i32(slots), has_state=torch.tensor(has, dtype=torch.uint8).cuda(), max_seqlen=hint)
+    sp.check(f64(states), ref_pool, pool_err, "f32", "states")
+    # the first five tokens start every sequence that holds them
+    alone = sp.scan_packed(_plain(p), [(0, T)], [0], [0], np.zeros((1, dim, N)), np.zeros((dim, T)),
+                           tensor=_tensor(dim, heads, N, "bf16", T, n))
+    sp.check(f64(out)[:, :5], alone[0][:, :5], alone[1][:, :5], "bf16", "out")
