@@ -614,15 +614,16 @@ __device__ __forceinline__ void run_chunk(const PackedParams& p, const Task& tk,
 // last one.  Items go by sequence, the long ones first so that no long one starts last: sequences
 // are ranked by the bucket of their length (two per octave) and within it by number.  Cut
 // sequences have ceil(length / chunk) items each, at least one, and keep their own order, which
-// their chunks' places in the workspace follow.  `cut`: whether this call cuts.  The workspace and the
-// grid have room for the chunks of sequences that share no token; where bounds run backwards and there
-// would be more, every sequence is one item.
+// their chunks' places in the workspace follow.  CUT: the call may cut, `cut`: it does.  The workspace
+// and the grid have room for the chunks of sequences that share no token; where bounds run backwards and
+// there would be more, every sequence is one item.
+template <bool CUT>
 __device__ __forceinline__ bool find_item(const PackedParams& p, int64_t x, int64_t* sh, int nt, int64_t& seq, int64_t& k,
                                           bool& cut) {
     // sh: [0] sequence, [1] item of it, [2 ..] warp sums, [34 ..] counts of the buckets
     constexpr int kBuckets = 64;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt / 32;
-    cut = p.chunk > 0;
+    cut = CUT;
     if (p.n_seq <= 32) {
         // few sequences, one per lane: every warp finds the item by itself, by exact length
         int64_t len = -1;
@@ -631,7 +632,7 @@ __device__ __forceinline__ bool find_item(const PackedParams& p, int64_t x, int6
             len = r.hi - r.lo;
         }
         int first = 0, n = 0;                           // the lane's sequence has items [first, first + n)
-        if (cut) {
+        if constexpr (CUT) {
             n = len > 0 ? (int)((len + p.chunk - 1) / p.chunk) : len == 0;
             int inc = n;
 #pragma unroll
@@ -665,7 +666,7 @@ __device__ __forceinline__ bool find_item(const PackedParams& p, int64_t x, int6
         return kBuckets - 2 - 2 * e - half;             // the longest come first
     };
     int want = 0;
-    if (cut) {
+    if constexpr (CUT) {
         unsigned long long* total = reinterpret_cast<unsigned long long*>(sh);
         if (tid == 0) *total = 0ull;
         __syncthreads();
@@ -729,12 +730,12 @@ __device__ __forceinline__ bool find_item(const PackedParams& p, int64_t x, int6
 // What this launch does with the x-th item: fills in the task's tokens, slot and chunk (its channels
 // are set), or, for a bad slot, writes the outputs' NaN.  All threads of the CTA call it.
 enum Run { kRunNone, kRunFull, kRunLocal };
-template <typename T>
+template <typename T, bool CUT>
 __device__ __forceinline__ Run find_run(const PackedParams& p, int64_t x, int64_t* sh, int nt, Task& tk) {
     int64_t seq, k;
     bool cut;
     tk.chunk_id = (int)x;
-    if (!find_item(p, x, sh, nt, seq, k, cut)) return kRunNone;
+    if (!find_item<CUT>(p, x, sh, nt, seq, k, cut)) return kRunNone;
     const TokenRange r = token_range(p.cu, seq, p.total);
     const int64_t t0 = r.lo + k * p.chunk;
     tk.k = (int)k;
@@ -771,7 +772,7 @@ scan_packed_kernel(const PackedParams p) {
     tk.ci0 = (int)(tile % p.tiles_per_group) * Cf::CT;
     tk.d0 = tk.g * (int)p.group_dim + tk.ci0;
     tk.nch = (int)p.group_dim - tk.ci0 < Cf::CT ? (int)p.group_dim - tk.ci0 : Cf::CT;
-    const Run run = find_run<T>(p, blockIdx.x / p.n_tiles, reinterpret_cast<int64_t*>(smem), Cf::NT, tk);
+    const Run run = find_run<T, CUT>(p, blockIdx.x / p.n_tiles, reinterpret_cast<int64_t*>(smem), Cf::NT, tk);
     if (run == kRunFull) run_chunk<T, N, HEAD, ALIGNED, false, CUT>(p, tk, smem);
     if constexpr (CUT)
         if (run == kRunLocal) run_chunk<T, N, HEAD, ALIGNED, true, true>(p, tk, smem);

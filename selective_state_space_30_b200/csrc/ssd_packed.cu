@@ -16,9 +16,9 @@
 // Precision.  B, C and X are bf16 and enter exactly.  X' is split into three bf16 terms (24 bits),
 // so the state is summed as exactly as in fp32; M and H into two (16 bits, 2^-17 of each product),
 // far inside the rounding of the bf16 outputs.  Sums of a that are subtracted from one another
-// lose their small differences, so every s(i, j) is added up from terms of its own: the steps left
-// in j's 32-step stretch, whole stretches between, and the steps of i's stretch; within one
-// stretch it is a difference of two sums of at most 32 terms.
+// lose their small differences, so every s(i, j) is added up from terms of its own: over stretches of
+// 32 steps and groups of four, what is left of j's, the whole ones between, and the steps of i's; a
+// step's own weight is its dt.
 //
 // Order of a block.  The products run under the threads' work: G, then S and C H while M is made from
 // G in tensor memory (M is Y's left operand there), Y while the state takes S and X' of the next
@@ -80,15 +80,16 @@ constexpr int OFF_DEC = 192 * 1024;            // two blocks' Decay
 constexpr int OFF_BAR = OFF_DEC + 2 * 4096;
 constexpr int kSmem = OFF_BAR + 256 + 1024;    // and room to align the base
 
-// A block's decay over the 32-step stretches of its 128 steps, in log2 units but for far and w.
-// Within a stretch dt_j is a factor of j's weights: as its logarithm, one product less per element of
-// M, where softplus makes it positive, and by itself (`dt`) where it may have any sign.
+// A block's decay over its 128 steps, in stretches of 32 and groups of four: head, a, pre and the whole
+// groups and stretches in log2 units, the others weights.
 struct Decay {
     float head[kQ];       // from the stretch's start through the step
-    float near[kQ];       // log2 dt_j less that: with head_i, the weight of j for i of the same stretch
     float far[kQ];        // dt_j times the decay from behind j to the stretch's end: for later stretches
     float w[kQ];          // 2^s(end, j) dt_j
-    float dt[kQ];
+    float close[kQ];      // dt_j times the decay from behind j to its group's end: for later groups of the stretch
+    float pre[kQ];        // from the group's start through the step
+    float a[kQ], dt[kQ];  // the step's own
+    float group[kQ / 4];  // whole groups
     float stretch[4];     // whole stretches
 };
 static_assert(sizeof(Decay) <= 4096, "fits its place");
@@ -226,20 +227,20 @@ __device__ __noinline__ void store_out(const unsigned char* tile, unsigned short
     }
 }
 
-// A block's decay, by one warp: four steps per lane, so eight lanes hold a stretch.
-template <bool SOFTPLUS>
+// A block's decay, by one warp: a group of four steps per lane, so eight lanes hold a stretch.
 __device__ __forceinline__ void block_decay(const PackedParams& p, const unsigned short* delta, const Block& k, float Ah,
                                             float bias, int lane, Decay& o) {
-    float dt[4], pre[4], run = 0.f;
+    float dt[4], a[4], pre[4], run = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int64_t t = k.tb + 4 * lane + e;
-        dt[e] = 0.f;
+        dt[e] = a[e] = 0.f;
         if (t >= k.t0 && t < k.t1) {
             const float x = __uint_as_float((uint32_t)__ldg(delta + t) << 16) + bias;
-            dt[e] = SOFTPLUS ? softplus1(x) : x;
+            dt[e] = p.softplus ? softplus1(x) : x;
+            a[e] = dt[e] * Ah;
         }
-        run += dt[e] * Ah;
+        run += a[e];
         pre[e] = run;
     }
     // sums of the lanes before and behind within the stretch
@@ -261,25 +262,32 @@ __device__ __forceinline__ void block_decay(const PackedParams& p, const unsigne
         if (s > (lane >> 3)) later += v;
     }
     const float rest = ex2_approx(later);
-    float suf = 0.f;
+    float suf = 0.f, head[4], far[4], w[4], close[4];
 #pragma unroll
     for (int e = 3; e >= 0; --e) {
-        const int j = 4 * lane + e;
-        const float l = SOFTPLUS ? __log2f(dt[e]) : 0.f;     // -inf where dt = 0: a weight of zero
-        o.head[j] = up + pre[e];
-        o.near[j] = l - (up + pre[e]);
-        const float far = ex2_approx(suf + down) * dt[e];
-        o.far[j] = far;
-        o.w[j] = far * rest;
-        if (!SOFTPLUS) o.dt[j] = dt[e];
-        suf += dt[e] * Ah;
+        head[e] = up + pre[e];
+        far[e] = ex2_approx(suf + down) * dt[e];
+        w[e] = far[e] * rest;
+        close[e] = ex2_approx(suf) * dt[e];
+        suf += a[e];
     }
+    auto put = [&](float* to, const float (&v)[4]) {
+        *reinterpret_cast<float4*>(to + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+    };
+    put(o.head, head);
+    put(o.far, far);
+    put(o.w, w);
+    put(o.close, close);
+    put(o.pre, pre);
+    put(o.a, a);
+    put(o.dt, dt);
+    o.group[lane] = run;
     if ((lane & 7) == 0) o.stretch[lane >> 3] = whole;
 }
 
 // Thread: TMEM lane and tile row `row`, and a quarter of that row's columns (32 of the 128 steps,
 // 16 of the 64 channels).  LOCAL: only the end state from zero and the product of the decays.
-template <bool LOCAL, bool SOFTPLUS>
+template <bool LOCAL>
 __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& maps, const Task& tk, unsigned char* smem) {
     uint64_t* mb_g = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
     uint64_t *mb_s = mb_g + 1, *mb_y = mb_g + 2, *mb_x = mb_g + 3, *mb_bc = mb_g + 4, *mb_z = mb_g + 5;
@@ -377,7 +385,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
     __syncthreads();
     stage_x(0);
     stage_bc(0);
-    if (warp == kDecayWarp && nblk > 0) block_decay<SOFTPLUS>(p, delta, block(0), Ah, bias, lane, dec[0]);
+    if (warp == kDecayWarp && nblk > 0) block_decay(p, delta, block(0), Ah, bias, lane, dec[0]);
 
     // the state: n = row, channels p0 .. p0 + 15
     float H[16], Dv[LOCAL ? 1 : 8];                     // the skip weights of the channels it writes
@@ -490,7 +498,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
         const Decay& dc = dec[c & 1];
         const unsigned char* sX = smem + OFF_X + (c & 1) * 16384;
         const bool with_state = c > 0 || start_state;
-        if (warp == kDecayWarp && c + 1 < nblk) block_decay<SOFTPLUS>(p, delta, block(c + 1), Ah, bias, lane, dec[(c + 1) & 1]);
+        if (warp == kDecayWarp && c + 1 < nblk) block_decay(p, delta, block(c + 1), Ah, bias, lane, dec[(c + 1) & 1]);
         ok = true;
         if constexpr (!LOCAL) {
             // ---- M, in two terms over G: row i = row, steps j0 .. (S and C H run)
@@ -505,36 +513,66 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
                 uint32_t gv[32];
                 tc::ld32(trow + kColG + j0, gv);
                 const bool same = part == quarter;
-                float ci = dc.head[row];
-                for (int s = part + 1; s < quarter; ++s) ci += dc.stretch[s];
-                // over whole stretches the weight is a product of the row's and the step's
-                const pair_t ci2 = pk(same ? ci : ex2_approx(ci));
-                const float* cj = (same ? dc.near : dc.far) + j0;
-                tc::wait_ld();
-                tc::after_wait(gv);
-#pragma unroll
-                for (int k = 0; k < 32; k += 8) {
-                    const ulonglong2 ca = *reinterpret_cast<const ulonglong2*>(cj + k);
-                    const ulonglong2 cb = *reinterpret_cast<const ulonglong2*>(cj + k + 4);
-                    const pair_t c2[4] = {ca.x, ca.y, cb.x, cb.y};
-                    pair_t v[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        v[q] = pk(__uint_as_float(gv[k + 2 * q]), __uint_as_float(gv[k + 2 * q + 1]));
-                        if (same) {                     // of the stretch's own steps, those up to the row's
-                            v[q] = pmul(v[q], pex2(padd(ci2, c2[q])));
-                            if constexpr (!SOFTPLUS) v[q] = pmul(v[q], *reinterpret_cast<const pair_t*>(dc.dt + j0 + k + 2 * q));
-                            const float2 f = halves(v[q]);
-                            const int j = k + 2 * q;
-                            v[q] = pk(j <= lane ? f.x : 0.f, j + 1 <= lane ? f.y : 0.f);
-                        } else {
-                            v[q] = pmul(v[q], pmul(ci2, c2[q]));
-                        }
-                    }
+                auto put = [&](int k, pair_t (&v)[4]) {
                     split8<2>(v, [&](int t, const uint32_t (&w)[4]) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) (t ? m1 : m0)[k / 2 + q] = w[q];
                     });
+                };
+                if (same) {
+                    // of the stretch's own steps those up to the row's: over whole groups of four the weight is
+                    // a product of the row's and the step's, in the row's own group it is made step by step
+                    const int e = lane & 3, gi = lane >> 2;
+                    const float4 a4 = *reinterpret_cast<const float4*>(dc.a + (row & ~3u));
+                    const float4 d4 = *reinterpret_cast<const float4*>(dc.dt + (row & ~3u));
+                    float s = e >= 3 ? a4.w : 0.f;
+                    const float o2 = d4.z * ex2_approx(s);
+                    s = e >= 2 ? s + a4.z : 0.f;
+                    const float o1 = d4.y * ex2_approx(s);
+                    s = e >= 1 ? s + a4.y : 0.f;
+                    const pair_t own[2] = {pk(d4.x * ex2_approx(s), o1), pk(o2, d4.w)};
+                    float run = dc.pre[row];            // from behind a group through the row
+                    tc::wait_ld();
+                    tc::after_wait(gv);
+#pragma unroll
+                    for (int k = 24; k >= 0; k -= 8) {
+                        pair_t v[4];
+#pragma unroll
+                        for (int g = 1; g >= 0; --g) {
+                            const int at = k / 4 + g;
+                            const pair_t to = pk(ex2_approx(run));
+                            const ulonglong2 c2 = *reinterpret_cast<const ulonglong2*>(dc.close + j0 + 4 * at);
+                            const float whole = dc.group[j0 / 4 + at];
+                            run = at < gi ? run + whole : run;
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                const int j = 4 * at + 2 * q;
+                                const pair_t w = at == gi ? own[q] : pmul(to, q ? c2.y : c2.x);
+                                const float2 f = halves(pmul(pk(__uint_as_float(gv[j]), __uint_as_float(gv[j + 1])), w));
+                                v[2 * g + q] = pk(j <= lane ? f.x : 0.f, j + 1 <= lane ? f.y : 0.f);
+                            }
+                        }
+                        put(k, v);
+                    }
+                } else {
+                    // over whole stretches it is a product too
+                    float ci = dc.head[row];
+                    for (int s = part + 1; s < quarter; ++s) ci += dc.stretch[s];
+                    const pair_t ci2 = pk(ex2_approx(ci));
+                    const float* cj = dc.far + j0;
+                    tc::wait_ld();
+                    tc::after_wait(gv);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) {
+                        const ulonglong2 ca = *reinterpret_cast<const ulonglong2*>(cj + k);
+                        const ulonglong2 cb = *reinterpret_cast<const ulonglong2*>(cj + k + 4);
+                        const pair_t c2[4] = {ca.x, ca.y, cb.x, cb.y};
+                        pair_t v[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            v[q] = pmul(pk(__uint_as_float(gv[k + 2 * q]), __uint_as_float(gv[k + 2 * q + 1])), pmul(ci2, c2[q]));
+                        put(k, v);
+                    }
                 }
             }
             tc::st16(trow + kColG + j0, m0);
@@ -686,7 +724,8 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
     if (warp == 0) tc::dealloc(tbase, kTmemCols);
 }
 
-template <bool SOFTPLUS>
+// CUT: sequences may be cut into chunks.
+template <bool CUT>
 __global__ void __launch_bounds__(kThreads, 1) ssd_packed_kernel(const PackedParams p, const __grid_constant__ SsdMaps maps) {
     extern __shared__ __align__(1024) unsigned char ssd_smem[];
     unsigned char* smem = ssd_smem + ((1024u - (smem_u32(ssd_smem) & 1023u)) & 1023u);
@@ -703,9 +742,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssd_packed_kernel(const PackedPar
     tk.g = tk.d0 / (int)p.group_dim;
     tk.ci0 = tk.d0 - tk.g * (int)p.group_dim;
     tk.nch = kP;
-    const Run run = find_run<bf16>(p, blockIdx.x / p.n_tiles, reinterpret_cast<int64_t*>(smem), kThreads, tk);
-    if (run == kRunFull) run_head<false, SOFTPLUS>(p, maps, tk, smem);
-    else if (run == kRunLocal) run_head<true, SOFTPLUS>(p, maps, tk, smem);
+    const Run run = find_run<bf16, CUT>(p, blockIdx.x / p.n_tiles, reinterpret_cast<int64_t*>(smem), kThreads, tk);
+    if (run == kRunFull) run_head<false>(p, maps, tk, smem);
+    if constexpr (CUT)
+        if (run == kRunLocal) run_head<true>(p, maps, tk, smem);
 }
 
 }  // namespace
@@ -728,7 +768,7 @@ int ssd_packed_launch(PackedParams& p, cudaStream_t s) {
             !rows(&maps.out, p.out, p.dim, kP) || (p.z && !rows(&maps.z, p.z, p.dim, kP)))
             return SSM_ERR_CUDA;
     }
-    auto* kernel = p.softplus ? ssd_packed_kernel<true> : ssd_packed_kernel<false>;
+    auto* kernel = p.chunk > 0 ? ssd_packed_kernel<true> : ssd_packed_kernel<false>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
         return SSM_ERR_CUDA;
     for (p.phase = 1; p.phase <= (p.chunk > 0 ? 2 : 1); ++p.phase) {

@@ -91,7 +91,7 @@ def spread(v, dim, axis=0):
     return np.repeat(v, dim // v.shape[axis], axis) if v.shape[axis] != dim else v
 
 
-def tensor_err(p, h0, A, delta, bias, lo, hi, dim):
+def tensor_err(p, h0, A, delta, bias, lo, hi, dim, stretch_sums=True):
     """What the tensor-core form adds to the errors of the recurrence: for every token of a sequence a bound
     for y ahead of the gate, and one for the state behind it.  mag is the sum of the magnitudes that make up
     the state.
@@ -100,7 +100,8 @@ def tensor_err(p, h0, A, delta, bias, lo, hi, dim):
         magnitudes.  The state takes 24 steps a block, y 32, G 8.
       * M and the state enter as two bf16 terms: 2^-18 of each product; X' as three: 2^-24 (in the steps')
       * the decay between two steps of a stretch is 2^(difference of two sums of at most 32 terms a): off by
-        2 * 32 u max|sum|, relative
+        2 * 32 u max|sum|, relative.  Without `stretch_sums` it is held to what no sum's size enters: a decay
+        that is not zero in fp32 is 2^-s, s < 127, whose sum of up to 14 roundings is off by 14 * 127 u ln 2 < 2^-13
     """
     mag, state, y = np.abs(h0), 24 * 2.0 ** -22, []
     a_abs = []
@@ -111,11 +112,11 @@ def tensor_err(p, h0, A, delta, bias, lo, hi, dim):
         a_abs.append(a.max())
         stretch = max(sum(a_abs[max(0, k - 31):k + 1]) for k in range(max(0, len(a_abs) - 32), len(a_abs)))
         mag = np.exp(dt[:, None] * A) * mag + np.abs((dt * p["u"][:, t])[:, None] * spread(p["B"][:, :, t], dim))
-        y.append((2.0 ** -18 + 40 * 2.0 ** -22 + 64 * U * stretch) * (np.abs(spread(p["C"][:, :, t], dim)) * mag).sum(1))
+        y.append((2.0 ** -18 + 40 * 2.0 ** -22 + (64 * U * stretch if stretch_sums else 2.0 ** -13)) * (np.abs(spread(p["C"][:, :, t], dim)) * mag).sum(1))
     return y, state * mag
 
 
-def scan_packed(p, bounds, slots, has, pool, out, chunk=0, tensor=False):
+def scan_packed(p, bounds, slots, has, pool, out, chunk=0, tensor=False, stretch_sums=True):
     """p: u, delta, A, B, C, D, z, delta_bias, softplus.  `chunk`: tokens of a chunk where sequences are cut;
     the join's product of decays comes from a sum of up to `chunk` dt, whose rounding (chunk u, relative)
     moves exp(-x) by at most 0.37 chunk u, once per chunk.  `tensor`: the shape runs on the tensor cores."""
@@ -143,7 +144,8 @@ def scan_packed(p, bounds, slots, has, pool, out, chunk=0, tensor=False):
                 p["z"][:, t] if p["z"] is not None else None, bias, p["softplus"])
             top = np.maximum(top, np.abs(h)) if t > lo else np.abs(h)
         if tensor:
-            more, state = tensor_err(p, before[slots[i]] if has[i] else np.zeros_like(h), A, delta, bias, lo, hi, dim)
+            more, state = tensor_err(p, before[slots[i]] if has[i] else np.zeros_like(h), A, delta, bias, lo, hi, dim,
+                                     stretch_sums)
             for t, m in zip(range(lo, hi), more):
                 err_out[:, t] += m * (np.abs(silu(p["z"][:, t])) if p["z"] is not None else 1.0)
             err = err + state

@@ -914,3 +914,28 @@ def test_scan_packed_cut_with_shared_tokens(ssm, dim, heads, N, T, many):
     alone = sp.scan_packed(_plain(p), [(0, T)], [0], [0], np.zeros((1, dim, N)), np.zeros((dim, T)),
                            tensor=_tensor(dim, heads, N, "bf16", T, n))
     sp.check(f64(out)[:, :5], alone[0][:, :5], alone[1][:, :5], "bf16", "out")
+
+
+@pytest.mark.parametrize("dim,heads,head", [(64, 1, 0), (128, 2, 5)])
+@pytest.mark.parametrize("softplus", [True, False])
+@pytest.mark.parametrize("cut", [False, True])
+def test_scan_packed_large_steps(ssm, dim, heads, head, softplus, cut):
+    """Steps of a hundred and more among small ones: what decays to nothing leaves the others' weights as they
+    are, however far the sums within a stretch run."""
+    gen = torch.Generator().manual_seed(33)
+    lens = [900, 40, 302] if cut else [150, 40, 302]
+    cu, total, bounds = packing(lens, head)
+    p = _scan_inputs(gen, total, dim, heads, 1, 128, "bf16", softplus=softplus)
+    big = torch.rand(heads, total, generator=gen).cuda()
+    steps = torch.where(big > 0.7, 400 * (big - 0.7) / 0.3, 0.05 + 0.1 * big)
+    p["delta"] = (torch.where(steps > 20, steps, torch.log(torch.expm1(steps))) if softplus else steps).to(torch.bfloat16)
+    p["delta_bias"] = None
+    p["A"] = torch.tensor([-16.0, -0.7][:heads]).cuda()
+    hint = 900 if cut else 302
+    assert (_chunk(ssm, p, 3, hint) > 0) == cut
+    states, out = rnd(gen, 3, dim, 128), rnd(gen, dim, total, dtype="bf16")
+    ref, err, ref_pool, pool_err = sp.scan_packed(_plain(p), bounds, [0, 1, 2], [1, 0, 1], f64(states), f64(out),
+                                                  chunk=128 if cut else 0, tensor=True, stretch_sums=False)
+    got = _call(ssm, p, i32(cu), states, out, has_state=torch.tensor([1, 0, 1], dtype=torch.uint8).cuda(), max_seqlen=hint)
+    sp.check(f64(got), ref, err, "bf16", "out")
+    sp.check(f64(states), ref_pool, pool_err, "f32", "states")
