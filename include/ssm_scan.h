@@ -475,9 +475,9 @@ int ssm_causal_conv1d_update(int64_t batch, int64_t dim, int32_t width, int32_t 
  * one workspace must not serve two calls at once, nor two graphs that may run at once.
  *
  * bf16 I/O with nheads < dim, dim / nheads == 64 and dstate 128 runs on the tensor cores once the
- * sequences are 32 tokens or more in the mean, in blocks of 128 tokens: there a NaN or infinity in
- * a token of u reaches every token of its block and sequence, the earlier ones too, and a wait for
- * the tensor cores or a copy that runs out (half a second) leaves NaN in the rest of that head's outputs.
+ * sequences are 32 tokens or more in the mean, in blocks of 128 tokens: there an infinity in u makes
+ * NaN, not infinities, of its channel's state and outputs from its token on, and a wait for the tensor
+ * cores or a copy that runs out (half a second) leaves NaN in the rest of that head's outputs.
  *
  * out must not overlap an input or the pool.  SSM_ERR_INVALID_ARG for a bad shape or stride, a pointer off its
  * element's alignment, a workspace that is too small, or a NULL A, cu_seqlens, states, or u,

@@ -11,7 +11,9 @@
 //   Y  = M X + diag(2^s(i, start)) (C H)             (Q x P)     out = (Y + D x) silu(z)
 //
 // Steps outside the sequence have dt = 0 and their rows of B, C and X are zeroed in shared memory,
-// so that no value there, NaN included, reaches a product.
+// so that no value there, NaN included, reaches a product.  A NaN or an infinity of the sequence's own u
+// would reach the outputs of earlier steps through M's zeros: where the state turns out not to be finite,
+// X is cleared of them and Y made again (no cost elsewhere: a sum of 16 values in four of the warps).
 //
 // Precision.  B, C and X are bf16 and enter exactly.  X' is split into three bf16 terms (24 bits),
 // so the state is summed as exactly as in fp32; M and H into two (16 bits, 2^-17 of each product),
@@ -78,7 +80,8 @@ constexpr int OFF_H = 144 * 1024;              // two terms of 128 x 64
 constexpr int OFF_Z = 176 * 1024;              // z, then the outputs
 constexpr int OFF_DEC = 192 * 1024;            // two blocks' Decay
 constexpr int OFF_BAR = OFF_DEC + 2 * 4096;
-constexpr int kSmem = OFF_BAR + 256 + 1024;    // and room to align the base
+constexpr int OFF_BAD = OFF_BAR + 256;         // what of X is not finite
+constexpr int kSmem = OFF_BAD + 256 + 1024;   // and room to align the base
 
 // A block's decay over its 128 steps, in stretches of 32 and groups of four: head, a, pre and the whole
 // groups and stretches in log2 units, the others weights.
@@ -117,6 +120,28 @@ __device__ __forceinline__ void store_split8(unsigned char* tile, int step, uint
     split8<K>(v, [&](int k, const uint32_t (&w)[4]) {
         *reinterpret_cast<uint4*>(to + k * step) = make_uint4(w[0], w[1], w[2], w[3]);
     });
+}
+
+// The first step of a block whose u is not finite, per channel (kQ: none).
+struct Bad {
+    int first[kP];
+};
+static_assert(sizeof(Bad) <= 256, "fits its place");
+
+// Notes what of a block's X is not finite and clears it; returns whether this thread met any.
+__device__ __noinline__ bool clear_bad(Bad& bad, unsigned char* tile) {
+    bool met = false;
+    for (uint32_t i = threadIdx.x; i < kP * 16; i += kThreads) {
+        const uint32_t p = i >> 4, s = (i & 15u) * 8u;
+        unsigned short* v = reinterpret_cast<unsigned short*>(tile + (s >> 6) * 8192 + tc::sw128_off(p, s & 63u));
+        for (uint32_t e = 0; e < 8; ++e)
+            if ((v[e] & 0x7F80u) == 0x7F80u) {
+                v[e] = 0;
+                atomicMin(&bad.first[p], (int)(s + e));
+                met = true;
+            }
+    }
+    return met;
 }
 
 struct Block {
@@ -293,7 +318,9 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
     uint64_t *mb_s = mb_g + 1, *mb_y = mb_g + 2, *mb_x = mb_g + 3, *mb_bc = mb_g + 4, *mb_z = mb_g + 5;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(mb_g + 6);
     int* status = reinterpret_cast<int*>(mb_g + 7);
+    uint64_t* mb_fix = mb_g + 8;
     Decay* dec = reinterpret_cast<Decay*>(smem + OFF_DEC);
+    Bad& bad = *reinterpret_cast<Bad*>(smem + OFF_BAD);
     static_assert(OFF_DEC % 16 == 0, "vector reads of the decay");
     unsigned char *sC = smem + OFF_C, *sB = smem + OFF_B, *sXw = smem + OFF_XW, *sH = smem + OFF_H, *sZ = smem + OFF_Z;
 
@@ -376,8 +403,10 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
 
     tc::fence_async_smem();                             // (the item search wrote where boxes will)
     __syncthreads();
+    if (!LOCAL && tid < kP) bad.first[tid] = kQ;
     if (tid == 0) {
         for (uint64_t* b = mb_g; b <= mb_z; ++b) mbar_init(b, 1);
+        mbar_init(mb_fix, 1);
         *status = SSM_OK;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -435,7 +464,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
         last_bar = bar;
         last_ph = ph;
     };
-    // X' of a block, in three terms: two 8-step pieces of a channel per thread
+    // X' of a block, in three terms: two 8-step pieces of a channel per thread.
     auto make_xw = [&](int c) {
         const Decay& dc = dec[c & 1];
         const unsigned char* sX = smem + OFF_X + (c & 1) * 16384;
@@ -482,6 +511,20 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
         }
         commit(mb_s, ph);
     };
+    // Y of a block, by one thread
+    auto issue_y = [&](int c, uint64_t* bar, unsigned ph) {
+        tc::fence_after();
+        constexpr uint32_t id = tc::idesc_bf16(128, kP, false, false);
+        const uint64_t b = tc::desc(smem + OFF_X + (c & 1) * 16384, 16, 1024, tc::kSwizzle128);
+#pragma unroll
+        for (int kk = 0; kk < kQ / 16; ++kk)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                tc::mma_bf16_ta(tbase + kColY, tbase + kColG + (kk >> 1) * 32 + s * 16 + (kk & 1) * 8,
+                                b + (kk >> 2) * (8192 >> 4) + (kk & 3) * 2, id, kk > 0 || s > 0 ? 1u : 0u);
+        commit(bar, ph);
+    };
+    unsigned ph_fix = 0u;
     if (nblk > 0) make_xw(0);
     tc::fence_async_smem();
     __syncthreads();
@@ -499,6 +542,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
         const unsigned char* sX = smem + OFF_X + (c & 1) * 16384;
         const bool with_state = c > 0 || start_state;
         if (warp == kDecayWarp && c + 1 < nblk) block_decay(p, delta, block(c + 1), Ah, bias, lane, dec[(c + 1) & 1]);
+        bool found = false, spoiled = false;            // the block's u may hold, holds what is not finite
         ok = true;
         if constexpr (!LOCAL) {
             // ---- M, in two terms over G: row i = row, steps j0 .. (S and C H run)
@@ -586,18 +630,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
         // (a wait that ran out is voted on before anything overwrites what the products may still read)
         if (__syncthreads_or(!ok)) break;
         if constexpr (!LOCAL) {
-            if (warp == kIssueWarp && tc::elect_one()) {
-                tc::fence_after();
-                constexpr uint32_t id = tc::idesc_bf16(128, kP, false, false);
-                const uint64_t b = tc::desc(sX, 16, 1024, tc::kSwizzle128);
-#pragma unroll
-                for (int kk = 0; kk < kQ / 16; ++kk)
-#pragma unroll
-                    for (int s = 0; s < 2; ++s)
-                        tc::mma_bf16_ta(tbase + kColY, tbase + kColG + (kk >> 1) * 32 + s * 16 + (kk & 1) * 8,
-                                        b + (kk >> 2) * (8192 >> 4) + (kk & 3) * 2, id, kk > 0 || s > 0 ? 1u : 0u);
-                commit(mb_y, ph);
-            }
+            if (warp == kIssueWarp && tc::elect_one()) issue_y(c, mb_y, ph);
             __syncwarp();
         }
         if constexpr (!LOCAL) stage_z(c);
@@ -620,6 +653,13 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
 #pragma unroll
             for (int k = 0; k < 16; ++k)
                 H[k] = fmaf(d, H[k], __uint_as_float(s0[k]) + (__uint_as_float(s1[k]) + __uint_as_float(s2[k])));
+            // what is not finite in X' is so in every row of the state then: one of them tells
+            if (!LOCAL && quarter == 2) {
+                float sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) sum += H[k];
+                found = !(sum * 0.f == 0.f);
+            }
             if constexpr (!LOCAL) {
                 store_state();
                 if (with_state) {
@@ -640,7 +680,22 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
             ok = mbar_wait(mb_y, ph, kWaitNs, status);
             tc::fence_after();
             ok = wait_box(due_z, mb_z, ph_z) && ok;
-            if (__syncthreads_or(!ok)) break;
+            if (__syncthreads_or(!ok || found)) {
+                if (__syncthreads_or(!ok)) break;
+                // M's zeros do not keep an infinity or a NaN in X from the outputs of earlier steps (0 * NaN):
+                // X is cleared of it, Y made again, and the outputs from its step on are NaN
+                const bool met = clear_bad(bad, smem + OFF_X + (c & 1) * 16384);
+                tc::fence_async_smem();
+                spoiled = __syncthreads_or(met);
+                if (spoiled) {
+                    if (warp == kIssueWarp && tc::elect_one()) issue_y(c, mb_fix, ph_fix);
+                    __syncwarp();
+                    ok = mbar_wait(mb_fix, ph_fix, kWaitNs, status);
+                    ph_fix ^= 1u;
+                    if (__syncthreads_or(!ok)) break;
+                    tc::fence_after();
+                }
+            }
             // ---- outputs of step row, channels p0 ..
             uint32_t yv[16];
             tc::ld16(trow + kColY + p0, yv);
@@ -676,12 +731,23 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
                 const __nv_bfloat162 t = __floats2bfloat162_rn(f.x, f.y);
                 *zo = *reinterpret_cast<const uint32_t*>(&t);
             }
+            if (spoiled) {
+                // from a channel's first step that is not finite on
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t ch = p0 + i / 4 * 8 + i % 4 + (odd ? 4u : 0u);
+                    uint32_t* zo = reinterpret_cast<uint32_t*>(zt + tc::sw128_off(ch, row & 62u));
+                    const int from = bad.first[ch], step = (int)(row & 126u);
+                    if (step >= from) *zo = 0x7FC07FC0u;
+                    else if (step + 1 >= from) *zo = (*zo & 0xFFFFu) | 0x7FC00000u;
+                }
+            }
         }
         ok = wait_bc(c + 1);
         tc::fence_async_smem();
         tc::fence_before();
         if (__syncthreads_or(!ok)) break;
         if constexpr (!LOCAL) {
+            if (spoiled && tid < kP) bad.first[tid] = kQ;
             if (!grid || !inside(c)) {
                 store_out(sZ, out, L, block(c), grid);
             } else if (warp == kCopyWarp && tc::elect_one()) {

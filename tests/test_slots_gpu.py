@@ -939,3 +939,61 @@ def test_scan_packed_large_steps(ssm, dim, heads, head, softplus, cut):
     got = _call(ssm, p, i32(cu), states, out, has_state=torch.tensor([1, 0, 1], dtype=torch.uint8).cuda(), max_seqlen=hint)
     sp.check(f64(got), ref, err, "bf16", "out")
     sp.check(f64(states), ref_pool, pool_err, "f32", "states")
+
+
+@pytest.mark.parametrize("dim,heads,N", [(128, 2, 128), (32, 32, 16)])
+@pytest.mark.parametrize("lens,head", [([300, 70, 260], 0), ([299, 70, 258], 3), ([1200, 40], 0), ([1201, 40], 1)])
+def test_scan_packed_not_finite_inputs_stay_behind(ssm, dim, heads, N, lens, head):
+    """NaN and infinities in u, delta, B, C and z spoil what the recurrence lets them spoil: no earlier token, no
+    other channel, with C and z no later token either."""
+    gen = torch.Generator().manual_seed(34)
+    cu, total, bounds = packing(lens, head)
+    n = len(lens)
+    p = _scan_inputs(gen, total, dim, heads, 1, N, "bf16")
+    cut = _chunk(ssm, p, n, max(lens)) > 0
+    assert cut == (lens[0] > 1000)
+    start = rnd(gen, n, dim, N)
+    ref, err, ref_pool, pool_err = sp.scan_packed(_plain(p), bounds, list(range(n)), [1] * n, f64(start), np.zeros((dim, total)),
+                                                  chunk=128 if cut else 0, tensor=_tensor(dim, heads, N, "bf16", total, n))
+    flags = torch.ones(n, dtype=torch.uint8).cuda()
+    nan, inf = float("nan"), float("inf")
+
+    def run(q):
+        states = start.clone()
+        out = _call(ssm, q, i32(cu), states, None, has_state=flags, max_seqlen=max(lens))
+        return f64(out), f64(states)
+
+    # u: single channels, at the edges of blocks, stretches and groups, several in one block
+    lo = bounds[0][0]
+    places = [(3, lo, nan), (5, lo + 1, inf), (17, lo + 31, -inf), (18, lo + 32, nan), (30, lo + 127, nan), (31, lo + 128, inf),
+              (8, lo + 200, nan), (8, lo + 203, nan), (9, bounds[0][1] - 1, nan), (11, bounds[1][0] + 37, -inf),
+              (12, bounds[-1][0] + 5, nan), (12, bounds[-1][1] - 1, inf)]
+    if dim > 32:
+        places += [(64, lo + 64, nan), (127, lo + 255, inf), (100, bounds[1][1] - 1, nan)]
+    q = dict(p, u=p["u"].clone())
+    good, live = np.ones((dim, total), bool), np.ones((n, dim), bool)
+    for c, t, v in places:
+        q["u"][c, t] = v
+        s = next(i for i, (a, b) in enumerate(bounds) if a <= t < b)
+        good[c, t:bounds[s][1]] = False
+        live[s, c] = False
+    got, states = run(q)
+    assert not np.isfinite(got[~good]).any() and not np.isfinite(states[~live]).any()
+    sp.check(np.where(good, got, 0.0), np.where(good, ref, 0.0), err, "bf16", "out")
+    sp.check(np.where(live[:, :, None], states, 0.0), np.where(live[:, :, None], ref_pool, 0.0), pool_err, "f32", "states")
+    # one token of the others, everything behind it in its sequence (C, z: that token alone)
+    for k, after in (("delta", True), ("B", True), ("C", False), ("z", False)):
+        for s, at in ((0, 0), (0, 63), (0, 161), (1, 33), (n - 1, 5)):
+            a, b = bounds[s]
+            t = min(a + at, b - 1)
+            q = dict(p, **{k: p[k].clone()})
+            q[k][..., t] = nan
+            got, states = run(q)
+            good = np.ones((dim, total), bool)
+            good[:, t:b if after else t + 1] = False
+            assert not np.isfinite(got[~good]).any(), (k, t)
+            sp.check(np.where(good, got, 0.0), np.where(good, ref, 0.0), err, "bf16", f"out, {k} at {t}")
+            ok = np.ones(n, bool)
+            ok[s] = not after
+            sp.check(states[ok], ref_pool[ok], pool_err[ok], "f32", "states")
+            assert ok[s] or not np.isfinite(states[s]).any()
