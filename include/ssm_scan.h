@@ -477,7 +477,8 @@ int ssm_causal_conv1d_update(int64_t batch, int64_t dim, int32_t width, int32_t 
  * bf16 I/O with nheads < dim, dim / nheads == 64 and dstate 128 runs on the tensor cores once the
  * sequences are 32 tokens or more in the mean, in blocks of 128 tokens: there an infinity in u makes
  * NaN, not infinities, of its channel's state and outputs from its token on, and a wait for the tensor
- * cores or a copy that runs out (half a second) leaves NaN in the rest of that head's outputs.
+ * cores or a copy that runs out (half a second) leaves NaN in the rest of that head's outputs and in its
+ * state, and SSM_ERR_TIMEOUT for ssm_selective_scan_packed_device_status.
  *
  * out must not overlap an input or the pool.  SSM_ERR_INVALID_ARG for a bad shape or stride, a pointer off its
  * element's alignment, a workspace that is too small, or a NULL A, cu_seqlens, states, or u,
@@ -491,6 +492,21 @@ int ssm_selective_scan_packed_fwd(const ssm_dims_t* dims, const void* u, const v
                                   const int32_t* slots, const uint8_t* has_state, float* states,
                                   int64_t n_slots, int64_t slot_stride, int64_t max_seqlen, void* out,
                                   void* workspace, size_t workspace_bytes, ssm_stream_t stream);
+
+/*
+ * Synchronise `stream` and return the kernel-side status (SSM_OK, SSM_ERR_TIMEOUT) of the current
+ * device's ssm_selective_scan_packed_fwd calls since the last such read, and clear it.  One word
+ * serves every stream of the device.  Not to be called while a stream is captured.
+ */
+int ssm_selective_scan_packed_device_status(ssm_stream_t stream);
+
+/*
+ * Test hook for the calls on the tensor cores that follow.  stall nonzero: in every sequence or chunk
+ * of more than 256 tokens the third block waits for what never comes, so that the wait runs out.
+ * wait_budget_us > 0 replaces the limit of a wait, 0 restores it.  SSM_ERR_INVALID_ARG for a budget
+ * outside [0, 10 s].
+ */
+int ssm_selective_scan_packed_test_hooks(int stall, int64_t wait_budget_us);
 
 /*
  * ssm_selective_state_update with the states in slots of a pool: row b's state is slot slots[b],

@@ -42,7 +42,8 @@ from ._abi import (SSM_BF16, SSM_ERR_BOUNDS, SSM_ERR_CUDA, SSM_ERR_INVALID_ARG, 
                    GRAD_NAMES,
                    ssm_status_string,
                    ssm_causal_conv1d_packed_fwd, ssm_causal_conv1d_update, ssm_selective_scan_packed_workspace_size,
-                   ssm_selective_scan_packed_fwd, ssm_selective_state_update_slots, ssm_state_slots_copy,
+                   ssm_selective_scan_packed_fwd, ssm_selective_scan_packed_device_status,
+                   ssm_selective_scan_packed_test_hooks, ssm_selective_state_update_slots, ssm_state_slots_copy,
                    ssm_causal_conv1d_bwd_workspace_size, ssm_causal_conv1d_bwd)
 from .slots import (causal_conv1d_packed, causal_conv1d_update, selective_scan_packed,  # noqa: F401
                     selective_state_update_slots, state_slots_copy)
@@ -64,6 +65,7 @@ __all__ = ["selective_scan_fwd", "selective_scan_fwd_host", "selective_scan_fn",
            "causal_conv1d_packed", "causal_conv1d_update", "selective_scan_packed", "selective_state_update_slots",
            "state_slots_copy", "ssm_causal_conv1d_packed_fwd", "ssm_causal_conv1d_update",
            "ssm_selective_scan_packed_workspace_size", "ssm_selective_scan_packed_fwd",
+           "ssm_selective_scan_packed_device_status", "ssm_selective_scan_packed_test_hooks",
            "ssm_selective_state_update_slots", "ssm_state_slots_copy"]
 
 

@@ -35,7 +35,8 @@ EXPORTS = ("ssm_scan_plan", "ssm_selective_scan_fwd", "ssm_selective_scan_fwd_h0
            "ssm_scan_plan_schedule", "ssm_scan_destroy",
            "ssm_scan_device_status", "ssm_status_string", "ssm_scan_plan_info", "ssm_probe_ex2",
            "ssm_causal_conv1d_packed_fwd", "ssm_causal_conv1d_update", "ssm_selective_scan_packed_workspace_size",
-           "ssm_selective_scan_packed_fwd", "ssm_selective_state_update_slots", "ssm_state_slots_copy",
+           "ssm_selective_scan_packed_fwd", "ssm_selective_scan_packed_device_status",
+           "ssm_selective_scan_packed_test_hooks", "ssm_selective_state_update_slots", "ssm_state_slots_copy",
            "ssm_causal_conv1d_bwd_workspace_size", "ssm_causal_conv1d_bwd")
 
 SSM_OPT_SPIN_LIMIT = 1
@@ -100,6 +101,8 @@ def load_library(path: Optional[str] = None):
     lib.ssm_causal_conv1d_update.argtypes = [i64, i64, i32, i32, vp, vp, vp, i32, vp, vp, i64, i64, vp, vp]
     lib.ssm_selective_scan_packed_workspace_size.argtypes = [dims_p, i64, ctypes.POINTER(sz)]
     lib.ssm_selective_scan_packed_fwd.argtypes = [dims_p] + [vp] * 8 + [i32, vp, vp, vp, vp, i64, i64, i64, vp, vp, sz, vp]
+    lib.ssm_selective_scan_packed_device_status.argtypes = [vp]
+    lib.ssm_selective_scan_packed_test_hooks.argtypes = [i32, i64]
     lib.ssm_selective_state_update_slots.argtypes = [dims_p, vp, vp, i64, i64] + [vp] * 8 + [i32, vp, vp]
     lib.ssm_state_slots_copy.argtypes = [vp, i64, i64, i64, i64, i64, vp, vp, i64, vp]
     lib.ssm_causal_conv1d_bwd_workspace_size.argtypes = [i64, i64, i64, i32, i32, ctypes.POINTER(sz)]
@@ -278,6 +281,17 @@ def ssm_selective_scan_packed_fwd(dims: ssm_dims_t, u, delta, A, B, C, D, z, del
         1 if softplus else 0, _ptr(cu_seqlens), _ptr(slots), _ptr(has_state), _ptr(states), n_slots, slot_stride,
         max_seqlen, _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream))
     return _check(rc, "ssm_selective_scan_packed_fwd") if check else rc
+
+
+def ssm_selective_scan_packed_device_status(stream=None) -> int:
+    """Kernel-side status of the current device's packed scans since the last read (synchronises the stream)."""
+    return int(load_library().ssm_selective_scan_packed_device_status(_stream(stream)))
+
+
+def ssm_selective_scan_packed_test_hooks(stall: bool, wait_budget_us: int = 0) -> int:
+    """Test hook: make the waits of the packed scans on the tensor cores run out (see include/ssm_scan.h)."""
+    return _check(load_library().ssm_selective_scan_packed_test_hooks(1 if stall else 0, int(wait_budget_us)),
+                  "ssm_selective_scan_packed_test_hooks")
 
 
 def ssm_selective_state_update_slots(dims: ssm_dims_t, states, slots, n_slots: int, slot_stride: int, u, delta, A, B, C,

@@ -67,6 +67,8 @@ struct PackedParams {
     unsigned tiles_per_group, n_tiles;
     int softplus, phase, state_vec;
     int grid16;              // every row starts on the 16-byte grid
+    int stall;               // tensor cores: the block whose wait runs out (a test's), and the limit of waits
+    uint64_t wait_ns;
 };
 
 template <typename T, int N, bool HEAD, bool ALIGNED, bool CUT = true>

@@ -42,11 +42,12 @@
 // have left.  Rows off the 16-byte grid are shifted into place through registers.
 //
 // Every wait for the tensor cores or a copy is bounded; one that ran out ends the CTA's work with NaN in the
-// rest of its outputs.
+// rest of its outputs and is recorded in the device's status word.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "layout.h"            // encode_rows
@@ -69,7 +70,14 @@ constexpr uint32_t kTmemCols = 512;
 // TMEM columns.  M's two terms lie where G was, 16 columns each for a stretch's 32 steps: each thread
 // writes what it has read.  C H and S keep the products of H's and X' terms apart.
 constexpr uint32_t kColG = 0, kColY = 128, kColCH = 192, kColS = 320;
-constexpr uint64_t kWaitNs = 500000000ull;
+constexpr int64_t kWaitUs = 500000;
+
+// Kernel-side status of the device's calls since it was last read.
+__device__ int g_status;
+// Test hooks: the block, of even number, that waits for nothing instead of its products (-1: none), and the
+// limit of a wait.
+std::atomic<int> g_stall{-1};
+std::atomic<int64_t> g_wait_us{kWaitUs};
 
 // shared memory (bytes from a 1024-aligned base); a tile is two 64-step halves of rows of 128 bytes
 constexpr int OFF_C = 0;                       // 128 states
@@ -348,7 +356,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
     bool due_x = false, due_bc = false, due_z = false;   // boxes are on their way
     auto wait_box = [&](bool& due, uint64_t* bar, unsigned& phase) {
         if (!due) return true;
-        if (!mbar_wait(bar, phase, kWaitNs, status)) return false;
+        if (!mbar_wait(bar, phase, p.wait_ns, status)) return false;
         phase ^= 1u;
         due = false;
         return true;
@@ -546,7 +554,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
         ok = true;
         if constexpr (!LOCAL) {
             // ---- M, in two terms over G: row i = row, steps j0 .. (S and C H run)
-            ok = mbar_wait(mb_g, ph, kWaitNs, status);
+            ok = mbar_wait(mb_g, ph, p.wait_ns, status);
             __syncwarp();
             tc::fence_after();
             uint32_t m0[16], m1[16];
@@ -623,7 +631,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
             tc::st16(trow + kColG + j0 + 16, m1);
             tc::wait_st();
         }
-        ok = mbar_wait(mb_s, ph, kWaitNs, status) && ok;
+        ok = mbar_wait(c == p.stall ? mb_fix : mb_s, ph, p.wait_ns, status) && ok;
         tc::fence_after();
         ok = wait_x(c + 1) && ok;
         tc::fence_before();
@@ -677,7 +685,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
         // ---- X' of the next block
         if (c + 1 < nblk) make_xw(c + 1);
         if constexpr (!LOCAL) {
-            ok = mbar_wait(mb_y, ph, kWaitNs, status);
+            ok = mbar_wait(mb_y, ph, p.wait_ns, status);
             tc::fence_after();
             ok = wait_box(due_z, mb_z, ph_z) && ok;
             if (__syncthreads_or(!ok || found)) {
@@ -690,7 +698,7 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
                 if (spoiled) {
                     if (warp == kIssueWarp && tc::elect_one()) issue_y(c, mb_fix, ph_fix);
                     __syncwarp();
-                    ok = mbar_wait(mb_fix, ph_fix, kWaitNs, status);
+                    ok = mbar_wait(mb_fix, ph_fix, p.wait_ns, status);
                     ph_fix ^= 1u;
                     if (__syncthreads_or(!ok)) break;
                     tc::fence_after();
@@ -766,7 +774,8 @@ __device__ __forceinline__ void run_head(const PackedParams& p, const SsdMaps& m
     // a wait ran out: the products may still be under way, so wait (bounded) for the last batch
     // before TMEM and shared memory go; the outputs that are missing become NaN
     if (done < nblk) {
-        if (last_bar) mbar_wait(last_bar, last_ph, kWaitNs, status);
+        if (tid == 0) atomicCAS(&g_status, SSM_OK, SSM_ERR_TIMEOUT);
+        if (last_bar) mbar_wait(last_bar, last_ph, p.wait_ns, status);
         wait_box(due_x, mb_x, ph_x);
         wait_box(due_bc, mb_bc, ph_bc);
         wait_box(due_z, mb_z, ph_z);
@@ -834,6 +843,8 @@ int ssd_packed_launch(PackedParams& p, cudaStream_t s) {
             !rows(&maps.out, p.out, p.dim, kP) || (p.z && !rows(&maps.z, p.z, p.dim, kP)))
             return SSM_ERR_CUDA;
     }
+    p.wait_ns = (uint64_t)g_wait_us.load() * 1000u;
+    p.stall = g_stall.load();
     auto* kernel = p.chunk > 0 ? ssd_packed_kernel<true> : ssd_packed_kernel<false>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
         return SSM_ERR_CUDA;
@@ -846,3 +857,24 @@ int ssd_packed_launch(PackedParams& p, cudaStream_t s) {
 
 }  // namespace packed
 }  // namespace ssm
+
+extern "C" int ssm_selective_scan_packed_device_status(ssm_stream_t stream) {
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int status = SSM_OK;
+    const int clear = SSM_OK;
+    if (cudaMemcpyFromSymbolAsync(&status, ssm::packed::g_status, sizeof status, 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+        return SSM_ERR_CUDA;
+    if (status != SSM_OK &&
+        (cudaMemcpyToSymbolAsync(ssm::packed::g_status, &clear, sizeof clear, 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+         cudaStreamSynchronize(s) != cudaSuccess))
+        return SSM_ERR_CUDA;
+    return status;
+}
+
+extern "C" int ssm_selective_scan_packed_test_hooks(int stall, int64_t wait_budget_us) {
+    if (wait_budget_us < 0 || wait_budget_us > 10000000) return SSM_ERR_INVALID_ARG;
+    ssm::packed::g_stall.store(stall ? 2 : -1);
+    ssm::packed::g_wait_us.store(wait_budget_us ? wait_budget_us : ssm::packed::kWaitUs);
+    return SSM_OK;
+}

@@ -43,7 +43,8 @@ def selective_scan_packed(u, delta, A, B, C, cu_seqlens, states, slots=None, has
     (ngroups, dstate, total) -> out.  Each sequence starts from its slot of states (n_slots, dim, dstate;
     fp32) where has_state is nonzero, else from zero, and leaves its final state there.  max_seqlen, if
     known, only saves the cutting of sequences that are all short.  The workspace (uint8, at least
-    ssm_selective_scan_packed_workspace_size bytes) must not serve two calls, or two graphs, at once."""
+    ssm_selective_scan_packed_workspace_size bytes) must not serve two calls, or two graphs, at once.
+    ssm_selective_scan_packed_device_status tells whether a kernel gave up on a wait."""
     f = load().scan_packed
     if stream is None:
         return f(u, delta, A, B, C, cu_seqlens, states, slots, has_state, D, z, delta_bias, softplus, max_seqlen, out,

@@ -318,3 +318,10 @@ def test_pointers_off_their_elements_are_refused(ssm):
                 off[i] = args[i] + 2
                 if name != "states" or fn is not ssm.ssm_causal_conv1d_packed_fwd:     # (that one's are bf16)
                     assert fn(*off, check=False) == inv, (fn.__name__, name)
+
+
+def test_packed_scan_hook_refusals(ssm):
+    lib = ssm.load_library()
+    for budget in (-1, 10 ** 7 + 1):
+        assert lib.ssm_selective_scan_packed_test_hooks(0, budget) == ssm.SSM_ERR_INVALID_ARG
+    assert ssm.ssm_selective_scan_packed_test_hooks(False) == ssm.SSM_OK

@@ -997,3 +997,33 @@ def test_scan_packed_not_finite_inputs_stay_behind(ssm, dim, heads, N, lens, hea
             ok[s] = not after
             sp.check(states[ok], ref_pool[ok], pool_err[ok], "f32", "states")
             assert ok[s] or not np.isfinite(states[s]).any()
+
+
+@pytest.mark.parametrize("total,heads", [(472, 2), (473, 2), (4096, 16)])
+def test_scan_packed_wait_that_runs_out_is_reported(ssm, total, heads):
+    """With the hook on, the third block of a sequence gives up its wait: NaN from there on in its outputs and
+    state, the status says so once, other sequences and the next call are as ever."""
+    gen = torch.Generator().manual_seed(35)
+    dim, N, short = 64 * heads, 128, 100
+    p = _scan_inputs(gen, total, dim, heads, 1, N, "bf16")
+    cu = i32([0, short, total])
+    cut = _chunk(ssm, p, 2, total - short) > 0
+    assert cut == (total > 1000)
+    want_s = torch.zeros(2, dim, N, device="cuda")
+    want = _call(ssm, p, cu, want_s, None, max_seqlen=total - short)
+    assert ssm.ssm_selective_scan_packed_device_status() == ssm.SSM_OK
+    ssm.ssm_selective_scan_packed_test_hooks(True, 1000)
+    try:
+        states = torch.zeros(2, dim, N, device="cuda")
+        out = _call(ssm, p, cu, states, None, max_seqlen=total - short)
+        assert ssm.ssm_selective_scan_packed_device_status() == ssm.SSM_ERR_TIMEOUT
+    finally:
+        ssm.ssm_selective_scan_packed_test_hooks(False)
+    assert ssm.ssm_selective_scan_packed_device_status() == ssm.SSM_OK
+    start = short - short % 8 if total % 8 == 0 else short     # where the sequence's first block lies
+    assert torch.equal(out[:, :start + 256], want[:, :start + 256]) and torch.equal(states[0], want_s[0])
+    assert torch.isnan(out[:, start + 256:]).all()
+    assert torch.isnan(states[1]).all()
+    again = torch.zeros(2, dim, N, device="cuda")
+    assert torch.equal(_call(ssm, p, cu, again, None, max_seqlen=total - short), want) and torch.equal(again, want_s)
+    assert ssm.ssm_selective_scan_packed_device_status() == ssm.SSM_OK
