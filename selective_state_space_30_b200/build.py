@@ -5,7 +5,8 @@
 The library is the product: kernels plus the C ABI declared in
 include/ssm_scan.h.  Each translation unit compiles in parallel, and beside them
 _front.so, the compiled torch front ends of the slot and convolution operators
-(csrc/front.cpp), which call the library's entry points.  --debug builds
+(csrc/front.cpp), which call the library's entry points.  Without torch the
+library is built alone.  --debug builds
 libssmscan_debug.so from the same sources with SSM_DEBUG defined: the scan
 kernels then check their indices against the buffers they touch and record
 SSM_ERR_BOUNDS in the device status word instead of making a bad access.
@@ -13,6 +14,7 @@ SSM_ERR_BOUNDS in the device status word instead of making a bad access.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
 import os
 import subprocess
 import sys
@@ -25,6 +27,7 @@ LIB = os.path.join(HERE, "libssmscan.so")
 LIB_DEBUG = os.path.join(HERE, "libssmscan_debug.so")
 FRONT = os.path.join(HERE, "_front.so")
 BUILD_DIR = os.path.join(HERE, "_build")
+FRONT_STAMP = os.path.join(BUILD_DIR, "_front.txt")
 BUILD_DIR_DEBUG = os.path.join(HERE, "_build_debug")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -48,6 +51,27 @@ def _compile(src: str, extra, build_dir=BUILD_DIR) -> str:
     return obj
 
 
+def _front_wants():
+    """What _front.so is built for beside its sources, torch's version and Python's; None without torch."""
+    try:
+        return f"torch {importlib.metadata.version('torch')}, Python {sys.version_info.major}.{sys.version_info.minor}"
+    except importlib.metadata.PackageNotFoundError:
+        return None
+
+
+def _front_stale() -> bool:
+    """Whether the front ends are to be built: sources newer than they are, or another torch or Python."""
+    wants = _front_wants()
+    if wants is None:
+        return False
+    try:
+        with open(FRONT_STAMP) as f:
+            built = f.read()
+    except OSError:
+        built = None
+    return built != wants or _stale(FRONT, [os.path.join(CSRC, "front.cpp"), os.path.join(INCLUDE, "ssm_scan.h")])
+
+
 def _compile_front() -> str:
     """The compiled front ends: host C++ against torch's headers; torch's libraries are loaded before it."""
     import sysconfig
@@ -61,6 +85,9 @@ def _compile_front() -> str:
     if res.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on front.cpp:\n{res.stderr[-4000:]}")
     os.replace(tmp, FRONT)
+    os.makedirs(os.path.dirname(FRONT_STAMP), exist_ok=True)
+    with open(FRONT_STAMP, "w") as f:
+        f.write(_front_wants() or "")
     return FRONT
 
 
@@ -77,24 +104,20 @@ def build(force: bool = False, extra=(), debug: bool = False) -> str:
     extra = list(extra) + (["-DSSM_DEBUG"] if debug else [])
     deps = sources() + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + \
         [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    front = force or _stale(FRONT, [os.path.join(CSRC, "front.cpp"), os.path.join(INCLUDE, "ssm_scan.h")])
-    if not force and not _stale(lib, deps):
-        if front:
-            _compile_front()
-        return lib
-    os.makedirs(build_dir, exist_ok=True)
-    srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        host = ex.submit(_compile_front) if front else None
-        objs = list(ex.map(lambda s: _compile(s, extra, build_dir), srcs))
-        if host:
-            host.result()
-    tmp = lib + f".tmp{os.getpid()}"
-    cmd = [NVCC, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{res.stderr[-4000:]}")
-    os.replace(tmp, lib)
+    if force or _stale(lib, deps):
+        os.makedirs(build_dir, exist_ok=True)
+        srcs = sources()
+        with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+            objs = list(ex.map(lambda s: _compile(s, extra, build_dir), srcs))
+        tmp = lib + f".tmp{os.getpid()}"
+        cmd = [NVCC, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"link failed:\n{res.stderr[-4000:]}")
+        os.replace(tmp, lib)
+    # the library stands by itself: the front ends come behind it, and only where torch is
+    if _front_stale() or (force and _front_wants() is not None):
+        _compile_front()
     return lib
 
 
