@@ -30,11 +30,19 @@ def load():
 
 def on_stream(fn, stream, like, *args):
     """fn(*args) with `stream` current, so what it allocates belongs to the stream that uses it.  stream:
-    a torch stream, or a raw handle of `like`'s device."""
+    a torch stream, or a raw handle of `like`'s device.  The tensors given are recorded as in use on it, so
+    that torch does not hand their memory out again before the call has run."""
     import torch
+    if not isinstance(like, torch.Tensor) or not like.is_cuda:
+        return fn(*args)                                 # which refuses it
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_abi._stream(stream) or 0, device=like.device)
     if stream.device != like.device:
         raise ValueError(f"stream must be on {like.device}")
     with torch.cuda.stream(stream):
-        return fn(*args)
+        result = fn(*args)
+    if stream.cuda_stream != torch.cuda.current_stream(like.device).cuda_stream:
+        for t in args:
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
+    return result

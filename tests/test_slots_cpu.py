@@ -325,3 +325,16 @@ def test_packed_scan_hook_refusals(ssm):
     for budget in (-1, 10 ** 7 + 1):
         assert lib.ssm_selective_scan_packed_test_hooks(0, budget) == ssm.SSM_ERR_INVALID_ARG
     assert ssm.ssm_selective_scan_packed_test_hooks(False) == ssm.SSM_OK
+
+
+def test_front_end_refusals_with_a_stream(ssm):
+    """The same refusals where a stream is given."""
+    import torch
+    z, i32 = torch.zeros, torch.int32
+    for bad, error, word in ((z(2, 4), ValueError, "CUDA"), (None, ValueError, "x must be a tensor"), ([1.0], TypeError, "tensor")):
+        with pytest.raises(error, match=word):
+            ssm.causal_conv1d_update(bad, z(4, 4), z(2, 4, 3), stream=0)
+    with pytest.raises(ValueError, match="CUDA"):
+        ssm.causal_conv1d_fwd(z(1, 4, 8), z(4, 4), stream=0)
+    with pytest.raises(ValueError, match="CUDA"):
+        ssm.state_slots_copy(z(2, 4), z(1, dtype=i32), z(1, dtype=i32), stream=0)

@@ -1027,3 +1027,48 @@ def test_scan_packed_wait_that_runs_out_is_reported(ssm, total, heads):
     again = torch.zeros(2, dim, N, device="cuda")
     assert torch.equal(_call(ssm, p, cu, again, None, max_seqlen=total - short), want) and torch.equal(again, want_s)
     assert ssm.ssm_selective_scan_packed_device_status() == ssm.SSM_OK
+
+
+def test_inputs_freed_behind_a_call_on_another_stream(ssm):
+    """The memory of a call's inputs is not handed out again while a stream that was given has yet to run it."""
+    gen = torch.Generator().manual_seed(36)
+    n, dim = 1024, 2056                                  # sizes of their own, so that a freed block would fit again
+    w, pool, x = rnd(gen, dim, 4), torch.zeros(n, dim, 3, device="cuda"), rnd(gen, n, dim)
+    want = ssm.causal_conv1d_update(x.clone(), w, pool.clone())
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        src = x.clone()
+        at = src.data_ptr()
+        kept = pool.clone()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)                # about 10 ms
+        got = ssm.causal_conv1d_update(src, w, kept, stream=stream)
+        del src
+        again = torch.full((n, dim), 7.0, device="cuda")
+        assert again.data_ptr() != at
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        del again, got, kept
+
+
+def test_given_stream_in_a_graph(ssm):
+    """A call on a given stream that joins a capture."""
+    gen = torch.Generator().manual_seed(37)
+    w, pool, x = rnd(gen, 40, 4), torch.zeros(6, 40, 3, device="cuda"), rnd(gen, 6, 40)
+    out = torch.zeros_like(x)
+    want = ssm.causal_conv1d_update(x, w, pool.clone())
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        ssm.causal_conv1d_update(x, w, pool, out=out, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    assert not out.any()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    del x, graph                                         # what the capture recorded is let go
+    torch.cuda.synchronize()
+    assert torch.full((6, 40), 2.0, device="cuda").sum() == 480
