@@ -153,3 +153,28 @@ def test_conv_bwd_last_input_not_finite(case, bad):
     sp.check(f64(got["dw"])[:, :-1], ref[1][:, :-1], err[1][:, :-1], "f32", "dw")
     assert not np.isfinite(f64(got["dw"])[:, -1]).any()
     sp.check(f64(got["dbias"]), ref[2], err[2], "f32", "dbias")
+
+
+@pytest.mark.parametrize("case", [(1, 4, 20000, 4, "f32", True, True, False), (40, 16, 130, 4, "bf16", True, True, False),
+                                  (1, 3, 40001, 3, "bf16", False, True, True)], ids=str)
+def test_conv_bwd_split_sums_in_a_graph(case):
+    """A channel split over CTAs: the second kernel and the caller's workspace in a graph, which holds nothing
+    from one replay to the next."""
+    import selective_state_space_30_b200 as ssm
+    x, w, b, g, silu, dtype = _inputs(case)
+    nbytes = ssm.ssm_causal_conv1d_bwd_workspace_size(*x.shape, w.shape[1], ssm.SSM_BF16 if dtype == "bf16" else ssm.SSM_F32)
+    assert nbytes > 0, "this case is here for the second kernel"
+    ws = torch.empty(nbytes // 4, device="cuda")
+    ssm.causal_conv1d_bwd(x, w, g, bias=b, silu=silu, workspace=ws.view(torch.uint8))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = ssm.causal_conv1d_bwd(x, w, g, bias=b, silu=silu, workspace=ws.view(torch.uint8))
+    for seed in (9, 10):
+        x.copy_(rnd(torch.Generator().manual_seed(seed), *x.shape, dtype=dtype))
+        ws.fill_(float("nan"))
+        graph.replay()
+        ref, err = sp.conv_bwd(f64(x), f64(w), f64(b), f64(g), silu)
+        for k, r, e, t in zip(("dx", "dw", "dbias"), ref, err, (dtype, "f32", "f32")):
+            sp.check(f64(got[k]), r, e, t, k)
+        want = ssm.causal_conv1d_bwd(x, w, g, bias=b, silu=silu)
+        assert all(torch.equal(got[k], want[k]) for k in got)

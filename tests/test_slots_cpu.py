@@ -338,3 +338,14 @@ def test_front_end_refusals_with_a_stream(ssm):
         ssm.causal_conv1d_fwd(z(1, 4, 8), z(4, 4), stream=0)
     with pytest.raises(ValueError, match="CUDA"):
         ssm.state_slots_copy(z(2, 4), z(1, dtype=i32), z(1, dtype=i32), stream=0)
+
+
+def test_conv_bwd_cases_take_both_paths(ssm):
+    """Which of the shapes that the GPU tests run split a channel's sums over CTAs (a workspace says so), so that a
+    change of the rule does not leave one of the paths untested."""
+    def split(batch, dim, seqlen, width, io):
+        return ssm.ssm_causal_conv1d_bwd_workspace_size(batch, dim, seqlen, width, io) > 0
+
+    assert split(1, 4, 20000, 4, ssm.SSM_F32) and split(40, 16, 130, 4, ssm.SSM_BF16) and split(1, 3, 40001, 3, ssm.SSM_BF16)
+    assert not split(2, 24, 67, 4, ssm.SSM_BF16) and not split(1, 3, 5000, 4, ssm.SSM_F32)
+    assert not split(1, 2, 8195, 4, ssm.SSM_BF16) and not split(2, 768, 1021, 3, ssm.SSM_F32)
