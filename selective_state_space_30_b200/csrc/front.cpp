@@ -186,6 +186,7 @@ void check(int rc, const char* where) {
     }
     throw Refused();
 }
+// `zeroed`: the call may leave some of it unwritten (padding, which only slots can name in a call of single tokens).
 Tensor out_or(const Arg& out, const Tensor& like, bool zeroed) {
     return out ? *out : zeroed ? at::zeros_like(like) : at::empty_like(like);
 }
@@ -273,7 +274,7 @@ PyObject* conv_update(PyObject* const* v) {
     need_apart(out, {&x}, true);
     need_apart(out, {&w, &bias, &states, &slots});
     const Launch on(dev);
-    Tensor o = out_or(out, *x, true);
+    Tensor o = out_or(out, *x, (bool)slots);
     check(entry.conv_update(batch, dim, (int32_t)width, io, x.ptr(), f32(w), f32(bias), silu, i32(slots), states.ptr(),
                             states->size(0), stride, o.data_ptr(), on.stream),
           "ssm_causal_conv1d_update");
@@ -349,7 +350,7 @@ PyObject* state_update(PyObject* const* v) {
     need_apart(out, {&delta, &B, &C, &A, &D, &bias, &states, &slots});
     const ssm_dims_t d = {batch, dim, 1, N, heads, groups, io, 0};
     const Launch on(dev);
-    Tensor o = out_or(out, *u, true);
+    Tensor o = out_or(out, *u, (bool)slots);
     check(entry.state_update(&d, static_cast<float*>(states.ptr()), i32(slots), states->size(0), stride, u.ptr(), delta.ptr(),
                              f32(A), B.ptr(), C.ptr(), f32(D), z.ptr(), f32(bias), softplus, o.data_ptr(), on.stream),
           "ssm_selective_state_update_slots");

@@ -5,11 +5,11 @@ Layouts, slots and lengths are those of include/ssm_scan.h ("packed prompts and 
 a negative slot marks a padding row.  Pools are (n_slots, ...) tensors whose slots are contiguous
 and may lie apart (a layer's view of a pool that holds several layers).  The calls update the
 pools in place, run on `stream` (default: the device's current one) and can be captured into a
-CUDA graph.  `out` is allocated with torch unless given, zeroed so that padding reads as zero; a
-workspace is allocated unless given.  An `out` that is given shares no memory with what the call reads
-(the single-token calls may write over x, u or z: out being that very tensor).  Tensors of another type, shape, device or layout are refused
-with ValueError, what the library refuses with SsmError.  The checks and calls are compiled
-(csrc/front.cpp).
+CUDA graph.  `out` is allocated with torch unless given, zeroed where a call may leave some of it as
+it was, so that padding reads as zero; a workspace is allocated unless given.  An `out` that is given
+shares no memory with what the call reads (the single-token calls may write over x, u or z: out being
+that very tensor).  Tensors of another type, shape, device or layout are refused with ValueError, what
+the library refuses with SsmError.  The checks and calls are compiled (csrc/front.cpp).
 """
 from __future__ import annotations
 

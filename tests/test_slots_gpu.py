@@ -1052,6 +1052,41 @@ def test_inputs_freed_behind_a_call_on_another_stream(ssm):
         del again, got, kept
 
 
+def test_outputs_of_the_calls_own_are_written_whole(ssm):
+    """Single tokens without slots have no padding: every row of an output that the call allocates is written, rows
+    past the pool with NaN.  With slots the padding rows read as zero."""
+    gen = torch.Generator().manual_seed(38)
+    batch, dim, N = 70, 328, 16
+    w, x = rnd(gen, dim, 4), rnd(gen, batch, dim)
+    q = _scan_inputs(gen, batch, dim, dim, 1, N, "f32", prompts=False)
+
+    def stale():
+        held = torch.full((batch, dim), 3.0, device="cuda")
+        del held                                          # the block that the call's output gets
+
+    for n_slots in (batch, batch - 5):
+        pool, states = rnd(gen, n_slots, dim, 3), rnd(gen, n_slots, dim, N)
+        for slots in (None, [i if i % 3 else -1 for i in range(batch)]):
+            idx = None if slots is None else i32(slots)
+            pad = [] if slots is None else [i for i, s in enumerate(slots) if s < 0]
+            rows = [i for i in range(batch) if i not in pad]
+            def conv(st, out):
+                return ssm.causal_conv1d_update(x, w, st, slots=idx, out=out)
+
+            def scan(st, out):
+                return ssm.selective_state_update_slots(st, q["u"], q["delta"], q["A"], q["B"], q["C"], slots=idx, D=q["D"],
+                                                        z=q["z"], delta_bias=q["delta_bias"], out=out)
+
+            for call, start in ((conv, pool), (scan, states)):
+                want = call(start.clone(), torch.full((batch, dim), 5.0, device="cuda"))
+                st = start.clone()
+                stale()
+                got = call(st, None)
+                assert torch.equal(torch.nan_to_num(got[rows], 9.0), torch.nan_to_num(want[rows], 9.0))
+                assert torch.isnan(got).any() == (n_slots < batch)
+                assert not pad or not got[pad].any()
+
+
 def test_given_stream_in_a_graph(ssm):
     """A call on a given stream that joins a capture."""
     gen = torch.Generator().manual_seed(37)
