@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) conv1d_bwd_kernel(const ConvBw
             tiles[r] = (L + m[r] + 32 * V - 1) / (32 * V);
         }
         const int64_t all = tiles[0] > tiles[1] ? tiles[0] : tiles[1];
+        const int64_t first_end = (tiles[0] < tiles[1] ? tiles[0] : tiles[1]) - 1;
         const int64_t tile0 = seg * p.tiles_per_seg, tile1 = tile0 + p.tiles_per_seg < all ? tile0 + p.tiles_per_seg : all;
         auto load = [&](int r, int64_t tile) {
             if constexpr (ALIGNED) {
@@ -235,15 +236,17 @@ __global__ void __launch_bounds__(32 * kWarps, 2) conv1d_bwd_kernel(const ConvBw
                 next[0] = load(0, tile - 1);
                 next[1] = load(1, tile - 1);
             }
-            // tokens of the lane's pieces up to the rows' ends.  Behind an end dv is zero, and the inputs that
-            // its sums would meet there, the last ones of the row, read as zero too: an infinity or a
-            // NaN among them stays out of the taps that it does not belong to
-            int64_t left[2];
-            bool tail = false;
+            // Behind a row's end dv is zero, and the inputs that its sums would meet there, the last ones of the
+            // row, read as zero too: an infinity or a NaN among them stays out of the taps that it does not
+            // belong to.  (With silu it is in dv of the last token, and so in every tap.)
+            const bool tail = !SILU && tile >= first_end;
+            int left[2] = {V, V};                         // the lane's tokens ahead of the end
+            if (tail) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                left[r] = L - ((tile * 32 + lane) * V - m[r]);
-                tail = tail || L < (tile + 1) * 32 * V - m[r];
+                for (int r = 0; r < 2; ++r) {
+                    const int64_t n = L - ((tile * 32 + lane) * V - m[r]);
+                    left[r] = n < V ? (int)(n > 0 ? n : 0) : V;
+                }
             }
             // tokens t - 4 .. t + V - 1 of x; t .. t + V + H - 1 of dv
             float2 xv[4 + V], dv[V + H];
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) conv1d_bwd_kernel(const ConvBw
                 for (int i = 0; i < PW; ++i) {
                     bw[i] = __shfl_up_sync(0xffffffffu, xw[4 - PW + i], 1);
                     if (lane == 0) bw[i] = cur[r].before[i];
-                    if (ALIGNED && left[r] <= 0) bw[i] = 0u;
+                    if (!SILU && ALIGNED && left[r] == 0) bw[i] = 0u;
                 }
                 float xb[4], xc[V], gc[V];
                 unpack<T, 4>(bw, xb);

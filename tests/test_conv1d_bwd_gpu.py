@@ -178,3 +178,24 @@ def test_conv_bwd_split_sums_in_a_graph(case):
             sp.check(f64(got[k]), r, e, t, k)
         want = ssm.causal_conv1d_bwd(x, w, g, bias=b, silu=silu)
         assert all(torch.equal(got[k], want[k]) for k in got)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("case", [(2, 40, 64, 4, "bf16", True, True, False), (2, 24, 67, 3, "bf16", True, True, True),
+                                  (1, 4, 5001, 4, "f32", True, False, False)], ids=str)
+def test_conv_bwd_last_input_not_finite_with_silu(case, bad):
+    """With silu the last token's own derivative is not finite then, and with it every tap; other rows stay."""
+    import selective_state_space_30_b200 as ssm
+    x, w, b, g, silu, dtype = _inputs(case)
+    x[-1, 1, -1] = bad
+    with np.errstate(invalid="ignore", over="ignore"):
+        ref, err = sp.conv_bwd(f64(x), f64(w), f64(b) if b is not None else np.zeros(w.shape[0]), f64(g), silu)
+    got = ssm.causal_conv1d_bwd(x, w, g, bias=b, silu=silu)
+    rows = [r for r in range(x.shape[1]) if r != 1]
+    assert not np.isfinite(ref[1][1]).any() and not np.isfinite(f64(got["dw"])[1]).any() and not torch.isfinite(got["dbias"][1])
+    sp.check(f64(got["dw"])[rows], ref[1][rows], err[1][rows], "f32", "dw")
+    sp.check(f64(got["dbias"])[rows], ref[2][rows], err[2][rows], "f32", "dbias")
+    sp.check(f64(got["dx"])[:, rows], ref[0][:, rows], err[0][:, rows], dtype, "dx")
+    # the row's own dx up to the tokens that reach the last one
+    n = x.shape[2] - w.shape[1]
+    sp.check(f64(got["dx"])[:, 1, :n], ref[0][:, 1, :n], err[0][:, 1, :n], dtype, "dx")
