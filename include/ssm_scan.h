@@ -469,7 +469,8 @@ int ssm_causal_conv1d_update(int64_t batch, int64_t dim, int32_t width, int32_t 
  * max_seqlen: the longest sequence if the caller knows it, else 0.  It is a hint: with few long
  * sequences the call cuts them into chunks that run at the same time and join their states
  * (two kernels instead of one), and the hint saves that where every sequence is short.  The
- * result is right for any value; the same arguments give the same bits.  `workspace` (device,
+ * result is right for any value; the same arguments give the same bits (the call's sizes decide on
+ * chunks and kernel, so a prompt in other company may differ from itself in the last bits).  `workspace` (device,
  * 16-byte aligned, caller-owned) has at least ssm_selective_scan_packed_workspace_size bytes
  * for the same dims and max_seqlen (0 bytes: it may be NULL); it is scratch after the call, and
  * one workspace must not serve two calls at once, nor two graphs that may run at once.
@@ -553,9 +554,10 @@ int ssm_state_slots_copy(void* pool, int64_t n_layers, int64_t n_slots, int64_t 
  *
  * dx is (batch, dim, seqlen) in io_dtype; dw (dim, width) and dbias (dim, nullable: not computed)
  * are fp32, summed in a fixed order.  bias is the forward's (NULL: zero).  `workspace` (device,
- * 4-byte aligned, caller-owned) has at least ssm_causal_conv1d_bwd_workspace_size bytes (0 bytes,
- * with one kernel instead of two, but for few channels with long rows: it may then be NULL); one workspace must not serve two calls at once.  Kernels on `stream`; the call allocates
- * nothing.  dx must not overlap x or dout.  width is 1 to 4, else SSM_ERR_UNSUPPORTED;
+ * 4-byte aligned, caller-owned) has at least ssm_causal_conv1d_bwd_workspace_size bytes, and must
+ * not serve two calls at once.  That is 0 bytes, and workspace may be NULL, for all shapes but few
+ * channels with long rows, whose sums a second kernel joins.  Kernels on `stream`; the call
+ * allocates nothing.  dx must not overlap x or dout.  width is 1 to 4, else SSM_ERR_UNSUPPORTED;
  * SSM_ERR_INVALID_ARG for a bad shape or dtype, a pointer off its element's alignment, a
  * workspace that is too small, or a NULL w, dw, x, dout or dx.
  */

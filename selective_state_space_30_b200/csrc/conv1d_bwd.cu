@@ -12,10 +12,10 @@
 // order; where a channel is split over CTAs a second kernel adds their partials, in order too, so
 // the gradients repeat bit for bit.
 //
-// Measured on one B200: 8 x 1536 x 2048 bf16, width 4, 43 us (3.5 TB/s; 23 us of HBM time), issue
-// 59 % busy with 14 of 64 warps an SM (128 registers hold two rows and the loads ahead); three CTAs an
-// SM with 84 registers 61 us.  2 x 768 x 1021 fp32 6.9 us in a graph with four warps a pair of channels,
-// 8.7 with eight, 9.6 with partials and a second kernel.
+// Measured on one B200: 8 x 1536 x 2048 bf16, width 4, 42 us (3.6 TB/s; 23 us of HBM time), issue
+// 55 % busy with 14 of 64 warps an SM (128 registers hold two rows and the loads ahead); three CTAs an
+// SM with 84 registers 61 us.  2 x 768 x 1021 fp32, width 3, 6.5 us in a graph with four warps a pair of
+// channels (beside one another 6.9, 8.7 with eight, 9.6 with partials and a second kernel).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

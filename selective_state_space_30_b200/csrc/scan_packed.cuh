@@ -23,12 +23,13 @@
 // aligned are copied as the aligned pieces that hold them and read at their offset.  The warps of a
 // CTA meet twice per block, around the conversion of B and C.
 //
-// Measured on one B200, bf16, dstate 16: 16384 tokens in 24 ragged prompts x 4096 channels 492 us
-// in the mean of three draws (the longest of them 3305 to 3913 tokens, whose chain of blocks is most
-// of it; 445 us where the tokens lie more evenly), one prompt of 8191 tokens x 1536 channels 199 us
-// in 24 chunks, of 8192 (rows on the 16-byte grid) 165.  MUFU two thirds busy while SMs have work.
-// Uncut calls: three CTAs an SM with more registers each 510 us and per-lane rows of y 492, against 538
-// of four CTAs that sum y by shuffles, as cut calls do (three CTAs there 213 against 200).  Against it:
+// Measured on one B200, bf16, dstate 16: 16384 tokens in 24 ragged prompts x 4096 channels 464 us
+// in the mean of three draws (413 to 522 us for longest prompts of 1845 to 3954 tokens, whose chain of
+// blocks is most of it), one prompt of 8191 tokens x 1536 channels 198 us in 24 chunks, of 8192 (rows on
+// the 16-byte grid) 165.  MUFU two thirds busy while SMs have work.
+// Uncut calls, on other draws: three CTAs an SM with more registers each 510 us and per-lane rows of y 492,
+// against 538 of four CTAs that sum y by shuffles, as cut calls do (three CTAs there 213 against 200).
+// Against it, from 492 and 200:
 // eight states of two channels per lane (half the warps, longer chains) 721 and 260 us; blocks of 32
 // bytes 636 and 226; eight warps a CTA 611 and 221; a quarter of the exponentials as polynomials on
 // the fp32 pipe 4 to 9 % more (the issue slots they need are as scarce); outputs stored without their
