@@ -477,7 +477,8 @@ int ssm_causal_conv1d_update(int64_t batch, int64_t dim, int32_t width, int32_t 
  *
  * bf16 I/O with nheads < dim, dim / nheads == 64 and dstate 128 runs on the tensor cores once the
  * sequences are 32 tokens or more in the mean, in blocks of 128 tokens: there an infinity in u makes
- * NaN, not infinities, of its channel's state and outputs from its token on, and a wait for the tensor
+ * NaN, not infinities, of its channel's state and outputs from its token on, steps that let the state
+ * grow (without softplus) overflow once they pass 2^127 within a block, and a wait for the tensor
  * cores or a copy that runs out (half a second) leaves NaN in the rest of that head's outputs and in its
  * state, and SSM_ERR_TIMEOUT for ssm_selective_scan_packed_device_status.
  *

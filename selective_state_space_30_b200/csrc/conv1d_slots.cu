@@ -11,10 +11,10 @@
 // Measured on one B200, bf16, width 4: 32768 tokens in 32 prompts x 4096 channels 120 us (4.5 TB/s;
 // a copy through the same loop, width 1 without silu, 95 us), of which the prompts' first tokens are
 // 8 us; fp32, 2048 channels 121 us; 1013 tokens in 7 prompts x 1536 channels 5.8 us; one token of 4 rows x
-// 1536 channels 2.7 us, of 248 rows x 4096 9.2 us (fp32 8.1), all in a graph.  Between the first of them and the HBM time (82 us)
-// stand silu's two MUFU operations per output (60 us of that pipe) and the issue of the rest (110
-// instructions per 8 outputs).  With three CTAs an SM (80 registers) it took 142 us against 130 of four; inputs
-// asked for ahead of the mask changed nothing there and made the small call 0.6 us longer.
+// 1536 channels 2.7 us, of 248 rows x 4096 9.2 us (fp32 8.1), all in a graph.  Between the first of them
+// and the HBM time (82 us) stand silu's two MUFU operations per output (60 us of that pipe) and the issue of
+// the rest (110 instructions per 8 outputs).  With three CTAs an SM (80 registers) it took 142 us against
+// 130 of four; inputs asked for ahead of the mask changed nothing there and made the small call 0.6 us longer.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -50,7 +50,8 @@ bool on_tensor_cores(const ssm_dims_t& d) { return ssm::packed::ssd_packed_cover
 // and so would still run when everything else is done: one prompt of 8191 tokens x 1536 channels
 // takes 203 us cut at 352 tokens, 231 at 448, 292 at 672; 24 ragged prompts (16384 tokens x 4096
 // channels, the longest under two shares) took 492 us uncut and 666 with every prompt cut at 1184 (what
-// cutting its longest prompts alone takes has not been tried).  On the tensor cores a middle chunk's first pass costs less than half of its second, so three shares do: 4 prompts of
+// cutting its longest prompts alone takes has not been tried).  On the tensor cores a middle chunk's first
+// pass costs less than half of its second, so three shares do: 4 prompts of
 // 4096 tokens in all, 32 heads, the longest of 3000 (3.3 shares), 116 us uncut and 91 cut at 896; 6,
 // the longest of 2241 (2.5 shares), 91 and 100, of 1508 (1.7) 65 and 99.
 int64_t choose_chunk(const ssm_dims_t& d, int64_t max_seqlen) {

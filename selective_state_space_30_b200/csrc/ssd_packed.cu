@@ -13,34 +13,36 @@
 // Steps outside the sequence have dt = 0 and their rows of B, C and X are zeroed in shared memory,
 // so that no value there, NaN included, reaches a product.  A NaN or an infinity of the sequence's own u
 // would reach the outputs of earlier steps through M's zeros: where the state turns out not to be finite,
-// X is cleared of them and Y made again (no cost elsewhere: a sum of 16 values in four of the warps).
+// X is cleared of them and Y made again (elsewhere that costs a sum of 16 values in four of the warps).
 //
 // Precision.  B, C and X are bf16 and enter exactly.  X' is split into three bf16 terms (24 bits); the
-// tensor core cuts its running sum of them, by 2^-22 of the magnitudes a step at the most.  Measured against
-// 64 bits after 400 and 1000 steps, the state is off by 1.5e-7 to 1.9e-7 of its size (rms), the recurrence's in fp32 by
-// 1.8e-7.  M and H are split into two terms (16 bits, 2^-17 of each product),
+// tensor core cuts its running sum of them, by 2^-22 of the magnitudes a step at the most.  Measured
+// against 64 bits after 400 and 1000 steps, the state is off by 1.5e-7 to 1.9e-7 of its size (rms), the
+// recurrence's in fp32 by 1.8e-7.  M and H are split into two terms (16 bits, 2^-17 of each product),
 // far inside the rounding of the bf16 outputs.  Sums of a that are subtracted from one another
 // lose their small differences, so every s(i, j) is added up from terms of its own: over stretches of
 // 32 steps and groups of four, what is left of j's, the whole ones between, and the steps of i's; a
-// step's own weight is its dt.
+// step's own weight is its dt.  (The factors of a weight may leave fp32's range where it does not: with
+// steps of either sign, a growth past 2^127 within a block overflows whatever decayed before it.)
 //
 // Order of a block.  The products run under the threads' work: G, then S and C H while M is made from
 // G in tensor memory (M is Y's left operand there), Y while the state takes S and X' of the next
 // block is made.  Three barriers a block.
 //
 // Bound: the threads' phases, chains of few instructions over 16 warps, one CTA per SM: a block takes
-// 4.1 us, off the 16-byte grid 10.  (When it took 4.8, about 0.4 went into waiting for G, 1.2 into M, 1.4 into
-// the state and X', 1.3 into the outputs, half of that silu's two MUFU operations, and 0.3 into the copies'
-// orders.)  Measured on one B200: 6 ragged prompts of 4096 tokens, 32 heads 62 us in the mean of three draws
-// (the longest prompt 1468 to 1589 tokens; the scan kernel 340 to 380 for heads of 32 or of 128 channels), one prompt of 8192
-// tokens, 16 heads 83 in chunks.  Steps, for other draws of the first of these: values in f32x2 pairs, log2 dt folded into the exponent and whole
+// 4.1 us, off the 16-byte grid 10.  (When it took 4.8, about 0.4 went into waiting for G, 1.2 into M, 1.4
+// into the state and X', 1.3 into the outputs, half of that silu's two MUFU operations, and 0.3 into the
+// copies' orders.)  Measured on one B200: 6 ragged prompts of 4096 tokens, 32 heads 62 us in the mean of
+// three draws (the longest prompt 1468 to 1589 tokens; the scan kernel 340 to 380 for heads of 32 or of 128
+// channels), one prompt of 8192 tokens, 16 heads 83 in chunks.  Steps, for other draws of the first of
+// these: values in f32x2 pairs, log2 dt folded into the exponent and whole
 // words of x, z and the outputs in the epilogue 120 us; M in tensor memory instead of shared memory, so
 // that S need not have left its place, 104; the terms of X' and H side by side in one product each (a product
 // of 64 columns takes as long to read its left operand as one of 192), the products asked for by a warp that
 // M leaves idle and X' under Y 87; boxes of TMA instead of the threads' copies, and what seldom
-// runs out of line 79; weights across stretches as products 78; the rule on cutting 74; epilogue rows in different banks, maps asked for
-// early 73; weights across groups of four as products too, kernels of their own for cut and
-// uncut calls 5 % less.
+// runs out of line 79; weights across stretches as products 78; the rule on cutting 74; epilogue rows in
+// different banks, maps asked for early 73; weights across groups of four as products too, kernels of
+// their own for cut and uncut calls 5 % less.
 //
 // Tiles arrive in the 128-byte swizzle that the tensor cores read, each as soon as its place is free: X a
 // block ahead in a second buffer, B and C once G, S and C H are done, z once the outputs before it
