@@ -668,22 +668,48 @@ __device__ __forceinline__ bool find_item(const PackedParams& p, int64_t x, int6
         const int half = e > 0 ? (int)(len >> (e - 1)) & 1 : 0;
         return kBuckets - 2 - 2 * e - half;             // the longest come first
     };
-    int want = 0;
-    if constexpr (CUT) {
-        unsigned long long* total = reinterpret_cast<unsigned long long*>(sh);
-        if (tid == 0) *total = 0ull;
-        __syncthreads();
-        int64_t n = 0;
-        for (int64_t i = tid; i < p.n_seq; i += nt) {
-            const TokenRange r = token_range(p.cu, i, p.total);
-            n += r.hi > r.lo ? (r.hi - r.lo + p.chunk - 1) / p.chunk : 1;
+    // the x-th of the items, of every sequence's chunks or of one bucket's sequences; returns how many were met
+    auto search = [&](bool chunks, int want) {
+        int64_t before = 0;
+        if (tid == 0) sh[0] = -1;
+        for (int64_t i0 = 0; i0 < p.n_seq; i0 += nt) {
+            const int64_t i = i0 + tid;
+            int64_t n = 0;
+            if (i < p.n_seq) {
+                const TokenRange r = token_range(p.cu, i, p.total);
+                const int64_t len = r.hi - r.lo;
+                n = chunks ? (len > 0 ? (len + p.chunk - 1) / p.chunk : 1) : bucket(len) == want;
+            }
+            int64_t inc = n;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, inc, m);
+                if (lane >= m) inc += v;
+            }
+            __syncthreads();
+            if (lane == 31) sh[2 + warp] = inc;
+            __syncthreads();
+            int64_t base = before, all = before;
+            for (int w = 0; w < nw; ++w) {
+                if (w < warp) base += sh[2 + w];
+                all += sh[2 + w];
+            }
+            if (n > 0 && x >= base + inc - n && x < base + inc) {
+                sh[0] = i;
+                sh[1] = x - (base + inc - n);
+            }
+            before = all;
+            if (!chunks && x < all) break;
         }
-        atomicAdd(total, (unsigned long long)n);
         __syncthreads();
-        cut = *total <= (unsigned long long)p.n_chunks;
-        __syncthreads();
+        return before;
+    };
+    if constexpr (CUT) {
+        cut = search(true, 0) <= p.n_chunks;
+        if (!cut) __syncthreads();
     }
     if (!cut) {
+        int want = 0;
         for (int i = tid; i < kBuckets; i += nt) count[i] = 0u;
         __syncthreads();
         for (int64_t i = tid; i < p.n_seq; i += nt) {
@@ -692,39 +718,8 @@ __device__ __forceinline__ bool find_item(const PackedParams& p, int64_t x, int6
         }
         __syncthreads();
         while (want < kBuckets - 1 && x >= (int64_t)count[want]) x -= count[want++];
+        search(false, want);
     }
-    int64_t before = 0;
-    if (tid == 0) sh[0] = -1;
-    for (int64_t i0 = 0; i0 < p.n_seq; i0 += nt) {
-        const int64_t i = i0 + tid;
-        int64_t n = 0;
-        if (i < p.n_seq) {
-            const TokenRange r = token_range(p.cu, i, p.total);
-            const int64_t len = r.hi - r.lo;
-            n = cut ? (len > 0 ? (len + p.chunk - 1) / p.chunk : 1) : bucket(len) == want;
-        }
-        int64_t inc = n;
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, inc, m);
-            if (lane >= m) inc += v;
-        }
-        __syncthreads();
-        if (lane == 31) sh[2 + warp] = inc;
-        __syncthreads();
-        int64_t base = before, all = before;
-        for (int w = 0; w < nw; ++w) {
-            if (w < warp) base += sh[2 + w];
-            all += sh[2 + w];
-        }
-        if (n > 0 && x >= base + inc - n && x < base + inc) {
-            sh[0] = i;
-            sh[1] = x - (base + inc - n);
-        }
-        before = all;
-        if (x < all) break;
-    }
-    __syncthreads();
     seq = sh[0];
     k = sh[1];
     return seq >= 0;
